@@ -8,6 +8,9 @@ for gfx950 (libkda.so, declared in include/kda.h) and its Python binding.
     from gated_delta_rule_101_amd import kda_chunk_bwd                             # gradients
     from gated_delta_rule_101_amd import kda_chunk_fwd_seqpar                      # sequence-parallel forward
     from gated_delta_rule_101_amd import kda_chunk_fwd_gate_seqpar                 # the same from gate logits
+    from gated_delta_rule_101_amd import kda_short_conv_fwd, kda_short_conv_step, kda_short_conv_bwd
+    from gated_delta_rule_101_amd import kda_selective_scan_fwd, kda_selective_scan_step, kda_selective_scan_bwd
+    from gated_delta_rule_101_amd import kda_layer_norm_fwd, kda_layer_norm_bwd
 """
 
 from .kda import (  # noqa: F401
@@ -19,4 +22,10 @@ from .kda import (  # noqa: F401
     kda_chunk_fwd_workspace_bytes, kda_commit_step, kda_decode_step,
     kda_decode_step_gate, kda_decode_step_gated, kda_output_gate, kda_verify_step, load_library,
     status_string,
+)
+from .block import (  # noqa: F401
+    kda_layer_norm_bwd, kda_layer_norm_bwd_workspace_bytes, kda_layer_norm_fwd, kda_selective_scan_bwd,
+    kda_selective_scan_bwd_workspace_bytes, kda_selective_scan_fwd, kda_selective_scan_fwd_workspace_bytes,
+    kda_selective_scan_step, kda_short_conv_bwd, kda_short_conv_bwd_workspace_bytes, kda_short_conv_fwd,
+    kda_short_conv_step,
 )

@@ -1,0 +1,58 @@
+// Device helpers of the short convolution, the selective scan and layer norm.
+#pragma once
+
+#include "kda_device.h"
+
+namespace kda {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+// V consecutive storage elements in one access: V = 16 / sizeof(T) takes a
+// 16-byte load, V = 1 a scalar one (rows whose length leaves them unaligned).
+template <typename T, int V> struct Pack;
+template <typename T> struct Pack<T, 1> {
+    T a;
+    __device__ __forceinline__ void load(const T *p) { a = *p; }
+    __device__ __forceinline__ void zero() { a = T(0); }
+    __device__ __forceinline__ void to_f32(float (&x)[1]) const { x[0] = kda::to_f32(a); }
+    static __device__ __forceinline__ void store(T *p, const float (&x)[1]) { *p = from_f32<T>(x[0]); }
+};
+template <> struct Pack<uint16_t, 8> : Raw8<uint16_t> {
+    static __device__ __forceinline__ void store(uint16_t *p, const float (&x)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (uint32_t)f32_to_bf16(x[2 * i]) | ((uint32_t)f32_to_bf16(x[2 * i + 1]) << 16);
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Pack<float, 4> : Raw4<float> {
+    static __device__ __forceinline__ void store(float *p, const float (&x)[4]) { store4(p, x); }
+};
+template <typename T> constexpr int WIDE = 16 / (int)sizeof(T);
+
+// log(1 + e) for e in [0, 1]: 2 artanh(r) with r = e / (2 + e) <= 1/3, whose
+// series in r^2 <= 1/9 is cut after r^13 (the rest is below 2e-8 of the sum).
+// log2(1 + e) directly would lose the small e, where softplus itself is e.
+__device__ __forceinline__ float log1p_unit(float e) {
+    const float r = e * fast_rcp(2.f + e), q = r * r;
+    float p = __builtin_fmaf(q, 1.f / 13, 1.f / 11);
+    p = __builtin_fmaf(q, p, 1.f / 9);
+    p = __builtin_fmaf(q, p, 1.f / 7);
+    p = __builtin_fmaf(q, p, 1.f / 5);
+    p = __builtin_fmaf(q, p, 1.f / 3);
+    p = __builtin_fmaf(q, p, 1.f);
+    return 2.f * r * p;
+}
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)); `sig` is its derivative, the sigmoid of v.
+__device__ __forceinline__ float softplus_f32(float v) {
+    return fmaxf(v, 0.f) + log1p_unit(fast_exp2(-fabsf(v) * LOG2E));
+}
+
+// Tokens of sequence b: lengths[b] clamped to [0, T], or T.
+__device__ __forceinline__ int seq_length(const int *lengths, int b, int T) {
+    return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+}  // namespace kda

@@ -1,0 +1,296 @@
+// Layer norm for gfx950, forward and backward, over rows of D channels:
+//   y = n w + b with n = (x - mean) r, r = 1 / sqrt(var + eps)
+//   dx = r (g - mean(g) - n mean(g n)) with g = dy w,   dw = sum dy n,  db = sum dy.
+//
+// One read and one write of each element, bound by HBM bandwidth.  A group of
+// TPR threads holds a whole row in registers (at most 16 elements a thread),
+// so the mean and then the centred sum of squares are taken without reading
+// the row again, and the variance does not cancel.  TPR grows with D: below a
+// wavefront the sums are shuffles, above it they also pass through LDS.
+// Groups walk rows with a stride, keeping their channels' weights and, in the
+// backward, their partial dw and db in registers; those go to the workspace
+// once a group and are summed by column afterwards.
+#include "kda_block.h"
+#include "kda_block_device.h"
+
+namespace kda {
+namespace {
+
+// Threads of a workgroup: whole groups, at least 256.
+template <int TPR> constexpr int BLOCK = TPR > 256 ? TPR : 256;
+
+// Sums of two values over a group.  Above a wavefront the waves' sums meet in
+// `part`, whose `slot` no later call may take before another barrier has
+// passed: callers alternate slots.
+template <int TPR>
+__device__ __forceinline__ void group_sum2(float &a, float &b, float2 (*part)[BLOCK<TPR> / 64], int slot)
+{
+    constexpr int LANES = TPR < 64 ? TPR : 64;
+#pragma unroll
+    for (int m = 1; m < LANES; m <<= 1) {
+        a += __shfl_xor(a, m, LANES);
+        b += __shfl_xor(b, m, LANES);
+    }
+    if constexpr (TPR > 64) {
+        constexpr int WAVES = TPR / 64;
+        const int wave = threadIdx.x / 64;
+        if ((threadIdx.x & 63) == 0) part[slot][wave] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            const float2 p = part[slot][wave / WAVES * WAVES + i];
+            a += p.x;
+            b += p.y;
+        }
+    }
+}
+
+// Channels of vector j of thread l: V j TPR + V l ..; live while below D.
+template <typename T, int V, int NV, int TPR>
+__global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs a)
+{
+    constexpr int GROUPS = BLOCK<TPR> / TPR;
+    __shared__ float2 part[4][BLOCK<TPR> / 64];
+    const int l = threadIdx.x % TPR, D = a.D;
+    float w[NV][V], b[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int d = V * (j * TPR + l) + c;
+            w[j][c] = a.weight && d < D ? a.weight[d] : 1.f;
+            b[j][c] = a.bias && d < D ? a.bias[d] : 0.f;
+        }
+    const float inv_d = 1.f / D;
+    int slot = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t row = r0 + threadIdx.x / TPR;
+        const bool live = row < a.rows;   // the last workgroup's idle groups repeat the last row
+        const T *x = (const T *)a.x + (live ? row : a.rows - 1) * D;
+        float v[NV][V], s = 0.f, unused = 0.f;
+        Pack<T, V> raw[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int d = V * (j * TPR + l);
+            if (d < D) raw[j].load(x + d);
+            else raw[j].zero();
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            raw[j].to_f32(v[j]);
+#pragma unroll
+            for (int c = 0; c < V; ++c) s += v[j][c];
+        }
+        group_sum2<TPR>(s, unused, part, slot);
+        const float mean = s * inv_d;
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (V * (j * TPR + l) < D)
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    v[j][c] -= mean;
+                    ss = __builtin_fmaf(v[j][c], v[j][c], ss);
+                }
+        group_sum2<TPR>(ss, unused, part, slot + 1);
+        slot ^= 2;
+        const float r = rsqrtf(__builtin_fmaf(ss, inv_d, a.eps));
+        if (live) {
+            T *y = (T *)a.y + row * D;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int d = V * (j * TPR + l);
+                if (d < D) {
+                    float o[V];
+#pragma unroll
+                    for (int c = 0; c < V; ++c) o[c] = __builtin_fmaf(v[j][c] * r, w[j][c], b[j][c]);
+                    Pack<T, V>::store(y + d, o);
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int V, int NV, int TPR>
+__global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_bwd_kernel(NormBwdArgs a)
+{
+    constexpr int GROUPS = BLOCK<TPR> / TPR;
+    __shared__ float2 part[4][BLOCK<TPR> / 64];
+    const int l = threadIdx.x % TPR, D = a.D;
+    float w[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int d = V * (j * TPR + l) + c;
+            w[j][c] = a.weight && d < D ? a.weight[d] : 1.f;
+            dw[j][c] = db[j][c] = 0.f;
+        }
+    const float inv_d = 1.f / D;
+    int slot = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t row = r0 + threadIdx.x / TPR;
+        const bool live = row < a.rows;
+        const int64_t at = (live ? row : a.rows - 1) * D;
+        Pack<T, V> xr[NV], gr[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int d = V * (j * TPR + l);
+            if (d < D) {
+                xr[j].load((const T *)a.x + at + d);
+                gr[j].load((const T *)a.dy + at + d);
+            } else {
+                xr[j].zero();
+                gr[j].zero();
+            }
+        }
+        float v[NV][V], s = 0.f, sg = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float g[V];
+            xr[j].to_f32(v[j]);
+            gr[j].to_f32(g);
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                s += v[j][c];
+                sg = __builtin_fmaf(g[c], w[j][c], sg);
+            }
+        }
+        group_sum2<TPR>(s, sg, part, slot);
+        const float mean = s * inv_d;
+        float ss = 0.f, sn = 0.f;   // sum (x - mean)^2, sum g (x - mean)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (V * (j * TPR + l) < D) {
+                float g[V];
+                gr[j].to_f32(g);
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    v[j][c] -= mean;
+                    ss = __builtin_fmaf(v[j][c], v[j][c], ss);
+                    sn = __builtin_fmaf(g[c] * w[j][c], v[j][c], sn);
+                }
+            }
+        group_sum2<TPR>(ss, sn, part, slot + 1);
+        slot ^= 2;
+        const float r = rsqrtf(__builtin_fmaf(ss, inv_d, a.eps));
+        const float c1 = sg * inv_d, c2 = sn * r * inv_d;   // mean g, mean g n
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int d = V * (j * TPR + l);
+                if (d < D) {
+                    float g[V], o[V];
+                    gr[j].to_f32(g);
+#pragma unroll
+                    for (int c = 0; c < V; ++c) {
+                        const float n = v[j][c] * r;
+                        dw[j][c] = __builtin_fmaf(g[c], n, dw[j][c]);
+                        db[j][c] += g[c];
+                        o[c] = r * (__builtin_fmaf(g[c], w[j][c], -c1) - n * c2);
+                    }
+                    Pack<T, V>::store((T *)a.dx + at + d, o);
+                }
+            }
+        }
+    }
+    if (a.ws) {
+        float *p = a.ws + ((int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR) * 2 * D;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                const int d = V * (j * TPR + l) + c;
+                if (d < D) {
+                    p[d] = dw[j][c];
+                    p[D + d] = db[j][c];
+                }
+            }
+    }
+}
+
+int threads_per_row(int D) { return D <= 256 ? 16 : D <= 1024 ? 64 : D <= 4096 ? 256 : 1024; }
+int groups_per_block(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
+
+// Workgroups: one round of rows if there are few, else a number that walks
+// the rows in a loop and keeps weights and partial sums in registers.
+int64_t fwd_blocks(int64_t rows, int tpr)
+{
+    const int64_t need = (rows + groups_per_block(tpr) - 1) / groups_per_block(tpr);
+    const int64_t most = tpr == 1024 ? 512 : 2048;
+    return need < most ? need : most;
+}
+int64_t bwd_blocks(int64_t rows, int tpr)
+{
+    const int64_t need = (rows + groups_per_block(tpr) - 1) / groups_per_block(tpr);
+    const int64_t most = tpr == 1024 ? 256 : 512;
+    return need < most ? need : most;
+}
+
+// f(integral constants V, NV, TPR): 16 / sizeof(T) elements an access where
+// D allows it; 8 or 16 elements a thread.
+template <int N> struct Int { static constexpr int value = N; };
+template <typename T, int V, typename F> hipError_t by_size(int D, int tpr, F f)
+{
+    const bool half = D <= 8 * tpr;
+    if (tpr == 16) return half ? f(Int<8 / V>{}, Int<16>{}) : f(Int<16 / V>{}, Int<16>{});
+    if (tpr == 64) return half ? f(Int<8 / V>{}, Int<64>{}) : f(Int<16 / V>{}, Int<64>{});
+    if (tpr == 256) return half ? f(Int<8 / V>{}, Int<256>{}) : f(Int<16 / V>{}, Int<256>{});
+    return half ? f(Int<8 / V>{}, Int<1024>{}) : f(Int<16 / V>{}, Int<1024>{});
+}
+
+template <typename T, int V> hipError_t fwd_v(const NormArgs &a, hipStream_t s)
+{
+    const int tpr = threads_per_row(a.D);
+    return by_size<T, V>(a.D, tpr, [&](auto nv, auto t) {
+        constexpr int NV = decltype(nv)::value, TPR = decltype(t)::value;
+        kda_layer_norm_fwd_kernel<T, V, NV, TPR><<<(unsigned)fwd_blocks(a.rows, TPR), BLOCK<TPR>, 0, s>>>(a);
+        return hipGetLastError();
+    });
+}
+
+template <typename T, int V> hipError_t bwd_v(const NormBwdArgs &a, hipStream_t s)
+{
+    const int tpr = threads_per_row(a.D);
+    return by_size<T, V>(a.D, tpr, [&](auto nv, auto t) {
+        constexpr int NV = decltype(nv)::value, TPR = decltype(t)::value;
+        kda_layer_norm_bwd_kernel<T, V, NV, TPR><<<(unsigned)bwd_blocks(a.rows, TPR), BLOCK<TPR>, 0, s>>>(a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+int64_t norm_bwd_workspace_floats(int64_t rows, int D)
+{
+    const int tpr = threads_per_row(D);
+    return bwd_blocks(rows, tpr) * groups_per_block(tpr) * 2 * D;
+}
+
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s)
+{
+    (void)hipGetLastError();
+    if (a.bf16) return a.D % 8 == 0 ? fwd_v<uint16_t, 8>(a, s) : fwd_v<uint16_t, 1>(a, s);
+    return a.D % 4 == 0 ? fwd_v<float, 4>(a, s) : fwd_v<float, 1>(a, s);
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs &args, hipStream_t s)
+{
+    (void)hipGetLastError();
+    NormBwdArgs a = args;
+    const bool sums = a.dweight || a.dbias;
+    if (!sums) a.ws = nullptr;
+    if (a.rows > 0) {
+        const hipError_t e = a.bf16 ? (a.D % 8 == 0 ? bwd_v<uint16_t, 8>(a, s) : bwd_v<uint16_t, 1>(a, s))
+                                    : (a.D % 4 == 0 ? bwd_v<float, 4>(a, s) : bwd_v<float, 1>(a, s));
+        if (e != hipSuccess || !sums) return e;
+    }
+    const int tpr = threads_per_row(a.D);
+    const int64_t n = a.rows > 0 ? bwd_blocks(a.rows, tpr) * groups_per_block(tpr) : 0;
+    const ColumnSum jobs[] = {{a.ws, a.dweight, n, a.D, 2 * (int64_t)a.D, false},
+                              {n ? a.ws + a.D : nullptr, a.dbias, n, a.D, 2 * (int64_t)a.D, false}};
+    return launch_column_sums(jobs, 2, s);
+}
+
+}  // namespace kda

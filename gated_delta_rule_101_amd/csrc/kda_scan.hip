@@ -1,0 +1,347 @@
+// Selective state space scan for gfx950, forward over a sequence and one token.
+//
+// Per channel d with N states (padded to NP = 16 NB):
+//   s = softplus(dt + bias),  h[n] <- exp(s A[n]) h[n] + s x B[n],
+//   y = (sum_n C[n] h[n] + D x) silu(z)
+//
+// A lane owns a channel and keeps its states and rates in registers, a
+// wavefront 64 neighbouring channels, so every token's row of x, dt, z and y
+// is read and written in whole 128-byte (bf16) lines, the sum over n stays in
+// the lane, and the token's B and C rows are the same for all lanes: they
+// come through the scalar cache and enter the vector instructions as scalar
+// operands.  One token costs a lane 6 issue slots per state (multiply, exp2
+// at half rate, two products, two sums): the vector units bound it, not HBM.
+//
+// The recurrence is a chain over tokens, and B D / 64 chains do not fill 1024
+// SIMDs.  With a workspace the tokens are cut into segments: a first pass
+// runs all but the last from a zero state (the first from h0) and stores end
+// states and sums of s, a second pass forms each segment's true starting state
+// from those (the decay of a whole segment is exp(A sum s)) and runs it again
+// with the outputs.
+#include "kda_block.h"
+#include "kda_block_device.h"
+
+namespace kda {
+namespace {
+
+constexpr int UNROLL = 8;   // tokens whose inputs are loaded together, one batch ahead
+
+// The NP values of a token's B or C row, the same for the whole wavefront.
+// FULL rows (N = NP) are read as 32-bit words through the scalar cache; other
+// N element by element, the padding states' values zero.
+template <typename T, int NP, bool FULL>
+__device__ __forceinline__ void load_row_uniform(float (&o)[NP], const T *p, int N)
+{
+    if constexpr (FULL && sizeof(T) == 2) {
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) {
+            const uint32_t w = q[i];
+            o[2 * i] = __uint_as_float(w << 16);
+            o[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+    } else if constexpr (FULL) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) o[i] = p[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) o[i] = i < N ? to_f32(p[i]) : 0.f;
+    }
+}
+
+// Workspace of the segmented forward: slot 0 is a copy of h0 (h_final may be
+// h0 itself, and other wavefronts write it while segment 0 still starts), slot
+// s the state at the end of segment s - 1 and sum[s] that segment's sum of
+// time steps.  States lie as [NP][D]: lanes are neighbouring channels.
+struct Segments {
+    float *slots, *sums;
+    int count, tokens;   // segments, tokens each
+};
+
+template <typename T, int NB, bool FULL, bool STATES_ONLY>
+__global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__restrict__ Bm, const T *__restrict__ Cm, Segments sg, int tiles)
+{
+    constexpr int NP = 16 * NB;
+    unsigned id = blockIdx.x;
+    const int tile = id % tiles;
+    id /= tiles;
+    const int g = id % a.G;
+    id /= a.G;
+    const int runs = STATES_ONLY ? sg.count - 1 : sg.count;
+    const int seg = id % runs, b = id / runs;
+    const int D = a.D, N = a.N, Dg = D / a.G;
+    const int c = tile * 64 + threadIdx.x;
+    const bool ok = c < Dg;
+    const int d = g * Dg + (ok ? c : Dg - 1);   // idle lanes repeat the last channel
+
+    const int len = seq_length(a.lengths, b, a.T);
+    const int t0 = seg * sg.tokens, t1 = min(t0 + sg.tokens, a.T), te = min(t1, len);
+
+    float A2[NP], h[NP];   // rates in base 2
+#pragma unroll
+    for (int n = 0; n < NP; ++n) A2[n] = n < N ? a.A[(int64_t)d * N + n] * LOG2E : 0.f;
+    float *slots = sg.slots + (int64_t)b * sg.count * NP * D + d;
+    float *sums = sg.sums + (int64_t)b * sg.count * D + d;
+    const int64_t at_state = ((int64_t)b * D + d) * N;
+    if (seg == 0 || sg.count == 1) {
+        if (STATES_ONLY || sg.count == 1) {
+#pragma unroll
+            for (int n = 0; n < NP; ++n) h[n] = a.h0 && n < N ? a.h0[at_state + n] : 0.f;
+            if (STATES_ONLY && ok)
+#pragma unroll
+                for (int n = 0; n < NP; ++n) slots[(int64_t)n * D] = h[n];
+        } else {
+#pragma unroll
+            for (int n = 0; n < NP; ++n) h[n] = slots[(int64_t)n * D];
+        }
+    } else if (STATES_ONLY) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) h[n] = 0.f;
+    } else {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) h[n] = slots[((int64_t)NP + n) * D];
+        for (int j = 2; j <= seg; ++j) {
+            const float *q = slots + (int64_t)j * NP * D;
+            const float s = sums[(int64_t)j * D];
+            float v[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) v[n] = q[(int64_t)n * D];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) h[n] = __builtin_fmaf(fast_exp2(A2[n] * s), h[n], v[n]);
+        }
+    }
+
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
+    const int64_t base = (int64_t)b * a.T * D + d;
+    const T *xp = (const T *)a.x + base, *tp = (const T *)a.dt + base;
+    const T *zp = a.z ? (const T *)a.z + base : nullptr;
+    T *yp = (T *)a.y + base;
+    const int64_t rows = ((int64_t)b * a.T * a.G + g) * N;
+    const T *Bp = Bm + rows, *Cp = Cm + rows;
+    const int64_t row = (int64_t)a.G * N;
+
+    float sum = 0.f;
+    if (t0 < te) {
+        T xr[UNROLL], tr[UNROLL], zr[UNROLL];
+        const auto fetch = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < UNROLL; ++i) {
+                const int64_t o = (int64_t)min(t + i, te - 1) * D;
+                xr[i] = xp[o];
+                tr[i] = tp[o];
+                zr[i] = !STATES_ONLY && zp ? zp[o] : T(0);
+            }
+        };
+        fetch(t0);
+        for (int t = t0; t < te; t += UNROLL) {
+            float x[UNROLL], s[UNROLL], z[UNROLL];
+#pragma unroll
+            for (int i = 0; i < UNROLL; ++i) {
+                x[i] = to_f32(xr[i]);
+                s[i] = to_f32(tr[i]) + bias;
+                z[i] = to_f32(zr[i]);
+            }
+            if (t + UNROLL < te) fetch(t + UNROLL);
+#pragma unroll
+            for (int i = 0; i < UNROLL; ++i) {
+                const int tt = min(t + i, te - 1);
+                if (a.softplus) s[i] = softplus_f32(s[i]);
+                if (t + i >= te) s[i] = 0.f;   // behind the end: a token that changes nothing
+                sum += s[i];
+                const float u = s[i] * x[i];
+                float Bv[NP];
+                load_row_uniform<T, NP, FULL>(Bv, Bp + tt * row, N);
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+                    h[n] = __builtin_fmaf(fast_exp2(s[i] * A2[n]), h[n], u * Bv[n]);
+                if constexpr (!STATES_ONLY) {
+                    float Cv[NP], y0 = 0.f, y1 = 0.f;
+                    load_row_uniform<T, NP, FULL>(Cv, Cp + tt * row, N);
+#pragma unroll
+                    for (int n = 0; n < NP; n += 2) {
+                        y0 = __builtin_fmaf(Cv[n], h[n], y0);
+                        y1 = __builtin_fmaf(Cv[n + 1], h[n + 1], y1);
+                    }
+                    float y = __builtin_fmaf(skip, x[i], y0 + y1);
+                    if (zp) y *= z[i] * sigmoid_f32(z[i]);
+                    if (ok && t + i < te) yp[(int64_t)(t + i) * D] = from_f32<T>(y);
+                }
+            }
+        }
+    }
+    if (!ok) return;
+    if constexpr (STATES_ONLY) {
+        float *q = slots + (int64_t)(seg + 1) * NP * D;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) q[(int64_t)n * D] = h[n];
+        sums[(int64_t)(seg + 1) * D] = sum;
+    } else {
+        for (int t = max(t0, te); t < t1; ++t) yp[(int64_t)t * D] = from_f32<T>(0.f);
+        if (a.h_final && seg == sg.count - 1)
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+                if (n < N) a.h_final[at_state + n] = h[n];
+    }
+}
+
+// One token: LPC lanes a channel, 4 states each, so a wavefront's states are
+// contiguous 16-byte accesses; the read and write of the states bound it.
+template <typename T, int LPC, bool VEC>
+__global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int64_t channels)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t c = min(id / LPC, channels - 1);   // idle groups repeat the last channel
+    const bool ok = id / LPC < channels;
+    const int l = id % LPC, D = a.D, N = a.N, n0 = 4 * l;
+    const int b = (int)(c / D), d = (int)(c % D), g = d / (D / a.G);
+    float *hp = a.h_final + c * N;
+    const int64_t row = ((int64_t)b * a.G + g) * N;
+    const T *Bp = (const T *)a.Bm + row, *Cp = (const T *)a.Cm + row;
+    const float *Ap = a.A + (int64_t)d * N;
+
+    float h[4], A[4], B[4], C[4];
+    if constexpr (VEC) {
+        if (n0 < N) {
+            Raw4<float> r;
+            Raw4<T> q;
+            r.load(hp + n0);
+            r.to_f32(h);
+            r.load(Ap + n0);
+            r.to_f32(A);
+            q.load(Bp + n0);
+            q.to_f32(B);
+            q.load(Cp + n0);
+            q.to_f32(C);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool in = n0 + i < N;
+        if (!VEC || !in) {
+            h[i] = in ? hp[n0 + i] : 0.f;
+            A[i] = in ? Ap[n0 + i] : 0.f;
+            B[i] = in ? to_f32(Bp[n0 + i]) : 0.f;
+            C[i] = in ? to_f32(Cp[n0 + i]) : 0.f;
+        }
+    }
+    const float x = to_f32(((const T *)a.x)[c]);
+    float s = to_f32(((const T *)a.dt)[c]) + (a.dt_bias ? a.dt_bias[d] : 0.f);
+    if (a.softplus) s = softplus_f32(s);
+    const float u = s * x, s2 = s * LOG2E;
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = __builtin_fmaf(fast_exp2(s2 * A[i]), h[i], u * B[i]);
+        y = __builtin_fmaf(C[i], h[i], y);
+    }
+#pragma unroll
+    for (int m = 1; m < LPC; m <<= 1) y += __shfl_xor(y, m, LPC);
+    if (!ok) return;
+    if (VEC) {
+        if (n0 < N) store4(hp + n0, h);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 + i < N) hp[n0 + i] = h[i];
+    }
+    if (l == 0) {
+        if (a.Dskip) y = __builtin_fmaf(a.Dskip[d], x, y);
+        if (a.z) {
+            const float z = to_f32(((const T *)a.z)[c]);
+            y *= z * sigmoid_f32(z);
+        }
+        ((T *)a.y)[c] = from_f32<T>(y);
+    }
+}
+
+int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // NB
+int channel_tiles(int D, int G) { return (D / G + 63) / 64; }
+
+// Segments: as many as bring the wavefronts to four a SIMD (4096), at least
+// 16 tokens each and at most 64 of them (every segment reads the end states
+// of those in front of it).
+Segments plan(int B, int T, int D, int G)
+{
+    const int64_t waves = (int64_t)B * G * channel_tiles(D, G);
+    int64_t n = (4096 + waves - 1) / waves;
+    n = min(n, min((int64_t)64, (int64_t)(T / 16)));
+    Segments s{};
+    s.count = (int)max(n, (int64_t)1);
+    s.tokens = (T + s.count - 1) / s.count;
+    if (s.count > 1) s.tokens = (s.tokens + UNROLL - 1) / UNROLL * UNROLL;
+    s.count = s.tokens > 0 ? (T + s.tokens - 1) / s.tokens : 1;
+    return s;
+}
+
+template <typename T, int NB, bool FULL>
+hipError_t fwd_launch(const ScanArgs &a, hipStream_t stream)
+{
+    const int tiles = channel_tiles(a.D, a.G);
+    Segments s = plan(a.B, a.T, a.D, a.G);
+    if (!a.ws || s.count == 1) {
+        s.count = 1;
+        s.tokens = a.T;
+    }
+    const int64_t waves = (int64_t)a.B * a.G * tiles;
+    if (waves * s.count >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (s.count > 1) {
+        s.slots = a.ws;
+        s.sums = a.ws + (int64_t)a.B * s.count * 16 * NB * a.D;
+        kda_scan_kernel<T, NB, FULL, true><<<(unsigned)(waves * (s.count - 1)), 64, 0, stream>>>(
+            a, (const T *)a.Bm, (const T *)a.Cm, s, tiles);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    kda_scan_kernel<T, NB, FULL, false><<<(unsigned)(waves * s.count), 64, 0, stream>>>(
+            a, (const T *)a.Bm, (const T *)a.Cm, s, tiles);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t fwd_dispatch(const ScanArgs &a, hipStream_t s)
+{
+    switch (state_blocks(a.N)) {
+    case 1: return a.N == 16 ? fwd_launch<T, 1, true>(a, s) : fwd_launch<T, 1, false>(a, s);
+    case 2: return a.N == 32 ? fwd_launch<T, 2, true>(a, s) : fwd_launch<T, 2, false>(a, s);
+    default: return a.N == 64 ? fwd_launch<T, 4, true>(a, s) : fwd_launch<T, 4, false>(a, s);
+    }
+}
+
+template <typename T, int LPC> hipError_t step_launch(const ScanArgs &a, hipStream_t s)
+{
+    const int64_t channels = (int64_t)a.B * a.D, blocks = (channels * LPC + 255) / 256;
+    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (a.N % 4 == 0) kda_scan_step_kernel<T, LPC, true><<<(unsigned)blocks, 256, 0, s>>>(a, channels);
+    else kda_scan_step_kernel<T, LPC, false><<<(unsigned)blocks, 256, 0, s>>>(a, channels);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t step_dispatch(const ScanArgs &a, hipStream_t s)
+{
+    if (a.N <= 4) return step_launch<T, 1>(a, s);
+    if (a.N <= 8) return step_launch<T, 2>(a, s);
+    if (a.N <= 16) return step_launch<T, 4>(a, s);
+    if (a.N <= 32) return step_launch<T, 8>(a, s);
+    return step_launch<T, 16>(a, s);
+}
+
+}  // namespace
+
+int64_t scan_fwd_workspace_floats(int B, int T, int D, int N, int G)
+{
+    const Segments s = plan(B, T, D, G);
+    return s.count > 1 ? (int64_t)B * s.count * D * (16 * state_blocks(N) + 1) : 0;
+}
+
+hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t s)
+{
+    (void)hipGetLastError();
+    return a.bf16 ? fwd_dispatch<uint16_t>(a, s) : fwd_dispatch<float>(a, s);
+}
+
+hipError_t launch_scan_step(const ScanArgs &a, hipStream_t s)
+{
+    (void)hipGetLastError();
+    return a.bf16 ? step_dispatch<uint16_t>(a, s) : step_dispatch<float>(a, s);
+}
+
+}  // namespace kda

@@ -35,7 +35,11 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_gate", "kda_chunk_fwd_ws", "kda_chunk
            "kda_chunk_fwd_seqpar_segments", "kda_chunk_fwd_gate_seqpar",
            "kda_chunk_fwd_workspace_bytes", "kda_debug_set_spin_limit", "kda_verify_step", "kda_commit_step",
            "kda_decode_step", "kda_decode_step_gate", "kda_decode_step_gated", "kda_output_gate",
-           "kda_chunk_bwd", "kda_chunk_bwd_workspace_bytes", "kda_status_string", "kda_abi_version")
+           "kda_chunk_bwd", "kda_chunk_bwd_workspace_bytes", "kda_status_string", "kda_abi_version",
+           "kda_short_conv_fwd", "kda_short_conv_step", "kda_short_conv_bwd", "kda_short_conv_bwd_workspace_bytes",
+           "kda_selective_scan_fwd", "kda_selective_scan_fwd_workspace_bytes", "kda_selective_scan_step",
+           "kda_selective_scan_bwd", "kda_selective_scan_bwd_workspace_bytes",
+           "kda_layer_norm_fwd", "kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_bytes")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -96,6 +100,24 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.kda_chunk_bwd_workspace_bytes.restype = sz
     lib.kda_chunk_bwd.argtypes = [vp] * 15 + [sz] + [i] * 8 + [vp]
     lib.kda_chunk_bwd.restype = i
+    i64 = ctypes.c_int64
+    for name, args in {
+            "kda_short_conv_fwd": [vp] * 7 + [i] * 6 + [vp],
+            "kda_short_conv_step": [vp] * 5 + [i] * 5 + [vp],
+            "kda_short_conv_bwd": [vp] * 12 + [sz] + [i] * 6 + [vp],
+            "kda_selective_scan_fwd": [vp] * 13 + [sz] + [i] * 7 + [vp],
+            "kda_selective_scan_step": [vp] * 10 + [i] * 6 + [vp],
+            "kda_selective_scan_bwd": [vp] * 22 + [sz] + [i] * 7 + [vp],
+            "kda_layer_norm_fwd": [vp] * 3 + [f, vp, i64, i, i, vp],
+            "kda_layer_norm_bwd": [vp] * 3 + [f] + [vp] * 4 + [sz, i64, i, i, vp]}.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i
+    for name, args in {"kda_short_conv_bwd_workspace_bytes": [i] * 4,
+                       "kda_selective_scan_fwd_workspace_bytes": [i] * 5,
+                       "kda_selective_scan_bwd_workspace_bytes": [i] * 5,
+                       "kda_layer_norm_bwd_workspace_bytes": [i64, i]}.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = sz
     lib.kda_status_string.argtypes = [i]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_abi_version.argtypes = []

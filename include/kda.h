@@ -448,6 +448,164 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const void *v, const vo
                            kda_dtype_t qkv_dtype, kda_dtype_t gate_dtype, kda_dtype_t do_dtype,
                            void *stream);
 
+/*
+ * Short causal convolution, selective state space scan and layer norm: the
+ * rest of a recurrent block around the layer above.  Common to these calls:
+ *
+ *  - One storage type per call (`dtype`: KDA_F32 or KDA_BF16) for every
+ *    per-token tensor, inputs, outputs and their gradients alike; parameters,
+ *    states of the scan and parameters' gradients are float32.  Arithmetic,
+ *    sums and states are float32; each output is rounded once, when stored.
+ *  - D (channels) and T are any size >= 0; a call with nothing to compute
+ *    still writes what its contract defines (states copied, gradients zero).
+ *    B T D, and every tensor's element count, must stay below 2^40, B, T and
+ *    D below 2^24 each (KDA_ERR_UNSUPPORTED beyond).
+ *  - lengths [B] int32 (device, or NULL: all T) are the sequences' lengths in
+ *    a right-padded batch, clamped to [0, T].  Tokens behind a sequence's end
+ *    are never read (they may hold anything, NaN included); their outputs and
+ *    their gradients are written as zeros, and final states are those after
+ *    the last real token.
+ *  - A workspace is device memory owned by the caller, 16-byte aligned, of at
+ *    least the bytes the call's _workspace_bytes function gives (0: none
+ *    needed, NULL allowed); no initialisation needed, contents undefined
+ *    afterwards.  Calls sharing one workspace must not overlap in time.
+ *  - No output may overlap an input, another output or the workspace, except
+ *    where stated.  Results do not depend on timing: no atomics are used.
+ */
+
+/*
+ * kda_short_conv_fwd -- depthwise causal convolution over the last W tokens of
+ * each channel, with an optional SiLU.
+ *
+ *   pre[b, t, d] = bias[d] + sum_{j < W} w[d, j] x[b, t - W + 1 + j, d]
+ *   y = pre * sigmoid(pre) if silu != 0, else pre
+ *
+ *   x            [B, T, D]      dtype
+ *   w            [D, W] float32 (tap W - 1 is the current token's), bias [D] float32 or NULL
+ *   state0       [B, W - 1, D]  dtype: the W - 1 inputs in front of token 0, oldest first;
+ *                               NULL for zeros
+ *   y            [B, T, D]      dtype (written)
+ *   state_final  [B, W - 1, D]  dtype: the last W - 1 inputs (of state0 followed by the
+ *                               sequence), written unless NULL; may be state0 itself
+ *
+ * W in {2, 3, 4} (KDA_ERR_UNSUPPORTED otherwise).
+ */
+kda_status_t kda_short_conv_fwd(const void *x, const float *w, const float *bias, const void *state0,
+                                const int *lengths, void *y, void *state_final,
+                                int B, int T, int D, int W, int silu, kda_dtype_t dtype, void *stream);
+
+/*
+ * kda_short_conv_step -- one token per sequence: x [B, D], y [B, D], and
+ * state [B, W - 1, D] shifted by one token IN PLACE.  y may be x itself.
+ */
+kda_status_t kda_short_conv_step(const void *x, const float *w, const float *bias, void *state, void *y,
+                                 int B, int D, int W, int silu, kda_dtype_t dtype, void *stream);
+
+/*
+ * kda_short_conv_bwd -- gradients of kda_short_conv_fwd for the upstream
+ * gradients dy [B, T, D] of y and dstate_final [B, W - 1, D] (dtype, or NULL)
+ * of state_final.
+ *
+ *   dx [B, T, D] dtype, dw [D, W] float32, dbias [D] float32 or NULL,
+ *   dstate0 [B, W - 1, D] dtype or NULL (written unless NULL)
+ */
+size_t kda_short_conv_bwd_workspace_bytes(int B, int T, int D, int W);
+
+kda_status_t kda_short_conv_bwd(const void *dy, const void *x, const float *w, const float *bias,
+                                const void *state0, const void *dstate_final, const int *lengths,
+                                void *dx, float *dw, float *dbias, void *dstate0,
+                                void *workspace, size_t workspace_bytes,
+                                int B, int T, int D, int W, int silu, kda_dtype_t dtype, void *stream);
+
+/*
+ * kda_selective_scan_fwd -- the selective state space recurrence: every
+ * channel d carries N states that fade at rates A[d, :] times the token's own
+ * time step, and takes its input through the token's own B and C rows.
+ *
+ *   s = dt + dt_bias, or softplus(dt + dt_bias) if softplus != 0
+ *   h[d, n] <- exp(s[d] A[d, n]) h[d, n] + s[d] x[d] Bm[g, n],   g = d / (D / G)
+ *   y[d] = (sum_n Cm[g, n] h[d, n] + Dskip[d] x[d]) * (z[d] sigmoid(z[d]))
+ *
+ *   x, dt    [B, T, D]     dtype
+ *   A        [D, N] float32; A <= 0 keeps the states bounded (not checked)
+ *   Bm, Cm   [B, T, G, N]  dtype; G groups of D / G channels each share them
+ *   Dskip    [D] float32 or NULL (0);  dt_bias [D] float32 or NULL (0)
+ *   z        [B, T, D]     dtype, or NULL: no gate
+ *   h0       [B, D, N] float32, or NULL for zeros
+ *   y        [B, T, D]     dtype (written)
+ *   h_final  [B, D, N] float32 (written), or NULL; may be h0 itself
+ *   workspace: with at least kda_selective_scan_fwd_workspace_bytes bytes the
+ *            sequence is cut into segments run side by side and joined through
+ *            their decays and end states; NULL runs each channel's tokens in one
+ *            chain (the same results up to float32 rounding, slower where B D
+ *            does not fill the device)
+ *
+ * N from 1 to 64, G >= 1 dividing D (KDA_ERR_INVALID_ARG if it does not);
+ * 16, 32 and 64 states run fastest, other counts are padded to them.
+ */
+size_t kda_selective_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G);
+
+kda_status_t kda_selective_scan_fwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                    const float *Dskip, const void *z, const float *dt_bias, const float *h0,
+                                    const int *lengths, void *y, float *h_final,
+                                    void *workspace, size_t workspace_bytes,
+                                    int B, int T, int D, int N, int G, int softplus, kda_dtype_t dtype,
+                                    void *stream);
+
+/*
+ * kda_selective_scan_step -- one token per sequence: x, dt, z, y [B, D],
+ * Bm, Cm [B, G, N], the states h [B, D, N] float32 advanced IN PLACE.
+ */
+kda_status_t kda_selective_scan_step(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                     const float *Dskip, const void *z, const float *dt_bias, float *h, void *y,
+                                     int B, int D, int N, int G, int softplus, kda_dtype_t dtype, void *stream);
+
+/*
+ * kda_selective_scan_bwd -- gradients of kda_selective_scan_fwd for the
+ * upstream gradients dy [B, T, D] (dtype) of y and dh_final [B, D, N] (float32,
+ * or NULL) of h_final; the states are recomputed, nothing of the forward call
+ * is needed.
+ *
+ *   dx, ddt [B, T, D] dtype;  dz [B, T, D] dtype, NULL exactly when z is NULL
+ *   dA [D, N] float32;  dBm, dCm [B, T, G, N] dtype
+ *   dDskip [D] float32, NULL exactly when Dskip is NULL
+ *   ddt_bias [D] float32, NULL exactly when dt_bias is NULL
+ *   dh0 [B, D, N] float32 or NULL (not written)
+ */
+size_t kda_selective_scan_bwd_workspace_bytes(int B, int T, int D, int N, int G);
+
+kda_status_t kda_selective_scan_bwd(const void *dy, const void *x, const void *dt, const float *A, const void *Bm,
+                                    const void *Cm, const float *Dskip, const void *z, const float *dt_bias,
+                                    const float *h0, const float *dh_final, const int *lengths,
+                                    void *dx, void *ddt, float *dA, void *dBm, void *dCm, float *dDskip, void *dz,
+                                    float *ddt_bias, float *dh0, void *workspace, size_t workspace_bytes,
+                                    int B, int T, int D, int N, int G, int softplus, kda_dtype_t dtype,
+                                    void *stream);
+
+/*
+ * kda_layer_norm_fwd -- y = (x - mean) / sqrt(var + eps) * weight + bias over
+ * rows of D channels, the variance over D (not D - 1).
+ *
+ *   x, y   [rows, D] dtype; y may be x itself
+ *   weight [D] float32 or NULL (1), bias [D] float32 or NULL (0)
+ *   eps    >= 0, finite (a constant row with eps = 0 is NaN, as the formula is)
+ *
+ * D from 1 to 16384 (KDA_ERR_UNSUPPORTED beyond), rows below 2^40.
+ */
+kda_status_t kda_layer_norm_fwd(const void *x, const float *weight, const float *bias, float eps, void *y,
+                                int64_t rows, int D, kda_dtype_t dtype, void *stream);
+
+/*
+ * kda_layer_norm_bwd -- gradients of kda_layer_norm_fwd: dx [rows, D] (dtype;
+ * may be dy itself), dweight and dbias [D] float32, each or both NULL where
+ * not wanted.  The rows' means and variances are computed again from x.
+ */
+size_t kda_layer_norm_bwd_workspace_bytes(int64_t rows, int D);
+
+kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const float *weight, float eps, void *dx,
+                                float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                                int64_t rows, int D, kda_dtype_t dtype, void *stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *kda_status_string(kda_status_t status);   /* codes outside the set: "KDA_ERR_UNKNOWN" */
 
