@@ -50,6 +50,33 @@ __device__ __forceinline__ float softplus_f32(float v) {
     return fmaxf(v, 0.f) + log1p_unit(fast_exp2(-fabsf(v) * LOG2E));
 }
 
+// The NP values of a token's B or C row, the same for the whole wavefront.
+// FULL rows (N = NP) are read as 32-bit words through the scalar cache.  Other
+// N (rows that may start on any element): lane n loads element n once, and each
+// value is handed to all lanes by a lane read; the padding states' values are
+// zero.
+template <typename T, int NP, bool FULL>
+__device__ __forceinline__ void load_row_uniform(float (&o)[NP], const T *p, int N)
+{
+    if constexpr (FULL && sizeof(T) == 2) {
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) {
+            const uint32_t w = q[i];
+            o[2 * i] = __uint_as_float(w << 16);
+            o[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+    } else if constexpr (FULL) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) o[i] = p[i];
+    } else {
+        const int lane = threadIdx.x & 63;
+        const float v = lane < N ? kda::to_f32(p[lane]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) o[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+    }
+}
+
 // Tokens of sequence b: lengths[b] clamped to [0, T], or T.
 __device__ __forceinline__ int seq_length(const int *lengths, int b, int T) {
     return lengths ? min(max(lengths[b], 0), T) : T;

@@ -26,29 +26,6 @@ namespace {
 
 constexpr int UNROLL = 8;   // tokens whose inputs are loaded together, one batch ahead
 
-// The NP values of a token's B or C row, the same for the whole wavefront.
-// FULL rows (N = NP) are read as 32-bit words through the scalar cache; other
-// N element by element, the padding states' values zero.
-template <typename T, int NP, bool FULL>
-__device__ __forceinline__ void load_row_uniform(float (&o)[NP], const T *p, int N)
-{
-    if constexpr (FULL && sizeof(T) == 2) {
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
-#pragma unroll
-        for (int i = 0; i < NP / 2; ++i) {
-            const uint32_t w = q[i];
-            o[2 * i] = __uint_as_float(w << 16);
-            o[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-        }
-    } else if constexpr (FULL) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) o[i] = p[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) o[i] = i < N ? to_f32(p[i]) : 0.f;
-    }
-}
-
 // Workspace of the segmented forward: slot 0 is a copy of h0 (h_final may be
 // h0 itself, and other wavefronts write it while segment 0 still starts), slot
 // s the state at the end of segment s - 1 and sum[s] that segment's sum of

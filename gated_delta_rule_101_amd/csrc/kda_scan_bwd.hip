@@ -12,25 +12,24 @@
 //
 // Four kernels.
 //  1. Segments of SEG tokens side by side, a lane a channel as in the forward:
-//     the state a segment adds (from zero) and, with the running decay
-//     P_t = prod a, the gradient it adds in front of itself, sum_t P_t C_t gy_t.
-//     Both directions share each exp.
+//     the states it adds (from zero), stored at every chunk of 16 tokens, and,
+//     with the running decay P_t = prod a, the gradient it adds in front of
+//     itself, sum_t P_t C_t gy_t.  Both directions share each exp.
 //  2. The true state in front of every segment and the true gradient behind it,
 //     one thread per (d, n) over the segments.
-//  3. The gradients.  A workgroup owns 64 channels and one segment.  Here a lane
-//     owns ONE state of one channel (16 lanes a channel, 4 channels a
-//     wavefront), so a whole chunk of 16 tokens keeps its decays and states in
-//     registers between the forward and the reverse walk, and the sums over
+//  3. The gradients.  A workgroup owns 64 channels and one segment, and walks
+//     its chunks backwards.  Here a lane owns ONE state of one channel (16 lanes
+//     a channel, 4 channels a wavefront), so a chunk keeps its decays and states
+//     in registers between its forward and its reverse walk, and the sums over
 //     channels of dB and dC are plain accumulators while the wavefront goes
 //     through its channels.  The sums over n (r, p1, p2) reduce 16 tokens over
 //     16 lanes by a butterfly that halves the values at each step (2 additions
-//     a value), leaving lane i with token i.  Per-token values enter as DPP row
-//     broadcasts of a register that holds token i in lane i.  First the
-//     segment's states at every chunk start are recomputed into LDS, then the
-//     chunks run backwards.
+//     a value), leaving lane i with token i.  Per-token values sit in a register
+//     that holds token i in lane i and enter the arithmetic as DPP row
+//     broadcasts, without instructions of their own.
 //  4. Column sums of the workgroups' partial dA, dD, dbias, dB, dC.
-// Bound by vector instructions (about 22 issue slots per token, channel and
-// state in kernel 3, 7 for its recomputation, 9 in kernel 1).
+// Bound by vector instructions: about 20 issue slots per token, channel and
+// state in kernel 3, 8 in kernel 1.
 #include "kda_block.h"
 #include "kda_block_device.h"
 
@@ -41,15 +40,16 @@ constexpr int CHUNK = 16;        // tokens a chunk: one per lane of a DPP row
 constexpr int CH = 64;           // channels a workgroup
 constexpr int WAVES = 4, QUADS = CH / WAVES / 4;
 
-// Blocks of 16 states, and chunks a segment (LDS: a chunk's start states take
-// 4 KiB per block).
-int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }
-constexpr int seg_chunks(int nb) { return nb <= 2 ? 8 : 4; }
+constexpr int SEG_CHUNKS = 8, SEG = CHUNK * SEG_CHUNKS;
+constexpr int UNROLL = 4;        // tokens whose inputs are loaded together
+
+int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // of 16
 
 // Workspace, in floats.
 struct Layout {
-    int nseg, tiles, np;             // segments, 64-channel tiles a group, padded states
+    int nseg, nchunk, tiles, np;     // segments, chunks, 64-channel tiles a group, padded states
     float *h, *g, *sum;              // [B][nseg][D][np] states in front / gradients behind; [B][nseg][D]
+    float *hc, *sc;                  // [B][nchunk][D][np] states a segment adds up to a chunk; [B][nchunk][D]
     float *dA, *dD, *db;             // [B nseg][D][N], [B nseg][D] twice
     float *dB, *dC;                  // [tiles][B][T][G][N]
     int64_t floats;
@@ -57,10 +57,10 @@ struct Layout {
 Layout layout(float *p, int B, int T, int D, int N, int G)
 {
     Layout w;
-    const int nb = state_blocks(N), seg = CHUNK * seg_chunks(nb);
-    w.nseg = T > 0 ? (T + seg - 1) / seg : 0;
+    w.nseg = (T + SEG - 1) / SEG;
+    w.nchunk = (T + CHUNK - 1) / CHUNK;
     w.tiles = (D / G + CH - 1) / CH;
-    w.np = 16 * nb;
+    w.np = 16 * state_blocks(N);
     const auto r4 = [](int64_t n) { return (n + 3) / 4 * 4; };   // 16-byte aligned parts
     const int64_t bs = (int64_t)B * w.nseg;
     const int64_t state = bs * D * w.np, chan = r4(bs * D), rows = r4((int64_t)w.tiles * B * T * G * N);
@@ -70,6 +70,8 @@ Layout layout(float *p, int B, int T, int D, int N, int G)
     w.h = take(state);
     w.g = take(state);
     w.sum = take(chan);
+    w.hc = take((int64_t)B * w.nchunk * D * w.np);
+    w.sc = take(r4((int64_t)B * w.nchunk * D));
     w.dA = take(a);
     w.dD = take(chan);
     w.db = take(chan);
@@ -81,16 +83,9 @@ Layout layout(float *p, int B, int T, int D, int N, int G)
 
 // --------------------------------------------------- 1. what a segment adds
 
-template <typename T, int NP>
-__device__ __forceinline__ void row_uniform(float (&o)[NP], const T *p, int N)
-{
-#pragma unroll
-    for (int i = 0; i < NP; ++i) o[i] = i < N ? to_f32(p[i]) : 0.f;
-}
-
-template <typename T, int NB>
+template <typename T, int NB, bool FULL>
 __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a, const T *__restrict__ Bm,
-                                                                  const T *__restrict__ Cm, Layout w, int seg_tokens)
+                                                                  const T *__restrict__ Cm, Layout w)
 {
     constexpr int NP = 16 * NB;
     unsigned id = blockIdx.x;
@@ -104,7 +99,7 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
     const bool ok = c < Dg;
     const int d = grp * Dg + (ok ? c : Dg - 1);
     const int len = seq_length(a.lengths, b, a.T);
-    const int t0 = seg * seg_tokens, te = min(t0 + seg_tokens, len);
+    const int t0 = seg * SEG, t1 = min(t0 + SEG, a.T), te = min(t1, len);
 
     float A2[NP], h[NP], r[NP], P[NP];
 #pragma unroll
@@ -119,26 +114,56 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
     const T *zp = a.z ? (const T *)a.z + base : nullptr;
     const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N, row = (int64_t)a.G * N;
     float sum = 0.f;
-    for (int t = t0; t < te; ++t) {
-        const int64_t o = (int64_t)t * D;
-        const float x = to_f32(xp[o]);
-        float s = to_f32(tp[o]) + bias, gy = to_f32(gp[o]);
-        if (a.softplus) s = softplus_f32(s);
-        if (zp) {
-            const float z = to_f32(zp[o]);
-            gy *= z * sigmoid_f32(z);
-        }
-        sum += s;
-        const float u = s * x;
-        float Bv[NP], Cv[NP];
-        row_uniform<T, NP>(Bv, Bm + row0 + t * row, N);
-        row_uniform<T, NP>(Cv, Cm + row0 + t * row, N);
+    T xr[UNROLL], tr[UNROLL], gr[UNROLL], zr[UNROLL];
+    const auto fetch = [&](int t) {
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            const float e = fast_exp2(s * A2[n]);
-            h[n] = __builtin_fmaf(e, h[n], u * Bv[n]);
-            P[n] *= e;
-            r[n] = __builtin_fmaf(P[n], gy * Cv[n], r[n]);
+        for (int i = 0; i < UNROLL; ++i) {
+            const int64_t o = (int64_t)min(t + i, te - 1) * D;
+            xr[i] = xp[o];
+            tr[i] = tp[o];
+            gr[i] = gp[o];
+            zr[i] = zp ? zp[o] : T(0);
+        }
+    };
+    if (t0 < te) fetch(t0);
+    for (int t = t0; t < t1; t += UNROLL) {
+        if (t % CHUNK == 0 && t > t0 && ok) {   // a segment's first chunk adds nothing
+            const int64_t at = ((int64_t)b * w.nchunk + t / CHUNK) * D + d;
+#pragma unroll
+            for (int n = 0; n < NP; n += 4) {
+                const float v[4] = {h[n], h[n + 1], h[n + 2], h[n + 3]};
+                store4(w.hc + at * NP + n, v);
+            }
+            w.sc[at] = sum;
+        }
+        if (t >= te) continue;
+        float x[UNROLL], s[UNROLL], gy[UNROLL], z[UNROLL];
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+            x[i] = to_f32(xr[i]);
+            s[i] = to_f32(tr[i]) + bias;
+            gy[i] = to_f32(gr[i]);
+            z[i] = to_f32(zr[i]);
+        }
+        if (t + UNROLL < te) fetch(t + UNROLL);
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+            const int64_t tt = row0 + (int64_t)min(t + i, te - 1) * row;
+            if (a.softplus) s[i] = softplus_f32(s[i]);
+            if (zp) gy[i] *= z[i] * sigmoid_f32(z[i]);
+            if (t + i >= te) s[i] = gy[i] = 0.f;   // behind the end: a token that changes nothing
+            sum += s[i];
+            const float u = s[i] * x[i];
+            float Bv[NP], Cv[NP];
+            load_row_uniform<T, NP, FULL>(Bv, Bm + tt, N);
+            load_row_uniform<T, NP, FULL>(Cv, Cm + tt, N);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const float e = fast_exp2(s[i] * A2[n]);
+                h[n] = __builtin_fmaf(e, h[n], u * Bv[n]);
+                P[n] *= e;
+                r[n] = __builtin_fmaf(P[n], gy[i] * Cv[n], r[n]);
+            }
         }
     }
     if (!ok) return;
@@ -192,29 +217,46 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_join_kernel(ScanBwdArgs a, L
 // returns token i's sum.  Each step adds a partner lane's half of the values
 // to the own half: lanes 8..15 keep tokens 8..15, then lanes with bit 2 set
 // the upper four, and so on.
-template <int CTRL, int BANKS>
-__device__ __forceinline__ float dpp_add(float keep, float x)
+//
+// A DPP source must not come from a vector instruction within the two before.
+// The compiler keeps that rule for its own instructions but does not look into
+// assembly, hence the s_nop in front of each block (its inputs) and behind the
+// last (its outputs).
+template <int CTRL> __device__ __forceinline__ float add_partner(float x)
 {
-    // lanes of the selected banks: x + x of the partner lane; others: keep
-    const int p = __builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true);
-    const float s = x + __int_as_float(p);
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(keep), __float_as_int(s), 0xE4, 0xF, BANKS, false));
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
 }
 __device__ __forceinline__ float row_sum_tokens(const float (&v)[16])
 {
-    constexpr int ROR8 = 0x128, SHL4 = 0x104, SHR4 = 0x114, SWAP2 = 0x4E, SWAP1 = 0xB1;
+    constexpr int SWAP2 = 0x4E, SWAP1 = 0xB1;   // quad_perm [2,3,0,1], [1,0,3,2]
     const int lane = threadIdx.x & 15;
     float a[8], b[4], c[2];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = dpp_add<ROR8, 0xC>(dpp_add<ROR8, 0xF>(0.f, v[i]), v[i + 8]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = dpp_add<SHR4, 0xA>(dpp_add<SHL4, 0xF>(0.f, a[i]), a[i + 4]);
+    // a[i]: v[i] of lanes l and l ^ 8 in lanes 0..7, v[i + 8] in lanes 8..15
+#define KDA_ROR8(i, j) "v_add_f32_dpp %" #i ", %" #j ", %" #j " row_ror:8 row_mask:0xf bank_mask:0xf\n"
+#define KDA_ROR8H(i, j) "v_add_f32_dpp %" #i ", %" #j ", %" #j " row_ror:8 row_mask:0xf bank_mask:0xc\n"
+    asm("s_nop 1\n" KDA_ROR8(0, 8) KDA_ROR8(1, 9) KDA_ROR8(2, 10) KDA_ROR8(3, 11) KDA_ROR8(4, 12) KDA_ROR8(5, 13)
+        KDA_ROR8(6, 14) KDA_ROR8(7, 15) KDA_ROR8H(0, 16) KDA_ROR8H(1, 17) KDA_ROR8H(2, 18) KDA_ROR8H(3, 19)
+        KDA_ROR8H(4, 20) KDA_ROR8H(5, 21) KDA_ROR8H(6, 22) KDA_ROR8H(7, 23)
+        : "=&v"(a[0]), "=&v"(a[1]), "=&v"(a[2]), "=&v"(a[3]), "=&v"(a[4]), "=&v"(a[5]), "=&v"(a[6]), "=&v"(a[7])
+        : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "v"(v[8]),
+          "v"(v[9]), "v"(v[10]), "v"(v[11]), "v"(v[12]), "v"(v[13]), "v"(v[14]), "v"(v[15]));
+#undef KDA_ROR8
+#undef KDA_ROR8H
+    // b[i]: lanes without bit 2 add lane l + 4 of a[i], lanes with it lane l - 4 of a[i + 4]
+#define KDA_SHL4(i, j) "v_add_f32_dpp %" #i ", %" #j ", %" #j " row_shl:4 row_mask:0xf bank_mask:0x5\n"
+#define KDA_SHR4(i, j) "v_add_f32_dpp %" #i ", %" #j ", %" #j " row_shr:4 row_mask:0xf bank_mask:0xa\n"
+    asm("s_nop 1\n" KDA_SHL4(0, 4) KDA_SHL4(1, 5) KDA_SHL4(2, 6) KDA_SHL4(3, 7) KDA_SHR4(0, 8) KDA_SHR4(1, 9)
+        KDA_SHR4(2, 10) KDA_SHR4(3, 11) "s_nop 1"
+        : "=&v"(b[0]), "=&v"(b[1]), "=&v"(b[2]), "=&v"(b[3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(a[4]), "v"(a[5]), "v"(a[6]), "v"(a[7]));
+#undef KDA_SHL4
+#undef KDA_SHR4
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float p = dpp_add<SWAP2, 0xF>(0.f, b[i]), q = dpp_add<SWAP2, 0xF>(0.f, b[i + 2]);
+        const float p = add_partner<SWAP2>(b[i]), q = add_partner<SWAP2>(b[i + 2]);
         c[i] = lane & 2 ? q : p;
     }
-    const float p = dpp_add<SWAP1, 0xF>(0.f, c[0]), q = dpp_add<SWAP1, 0xF>(0.f, c[1]);
+    const float p = add_partner<SWAP1>(c[0]), q = add_partner<SWAP1>(c[1]);
     return lane & 1 ? q : p;
 }
 
@@ -231,6 +273,13 @@ template <int I = CHUNK - 1, typename F> __device__ __forceinline__ void each_to
     if constexpr (I > 0) each_token_back<I - 1>(f);
 }
 
+// acc += (row's lane t of x) * y.  The DPP source x must not come from a
+// vector instruction within the two before: callers pass values read from LDS.
+template <int t> __device__ __forceinline__ void fma_bcast(float &acc, float x, float y)
+{
+    asm("v_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 row_mask:0xf bank_mask:0xf" : "+v"(acc) : "v"(x), "v"(y), "i"(t));
+}
+
 // [channel][16 tokens] tiles in LDS.  Threads that stage and finish tokens
 // access 4 tokens of one channel (16 bytes), 64 channels a wavefront; those
 // that compute access 4 channels' 16 tokens.  The 4-token pieces of a channel
@@ -241,13 +290,14 @@ __device__ __forceinline__ int token_at(int ch, int t) { return piece(ch, t >> 2
 template <typename T, int NB>
 __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout w)
 {
-    constexpr int K = NB <= 2 ? 8 : 4, SEG = K * CHUNK;
     static_assert(QUADS == 4 && WAVES * QUADS * 4 == CH, "a wavefront's channels");
+    static_assert(CHUNK == 16, "a token per lane of a DPP row");
     __shared__ __attribute__((aligned(16))) float t_s[CH * 16], t_u[CH * 16], t_g[CH * 16];   // s, s x, gy
     __shared__ __attribute__((aligned(16))) float t_r[CH * 16], t_p1[CH * 16], t_p2[CH * 16];
-    __shared__ float start[K][NB][CH * 16];               // states at the chunks' starts, [channel][16]
-    __shared__ float l_A[NB][CH * 16], l_g[NB][CH * 16], l_dA[NB][CH * 16];
-    __shared__ float flush[WAVES][8][64];                 // dB, dC of a chunk, per wavefront
+    __shared__ float t_B[NB][CHUNK * 16], t_C[NB][CHUNK * 16];              // [token][16 states]
+    __shared__ float l_h[NB][CH * 16];                                      // state in front of the chunk
+    __shared__ float l_A[NB][CH * 16], l_g[NB][CH * 16], l_dA[NB][CH * 16]; // [channel][16 states]
+    __shared__ float flush[WAVES][8][64];                                   // dB, dC of a chunk, per wavefront
 
     const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
     const int ch4 = lane / 16, n = lane & 15;             // compute: channel of the quad, state or token
@@ -262,68 +312,57 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
     const int t0 = seg * SEG, t1 = min(t0 + SEG, a.T), nch = (t1 - t0 + CHUNK - 1) / CHUNK;
     const int64_t bseg = (int64_t)b * w.nseg + seg;
 
-    // staging role: channel `lane` of the tile, tokens 4 wave .. 4 wave + 3 of a chunk
+    // staging role: channel `lane` of the tile, tokens 4 wave .. 4 wave + 3 of a
+    // chunk; and token tid / 16, state tid % 16 of B and C
     const bool ok = tile * CH + lane < Dg;
     const int d = grp * Dg + (ok ? tile * CH + lane : Dg - 1);
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
     const int64_t base = (int64_t)b * a.T * D + d;
     const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N, row = (int64_t)a.G * N;
 
-    for (int i = tid; i < NB * CH * 16; i += 256) {
-        const int nb = i / (CH * 16), c = i / 16 % CH, st = nb * 16 + (i & 15);
-        const bool in = tile * CH + c < Dg;
-        const int dd = grp * Dg + (in ? tile * CH + c : Dg - 1);
+    // h_start[i]: state in front of the segment, for the staging of l_h
+    constexpr int SLOTS = NB * CH * 16 / 256;
+    float h_seg[SLOTS];
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+        const int i = k * 256 + tid, nb = i / (CH * 16), c = i / 16 % CH, st = nb * 16 + (i & 15);
+        const int dd = grp * Dg + min(tile * CH + c, Dg - 1);
         const int64_t at = (bseg * D + dd) * w.np + st;
         l_A[nb][i % (CH * 16)] = st < N ? a.A[(int64_t)dd * N + st] : 0.f;
-        start[0][nb][i % (CH * 16)] = w.h[at];
+        h_seg[k] = w.h[at];
         l_g[nb][i % (CH * 16)] = w.g[at];
         l_dA[nb][i % (CH * 16)] = 0.f;
     }
 
-    // B or C of a chunk's tokens for the lane's state; zero behind the end
-    const auto load_rows = [&](float (&o)[CHUNK], const void *p, int tc, int nb) {
-        const int st = nb * 16 + n;
-#pragma unroll
-        for (int t = 0; t < CHUNK; ++t)
-            o[t] = tc + t < len && st < N ? to_f32(((const T *)p)[row0 + (tc + t) * row + st]) : 0.f;
-    };
-
-    // states at the chunks' starts
-    for (int c = 0; c + 1 < nch; ++c) {
+    // raw inputs of one chunk, loaded a chunk ahead
+    T xr[4], tr[4], gr[4], zr[4], Br[NB], Cr[NB];
+    float hr[SLOTS], sr[SLOTS];
+    const auto fetch = [&](int c) {
         const int tc = t0 + c * CHUNK;
-        float s4[4], u4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = tc + 4 * wave + i;
-            s4[i] = u4[i] = 0.f;
-            if (t < len) {
-                const int64_t o = base + (int64_t)t * D;
-                const float v = to_f32(((const T *)a.dt)[o]) + bias;
-                s4[i] = a.softplus ? softplus_f32(v) : v;
-                u4[i] = s4[i] * to_f32(((const T *)a.x)[o]);
-            }
+            const int64_t o = base + (int64_t)max(min(tc + 4 * wave + i, len - 1), 0) * D;
+            xr[i] = ((const T *)a.x)[o];
+            tr[i] = ((const T *)a.dt)[o];
+            gr[i] = ((const T *)a.dy)[o];
+            zr[i] = a.z ? ((const T *)a.z)[o] : T(0);
         }
-        store4(t_s + piece(lane, wave), s4);
-        store4(t_u + piece(lane, wave), u4);
-        __syncthreads();
+#pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            float Bv[CHUNK];
-            load_rows(Bv, a.Bm, tc, nb);
-#pragma unroll 1
-            for (int q = 0; q < QUADS; ++q) {
-                const int cc = wave * 16 + q * 4 + ch4, at = cc * 16 + n;
-                const float A2 = l_A[nb][at] * LOG2E;
-                const float sv = t_s[token_at(cc, n)], uv = t_u[token_at(cc, n)];
-                float h = start[c][nb][at];
-                each_token([&](auto tt) {
-                    constexpr int t = decltype(tt)::value;
-                    h = __builtin_fmaf(fast_exp2(row_bcast<t>(sv) * A2), h, row_bcast<t>(uv) * Bv[t]);
-                });
-                start[c + 1][nb][at] = h;
-            }
+            const int64_t o = row0 + (int64_t)max(min(tc + tid / 16, len - 1), 0) * row + min(nb * 16 + (tid & 15), N - 1);
+            Br[nb] = ((const T *)a.Bm)[o];
+            Cr[nb] = ((const T *)a.Cm)[o];
         }
-        __syncthreads();
-    }
+        if (c > 0)
+#pragma unroll
+            for (int k = 0; k < SLOTS; ++k) {
+                const int i = k * 256 + tid, nb = i / (CH * 16), cc = i / 16 % CH, st = nb * 16 + (i & 15);
+                const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D + grp * Dg + min(tile * CH + cc, Dg - 1);
+                hr[k] = w.hc[at * w.np + st];
+                sr[k] = w.sc[at];
+            }
+    };
+    fetch(nch - 1);
 
     float dD = 0.f, db = 0.f;
     for (int c = nch - 1; c >= 0; --c) {
@@ -331,38 +370,48 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
         float x4[4], s4[4], u4[4], g4[4], ds4[4], dz4[4];   // ds4: ds/ddt; dz4: dy silu'(z)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = tc + 4 * wave + i;
-            x4[i] = s4[i] = u4[i] = g4[i] = ds4[i] = dz4[i] = 0.f;
-            if (ok && t < len) {   // idle lanes stay zero: their channel is another's
-                const int64_t o = base + (int64_t)t * D;
-                const float v = to_f32(((const T *)a.dt)[o]) + bias, dy = to_f32(((const T *)a.dy)[o]);
-                x4[i] = to_f32(((const T *)a.x)[o]);
-                s4[i] = a.softplus ? softplus_f32(v) : v;
-                ds4[i] = a.softplus ? sigmoid_f32(v) : 1.f;
-                u4[i] = s4[i] * x4[i];
-                g4[i] = dy;
-                if (a.z) {
-                    const float z = to_f32(((const T *)a.z)[o]), sg = sigmoid_f32(z);
-                    g4[i] = dy * z * sg;
-                    dz4[i] = dy * sg * __builtin_fmaf(z, 1.f - sg, 1.f);
-                }
-            }
+            const bool in = ok && tc + 4 * wave + i < len;   // idle lanes stay zero: their channel is another's
+            const float v = to_f32(tr[i]) + bias, dy = to_f32(gr[i]), z = to_f32(zr[i]);
+            const float sg = sigmoid_f32(z);
+            x4[i] = in ? to_f32(xr[i]) : 0.f;
+            s4[i] = in ? (a.softplus ? softplus_f32(v) : v) : 0.f;
+            ds4[i] = in ? (a.softplus ? sigmoid_f32(v) : 1.f) : 0.f;
+            u4[i] = s4[i] * x4[i];
+            g4[i] = in ? (a.z ? dy * z * sg : dy) : 0.f;
+            dz4[i] = in ? dy * sg * __builtin_fmaf(z, 1.f - sg, 1.f) : 0.f;
         }
         store4(t_s + piece(lane, wave), s4);
         store4(t_u + piece(lane, wave), u4);
         store4(t_g + piece(lane, wave), g4);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const bool in = tc + tid / 16 < len && nb * 16 + (tid & 15) < N;
+            t_B[nb][tid] = in ? to_f32(Br[nb]) : 0.f;
+            t_C[nb][tid] = in ? to_f32(Cr[nb]) : 0.f;
+        }
+        // a chunk's start: what the segment added so far, and the rest of its own start
+#pragma unroll
+        for (int k = 0; k < SLOTS; ++k) {
+            const int i = k * 256 + tid, nb = i / (CH * 16), at = i % (CH * 16);
+            l_h[nb][at] = c > 0 ? __builtin_fmaf(fast_exp2(l_A[nb][at] * LOG2E * sr[k]), h_seg[k], hr[k]) : h_seg[k];
+        }
         __syncthreads();
+        if (c > 0) fetch(c - 1);
 
+#pragma unroll 1
         for (int nb = 0; nb < NB; ++nb) {
             float Bv[CHUNK], Cv[CHUNK], accB[CHUNK] = {}, accC[CHUNK] = {};
-            load_rows(Bv, a.Bm, tc, nb);
-            load_rows(Cv, a.Cm, tc, nb);
+#pragma unroll
+            for (int t = 0; t < CHUNK; ++t) {
+                Bv[t] = t_B[nb][t * 16 + n];
+                Cv[t] = t_C[nb][t * 16 + n];
+            }
 #pragma unroll 1
             for (int q = 0; q < QUADS; ++q) {
                 const int cc = wave * 16 + q * 4 + ch4, at = cc * 16 + n, tok = token_at(cc, n);
                 const float A = l_A[nb][at], A2 = A * LOG2E;
                 const float sv = t_s[tok], uv = t_u[tok], gv = t_g[tok];
-                float h = start[c][nb][at], g = l_g[nb][at], dA = l_dA[nb][at];
+                float h = l_h[nb][at], g = l_g[nb][at], dA = l_dA[nb][at];
                 float e[CHUNK], hp[CHUNK], v[CHUNK], v2[CHUNK];
                 each_token([&](auto tt) {
                     constexpr int t = decltype(tt)::value;
@@ -370,23 +419,23 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
                     hp[t] = h;
                     h = __builtin_fmaf(e[t], h, row_bcast<t>(uv) * Bv[t]);
                     v[t] = h * Cv[t];
-                    accC[t] = __builtin_fmaf(row_bcast<t>(gv), h, accC[t]);
+                    fma_bcast<t>(accC[t], gv, h);
                 });
                 float r = row_sum_tokens(v);
                 each_token_back([&](auto tt) {
                     constexpr int t = decltype(tt)::value;
-                    const float qt = __builtin_fmaf(row_bcast<t>(gv), Cv[t], g);
-                    accB[t] = __builtin_fmaf(row_bcast<t>(uv), qt, accB[t]);
-                    v[t] = qt * Bv[t];
-                    g = e[t] * qt;
+                    fma_bcast<t>(g, gv, Cv[t]);          // q_t
+                    fma_bcast<t>(accB[t], uv, g);
+                    v[t] = g * Bv[t];
+                    g *= e[t];                           // g_t
                     const float k = g * hp[t];
-                    dA = __builtin_fmaf(row_bcast<t>(sv), k, dA);
+                    fma_bcast<t>(dA, sv, k);
                     v2[t] = A * k;
                 });
                 float p1 = row_sum_tokens(v), p2 = row_sum_tokens(v2);
                 l_g[nb][at] = g;
                 l_dA[nb][at] = dA;
-                if (nb > 0) {
+                if (NB > 1 && nb > 0) {
                     r += t_r[tok];
                     p1 += t_p1[tok];
                     p2 += t_p2[tok];
@@ -397,7 +446,7 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
             }
             // sums over the quad's four channels, tokens dealt out over the rows:
             // row 0 dB of tokens 0..7, row 1 of 8..15, rows 2 and 3 dC
-            if (nb > 0) __syncthreads();   // the last block's sums have been read
+            if (NB > 1 && nb > 0) __syncthreads();   // the last block's sums have been read
             float k[CHUNK];
 #pragma unroll
             for (int t = 0; t < CHUNK; ++t) {
@@ -444,8 +493,8 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
                 if (a.dz) ((T *)a.dz)[o] = from_f32<T>(dz4[i] * __builtin_fmaf(skip, x4[i], r4[i]));
             }
         }
-        // the next chunk's staging writes only what this chunk no longer reads
-        // (t_s, t_u, t_g); its results wait behind the barrier after it
+        // the next chunk's staging writes only what no wavefront reads any more
+        // (t_s, t_u, t_g, t_B, t_C, l_h); its results wait behind the next barrier
     }
 
     __syncthreads();
@@ -478,11 +527,12 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_pass_kernel(const float *in,
 
 template <typename T, int NB> hipError_t run(const ScanBwdArgs &a, const Layout &w, hipStream_t s)
 {
-    const int seg = CHUNK * seg_chunks(NB);
     const int64_t blocks = (int64_t)a.B * w.nseg * a.G * w.tiles;
     const int64_t join = ((int64_t)a.B * a.D * w.np + 255) / 256;
     if (blocks >= ((int64_t)1 << 31) || join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    kda_scan_bwd_segment_kernel<T, NB><<<(unsigned)blocks, 64, 0, s>>>(a, (const T *)a.Bm, (const T *)a.Cm, w, seg);
+    const T *Bm = (const T *)a.Bm, *Cm = (const T *)a.Cm;
+    if (a.N == 16 * NB) kda_scan_bwd_segment_kernel<T, NB, true><<<(unsigned)blocks, 64, 0, s>>>(a, Bm, Cm, w);
+    else kda_scan_bwd_segment_kernel<T, NB, false><<<(unsigned)blocks, 64, 0, s>>>(a, Bm, Cm, w);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     kda_scan_bwd_join_kernel<<<(unsigned)join, 256, 0, s>>>(a, w);
