@@ -32,6 +32,25 @@ template <> struct Pack<float, 4> : Raw4<float> {
 };
 template <typename T> constexpr int WIDE = 16 / (int)sizeof(T);
 
+// A few rows of a token tensor behind a pointer that is the same for the whole
+// wavefront, accessed at a lane's byte offset plus a uniform one, both 32 bits:
+// buffer instructions take all three as they are, where a global access pays a
+// 64-bit vector addition each.  The row pointer must be rebuilt often enough
+// that the uniform offset stays below 2^31.
+template <typename T> struct Rows {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ explicit Rows(const T *p)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p), (short)0, (int)0xFFFFFFFF, 0x00020000)) {}
+    __device__ __forceinline__ T load(unsigned lane, unsigned uniform) const {
+        if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, lane, uniform, 0);
+        else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, lane, uniform, 0));
+    }
+    __device__ __forceinline__ void store(T v, unsigned lane, unsigned uniform) const {
+        if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(v, r, lane, uniform, 0);
+        else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, lane, uniform, 0);
+    }
+};
+
 // log(1 + e) for e in [0, 1]: 2 artanh(r) with r = e / (2 + e) <= 1/3, whose
 // series in r^2 <= 1/9 is cut after r^13 (the rest is below 2e-8 of the sum).
 // log2(1 + e) directly would lose the small e, where softplus itself is e.

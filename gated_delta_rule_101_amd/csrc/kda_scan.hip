@@ -89,24 +89,28 @@ __global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__res
     }
 
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
-    const int64_t base = (int64_t)b * a.T * D + d;
-    const T *xp = (const T *)a.x + base, *tp = (const T *)a.dt + base;
-    const T *zp = a.z ? (const T *)a.z + base : nullptr;
-    T *yp = (T *)a.y + base;
+    // Without a gate z reads x, unused: uniform selects below, no branches.
+    const bool gated = a.z != nullptr, soft = a.softplus;
+    const int64_t base = (int64_t)b * a.T * D;   // uniform; a lane adds its channel
+    const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *zb = (const T *)(gated ? a.z : a.x) + base;
+    T *yb = (T *)a.y + base;
     const int64_t rows = ((int64_t)b * a.T * a.G + g) * N;
     const T *Bp = Bm + rows, *Cp = Cm + rows;
     const int64_t row = (int64_t)a.G * N;
+    const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
 
     float sum = 0.f;
     if (t0 < te) {
         T xr[UNROLL], tr[UNROLL], zr[UNROLL];
         const auto fetch = [&](int t) {
+            const int tf = min(t, te - 1);   // past the end: the last token again, unused
+            const Rows<T> xs(xb + (int64_t)tf * D), ts(tb + (int64_t)tf * D), zs(zb + (int64_t)tf * D);
 #pragma unroll
             for (int i = 0; i < UNROLL; ++i) {
-                const int64_t o = (int64_t)min(t + i, te - 1) * D;
-                xr[i] = xp[o];
-                tr[i] = tp[o];
-                zr[i] = !STATES_ONLY && zp ? zp[o] : T(0);
+                const unsigned o = (unsigned)min(i, te - 1 - tf) * rb;
+                xr[i] = xs.load(dl, o);
+                tr[i] = ts.load(dl, o);
+                if (!STATES_ONLY) zr[i] = zs.load(dl, o);
             }
         };
         fetch(t0);
@@ -116,13 +120,15 @@ __global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__res
             for (int i = 0; i < UNROLL; ++i) {
                 x[i] = to_f32(xr[i]);
                 s[i] = to_f32(tr[i]) + bias;
-                z[i] = to_f32(zr[i]);
+                if (!STATES_ONLY) z[i] = to_f32(zr[i]);
             }
-            if (t + UNROLL < te) fetch(t + UNROLL);
+            fetch(t + UNROLL);
+            const Rows<T> ys(yb + (int64_t)t * D);
 #pragma unroll
             for (int i = 0; i < UNROLL; ++i) {
                 const int tt = min(t + i, te - 1);
-                if (a.softplus) s[i] = softplus_f32(s[i]);
+                const float sp = softplus_f32(s[i]);
+                s[i] = soft ? sp : s[i];
                 if (t + i >= te) s[i] = 0.f;   // behind the end: a token that changes nothing
                 sum += s[i];
                 const float u = s[i] * x[i];
@@ -139,9 +145,9 @@ __global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__res
                         y0 = __builtin_fmaf(Cv[n], h[n], y0);
                         y1 = __builtin_fmaf(Cv[n + 1], h[n + 1], y1);
                     }
-                    float y = __builtin_fmaf(skip, x[i], y0 + y1);
-                    if (zp) y *= z[i] * sigmoid_f32(z[i]);
-                    if (ok && t + i < te) yp[(int64_t)(t + i) * D] = from_f32<T>(y);
+                    const float gate = z[i] * sigmoid_f32(z[i]);
+                    const float y = __builtin_fmaf(skip, x[i], y0 + y1) * (gated ? gate : 1.f);
+                    if (ok && t + i < te) ys.store(from_f32<T>(y), dl, i * rb);
                 }
             }
         }
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__res
         for (int n = 0; n < NP; ++n) q[(int64_t)n * D] = h[n];
         sums[(int64_t)(seg + 1) * D] = sum;
     } else {
-        for (int t = max(t0, te); t < t1; ++t) yp[(int64_t)t * D] = from_f32<T>(0.f);
+        for (int t = max(t0, te); t < t1; ++t) Rows<T>(yb + (int64_t)t * D).store(from_f32<T>(0.f), dl, 0);
         if (a.h_final && seg == sg.count - 1)
 #pragma unroll
             for (int n = 0; n < NP; ++n)

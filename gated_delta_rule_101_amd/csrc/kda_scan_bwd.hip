@@ -109,63 +109,76 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
         P[n] = 1.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-    const int64_t base = (int64_t)b * a.T * D + d;
-    const T *xp = (const T *)a.x + base, *tp = (const T *)a.dt + base, *gp = (const T *)a.dy + base;
-    const T *zp = a.z ? (const T *)a.z + base : nullptr;
+    // Without a gate z reads x, unused: uniform selects below, no branches.
+    const bool gated = a.z != nullptr, soft = a.softplus;
+    const int64_t base = (int64_t)b * a.T * D;   // uniform; a lane adds its channel
+    const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *gb = (const T *)a.dy + base;
+    const T *zb = (const T *)(gated ? a.z : a.x) + base;
     const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N, row = (int64_t)a.G * N;
-    float sum = 0.f;
-    T xr[UNROLL], tr[UNROLL], gr[UNROLL], zr[UNROLL];
-    const auto fetch = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-            const int64_t o = (int64_t)min(t + i, te - 1) * D;
-            xr[i] = xp[o];
-            tr[i] = tp[o];
-            gr[i] = gp[o];
-            zr[i] = zp ? zp[o] : T(0);
-        }
-    };
-    if (t0 < te) fetch(t0);
-    for (int t = t0; t < t1; t += UNROLL) {
-        if (t % CHUNK == 0 && t > t0 && ok) {   // a segment's first chunk adds nothing
+    const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
+    const auto store_chunk = [&](int t, float s) {   // a segment's first chunk adds nothing
+        if (t % CHUNK == 0 && t > t0 && ok) {
             const int64_t at = ((int64_t)b * w.nchunk + t / CHUNK) * D + d;
 #pragma unroll
             for (int n = 0; n < NP; n += 4) {
                 const float v[4] = {h[n], h[n + 1], h[n + 2], h[n + 3]};
                 store4(w.hc + at * NP + n, v);
             }
-            w.sc[at] = sum;
+            w.sc[at] = s;
         }
-        if (t >= te) continue;
-        float x[UNROLL], s[UNROLL], gy[UNROLL], z[UNROLL];
+    };
+    float sum = 0.f;
+    int t = t0;
+    if (t0 < te) {
+        T xr[UNROLL], tr[UNROLL], gr[UNROLL], zr[UNROLL];
+        const auto fetch = [&](int t) {
+            const int tf = min(t, te - 1);   // past the end: the last token again, unused
+            const int64_t at = (int64_t)tf * D;
+            const Rows<T> xs(xb + at), ts(tb + at), gs(gb + at), zs(zb + at);
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-            x[i] = to_f32(xr[i]);
-            s[i] = to_f32(tr[i]) + bias;
-            gy[i] = to_f32(gr[i]);
-            z[i] = to_f32(zr[i]);
-        }
-        if (t + UNROLL < te) fetch(t + UNROLL);
+            for (int i = 0; i < UNROLL; ++i) {
+                const unsigned o = (unsigned)min(i, te - 1 - tf) * rb;
+                xr[i] = xs.load(dl, o);
+                tr[i] = ts.load(dl, o);
+                gr[i] = gs.load(dl, o);
+                zr[i] = zs.load(dl, o);
+            }
+        };
+        fetch(t0);
+        for (; t < te; t += UNROLL) {
+            store_chunk(t, sum);
+            float x[UNROLL], s[UNROLL], gy[UNROLL], z[UNROLL];
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-            const int64_t tt = row0 + (int64_t)min(t + i, te - 1) * row;
-            if (a.softplus) s[i] = softplus_f32(s[i]);
-            if (zp) gy[i] *= z[i] * sigmoid_f32(z[i]);
-            if (t + i >= te) s[i] = gy[i] = 0.f;   // behind the end: a token that changes nothing
-            sum += s[i];
-            const float u = s[i] * x[i];
-            float Bv[NP], Cv[NP];
-            load_row_uniform<T, NP, FULL>(Bv, Bm + tt, N);
-            load_row_uniform<T, NP, FULL>(Cv, Cm + tt, N);
+            for (int i = 0; i < UNROLL; ++i) {
+                x[i] = to_f32(xr[i]);
+                s[i] = to_f32(tr[i]) + bias;
+                gy[i] = to_f32(gr[i]);
+                z[i] = to_f32(zr[i]);
+            }
+            fetch(t + UNROLL);
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                const float e = fast_exp2(s[i] * A2[n]);
-                h[n] = __builtin_fmaf(e, h[n], u * Bv[n]);
-                P[n] *= e;
-                r[n] = __builtin_fmaf(P[n], gy[i] * Cv[n], r[n]);
+            for (int i = 0; i < UNROLL; ++i) {
+                const int64_t tt = row0 + (int64_t)min(t + i, te - 1) * row;
+                const float sp = softplus_f32(s[i]), gate = z[i] * sigmoid_f32(z[i]);
+                s[i] = soft ? sp : s[i];
+                gy[i] *= gated ? gate : 1.f;
+                if (t + i >= te) s[i] = gy[i] = 0.f;   // behind the end: a token that changes nothing
+                sum += s[i];
+                const float u = s[i] * x[i];
+                float Bv[NP], Cv[NP];
+                load_row_uniform<T, NP, FULL>(Bv, Bm + tt, N);
+                load_row_uniform<T, NP, FULL>(Cv, Cm + tt, N);
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    const float e = fast_exp2(s[i] * A2[n]);
+                    h[n] = __builtin_fmaf(e, h[n], u * Bv[n]);
+                    P[n] *= e;
+                    r[n] = __builtin_fmaf(P[n], gy[i] * Cv[n], r[n]);
+                }
             }
         }
     }
+    for (; t < t1; t += UNROLL) store_chunk(t, sum);
     if (!ok) return;
     const int64_t at = (((int64_t)b * w.nseg + seg) * D + d);
 #pragma unroll
@@ -288,7 +301,7 @@ __device__ __forceinline__ int piece(int ch, int p) { return ch * 16 + 4 * (p ^ 
 __device__ __forceinline__ int token_at(int ch, int t) { return piece(ch, t >> 2) + (t & 3); }
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout w)
+__global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(ScanBwdArgs a, Layout w)
 {
     static_assert(QUADS == 4 && WAVES * QUADS * 4 == CH, "a wavefront's channels");
     static_assert(CHUNK == 16, "a token per lane of a DPP row");
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
     __shared__ float l_A[NB][CH * 16], l_g[NB][CH * 16], l_dA[NB][CH * 16]; // [channel][16 states]
     __shared__ float flush[WAVES][8][64];                                   // dB, dC of a chunk, per wavefront
 
-    const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid & 63;
     const int ch4 = lane / 16, n = lane & 15;             // compute: channel of the quad, state or token
     unsigned id = blockIdx.x;
     const int tile = id % w.tiles;
@@ -317,16 +330,23 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
     const bool ok = tile * CH + lane < Dg;
     const int d = grp * Dg + (ok ? tile * CH + lane : Dg - 1);
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
-    const int64_t base = (int64_t)b * a.T * D + d;
+    const bool gated = a.z != nullptr, soft = a.softplus;   // without a gate z reads x, unused
+    const int64_t base = (int64_t)b * a.T * D;              // uniform; a lane adds its channel
+    const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *gb = (const T *)a.dy + base;
+    const T *zb = (const T *)(gated ? a.z : a.x) + base;
+    T *dxb = (T *)a.dx + base, *dtb = (T *)a.ddt + base, *dzb = (T *)a.dz + base;
+    const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
     const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N, row = (int64_t)a.G * N;
 
     // h_start[i]: state in front of the segment, for the staging of l_h
     constexpr int SLOTS = NB * CH * 16 / 256;
     float h_seg[SLOTS];
+    unsigned chan[SLOTS];                                   // channels of the slots
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
         const int i = k * 256 + tid, nb = i / (CH * 16), c = i / 16 % CH, st = nb * 16 + (i & 15);
         const int dd = grp * Dg + min(tile * CH + c, Dg - 1);
+        chan[k] = dd;
         const int64_t at = (bseg * D + dd) * w.np + st;
         l_A[nb][i % (CH * 16)] = st < N ? a.A[(int64_t)dd * N + st] : 0.f;
         h_seg[k] = w.h[at];
@@ -339,28 +359,33 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
     float hr[SLOTS], sr[SLOTS];
     const auto fetch = [&](int c) {
         const int tc = t0 + c * CHUNK;
+        const int tf = max(min(tc + 4 * wave, len - 1), 0);   // past the end: the last token, masked later
+        const int64_t rf = (int64_t)tf * D;
+        const Rows<T> xs(xb + rf), ts(tb + rf), gs(gb + rf), zs(zb + rf);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t o = base + (int64_t)max(min(tc + 4 * wave + i, len - 1), 0) * D;
-            xr[i] = ((const T *)a.x)[o];
-            tr[i] = ((const T *)a.dt)[o];
-            gr[i] = ((const T *)a.dy)[o];
-            zr[i] = a.z ? ((const T *)a.z)[o] : T(0);
+            const unsigned o = (unsigned)max(min(i, len - 1 - tf), 0) * rb;
+            xr[i] = xs.load(dl, o);
+            tr[i] = ts.load(dl, o);
+            gr[i] = gs.load(dl, o);
+            zr[i] = zs.load(dl, o);
         }
+        const int64_t o = row0 + (int64_t)max(min(tc + tid / 16, len - 1), 0) * row;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int64_t o = row0 + (int64_t)max(min(tc + tid / 16, len - 1), 0) * row + min(nb * 16 + (tid & 15), N - 1);
-            Br[nb] = ((const T *)a.Bm)[o];
-            Cr[nb] = ((const T *)a.Cm)[o];
+            const int st = min(nb * 16 + (tid & 15), N - 1);
+            Br[nb] = ((const T *)a.Bm)[o + st];
+            Cr[nb] = ((const T *)a.Cm)[o + st];
         }
-        if (c > 0)
+        // (the segment's first chunk has nothing in front of it: its values go unused)
+        const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D;
+        const float *hp = w.hc + at * (16 * NB), *sp = w.sc + at;
 #pragma unroll
-            for (int k = 0; k < SLOTS; ++k) {
-                const int i = k * 256 + tid, nb = i / (CH * 16), cc = i / 16 % CH, st = nb * 16 + (i & 15);
-                const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D + grp * Dg + min(tile * CH + cc, Dg - 1);
-                hr[k] = w.hc[at * w.np + st];
-                sr[k] = w.sc[at];
-            }
+        for (int k = 0; k < SLOTS; ++k) {
+            const unsigned st = (k * 256 + tid) / (CH * 16) * 16 + (tid & 15);
+            hr[k] = (hp + st)[(size_t)chan[k] * (16 * NB)];
+            sr[k] = sp[chan[k]];
+        }
     };
     fetch(nch - 1);
 
@@ -371,14 +396,14 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool in = ok && tc + 4 * wave + i < len;   // idle lanes stay zero: their channel is another's
-            const float v = to_f32(tr[i]) + bias, dy = to_f32(gr[i]), z = to_f32(zr[i]);
-            const float sg = sigmoid_f32(z);
+            const float v = to_f32(tr[i]) + bias, dy = in ? to_f32(gr[i]) : 0.f, z = in ? to_f32(zr[i]) : 0.f;
+            const float sg = sigmoid_f32(z), sp = softplus_f32(v), sv = sigmoid_f32(v);
             x4[i] = in ? to_f32(xr[i]) : 0.f;
-            s4[i] = in ? (a.softplus ? softplus_f32(v) : v) : 0.f;
-            ds4[i] = in ? (a.softplus ? sigmoid_f32(v) : 1.f) : 0.f;
+            s4[i] = in ? (soft ? sp : v) : 0.f;
+            ds4[i] = in ? (soft ? sv : 1.f) : 0.f;
             u4[i] = s4[i] * x4[i];
-            g4[i] = in ? (a.z ? dy * z * sg : dy) : 0.f;
-            dz4[i] = in ? dy * sg * __builtin_fmaf(z, 1.f - sg, 1.f) : 0.f;
+            g4[i] = dy * (gated ? z * sg : 1.f);
+            dz4[i] = dy * (sg * __builtin_fmaf(z, 1.f - sg, 1.f));
         }
         store4(t_s + piece(lane, wave), s4);
         store4(t_u + piece(lane, wave), u4);
@@ -396,7 +421,7 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
             l_h[nb][at] = c > 0 ? __builtin_fmaf(fast_exp2(l_A[nb][at] * LOG2E * sr[k]), h_seg[k], hr[k]) : h_seg[k];
         }
         __syncthreads();
-        if (c > 0) fetch(c - 1);
+        fetch(max(c - 1, 0));
 
 #pragma unroll 1
         for (int nb = 0; nb < NB; ++nb) {
@@ -480,17 +505,17 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_kernel(ScanBwdArgs a, Layout
         f.to_f32(p1);
         f.load(t_p2 + piece(lane, wave));
         f.to_f32(p2);
+        const int64_t rw = (int64_t)(tc + 4 * wave) * D;
+        const Rows<T> dxs(dxb + rw), dts(dtb + rw), dzs(dzb + rw);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = tc + 4 * wave + i;
             const float ddt = __builtin_fmaf(x4[i], p1[i], p2[i]) * ds4[i];
             dD = __builtin_fmaf(g4[i], x4[i], dD);
             db += ddt;
-            if (ok && t < t1) {
-                const int64_t o = base + (int64_t)t * D;
-                ((T *)a.dx)[o] = from_f32<T>(__builtin_fmaf(s4[i], p1[i], skip * g4[i]));
-                ((T *)a.ddt)[o] = from_f32<T>(ddt);
-                if (a.dz) ((T *)a.dz)[o] = from_f32<T>(dz4[i] * __builtin_fmaf(skip, x4[i], r4[i]));
+            if (ok && tc + 4 * wave + i < t1) {
+                dxs.store(from_f32<T>(__builtin_fmaf(s4[i], p1[i], skip * g4[i])), dl, i * rb);
+                dts.store(from_f32<T>(ddt), dl, i * rb);
+                if (gated) dzs.store(from_f32<T>(dz4[i] * __builtin_fmaf(skip, x4[i], r4[i])), dl, i * rb);
             }
         }
         // the next chunk's staging writes only what no wavefront reads any more
