@@ -167,6 +167,168 @@ __global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__res
     }
 }
 
+// One chain per channel with four lanes to it (N <= 16): lane j of a quad owns
+// states 4 j .. 4 j + 3, so there are four times the wavefronts of the kernel
+// above and a token costs each a quarter of the states.  What a channel's token
+// costs once (softplus, gate, conversions) is dealt out over the quad: lane j
+// takes every fourth token and hands its s and u to the others by DPP quad
+// broadcasts, and the partial sums of four tokens' outputs meet so that lane j
+// keeps token j's.  B and C rows go through LDS as float32, CHUNK tokens at a
+// time, read as one 16-byte broadcast per token and row.
+constexpr int CHUNK = 16;
+
+template <int K> struct Const { static constexpr int value = K; };
+template <int K> __device__ __forceinline__ float quad_bcast(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), K * 0x55, 0xF, 0xF, true));
+}
+template <int CTRL> __device__ __forceinline__ float quad_add(float x)
+{
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+
+template <typename F> __device__ __forceinline__ void each4(F f)
+{
+    f(Const<0>{});
+    f(Const<1>{});
+    f(Const<2>{});
+    f(Const<3>{});
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) kda_scan_quad_kernel(ScanArgs a, int tiles)
+{
+    __shared__ __attribute__((aligned(16))) float rows[2][2][CHUNK * 16];   // [buffer][B, C][token][state]
+    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * j;
+    unsigned id = blockIdx.x;
+    const int tile = id % tiles;
+    id /= tiles;
+    const int g = id % a.G, b = id / a.G;
+    const int D = a.D, N = a.N, Dg = D / a.G;
+    const int c = tile * 64 + tid / 4;
+    const bool ok = c < Dg;
+    const int d = g * Dg + (ok ? c : Dg - 1);   // idle quads repeat the last channel
+    const int te = seq_length(a.lengths, b, a.T);
+
+    float A2[4], h[4];
+    const int64_t at_state = ((int64_t)b * D + d) * N + n0;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        A2[n] = n0 + n < N ? a.A[(int64_t)d * N + n0 + n] * LOG2E : 0.f;
+        h[n] = a.h0 && n0 + n < N ? a.h0[at_state + n] : 0.f;
+    }
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
+    const bool gated = a.z != nullptr, soft = a.softplus;   // without a gate z reads x, unused
+    const int64_t base = (int64_t)b * a.T * D;
+    const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *zb = (const T *)(gated ? a.z : a.x) + base;
+    T *yb = (T *)a.y + base;
+    const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
+    const int64_t row = (int64_t)a.G * N, row0 = ((int64_t)b * a.T * a.G + g) * N;
+    const int rt = tid / 16, rn = tid & 15;   // staging of B and C: token, state
+
+    if (te > 0) {
+        T xr[4], tr[4], zr[4], Br, Cr;
+        const auto fetch = [&](int tc) {      // tokens past the end: the last one again, masked later
+            const int tf = min(tc, te - 1);
+            const int64_t at = (int64_t)tf * D;
+            const Rows<T> xs(xb + at), ts(tb + at), zs(zb + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const unsigned o = (unsigned)min(4 * i + j, te - 1 - tf) * rb + dl;
+                xr[i] = xs.load(o, 0);
+                tr[i] = ts.load(o, 0);
+                zr[i] = zs.load(o, 0);
+            }
+            const int64_t o = row0 + (int64_t)min(tc + rt, te - 1) * row + min(rn, N - 1);
+            Br = ((const T *)a.Bm)[o];
+            Cr = ((const T *)a.Cm)[o];
+        };
+        fetch(0);
+        for (int tc = 0; tc < te; tc += CHUNK) {
+            float (&Bs)[CHUNK * 16] = rows[(tc / CHUNK) & 1][0], (&Cs)[CHUNK * 16] = rows[(tc / CHUNK) & 1][1];
+            Bs[tid] = rn < N ? to_f32(Br) : 0.f;
+            Cs[tid] = rn < N ? to_f32(Cr) : 0.f;
+            float x[4], s[4], z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = to_f32(xr[i]);
+                s[i] = to_f32(tr[i]) + bias;
+                z[i] = to_f32(zr[i]);
+            }
+            // one barrier a chunk: the buffer written next was last read a chunk earlier
+            lds_barrier();
+            fetch(tc + CHUNK);
+            float u[4], r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float sp = softplus_f32(s[i]);
+                s[i] = tc + 4 * i + j < te ? (soft ? sp : s[i]) : 0.f;
+                u[i] = s[i] * x[i];
+            }
+            // Four tokens at a time: all their rows and decays first, then the
+            // chain.  Few wavefronts share a SIMD here, so the order has to give
+            // each instruction independent neighbours; the barriers keep it.
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float4 Bv[4], Cv[4];
+                float e[4][4], y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) Bv[k] = *reinterpret_cast<const float4 *>(Bs + (4 * i + k) * 16 + n0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) Cv[k] = *reinterpret_cast<const float4 *>(Cs + (4 * i + k) * 16 + n0);
+                each4([&](auto k) {
+                    constexpr int K = decltype(k)::value;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) e[K][n] = quad_bcast<K>(s[i]) * A2[n];
+                });
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) e[k][n] = fast_exp2(e[k][n]);
+                __builtin_amdgcn_sched_barrier(0);
+                each4([&](auto k) {
+                    constexpr int K = decltype(k)::value;
+                    const float ub[4] = {quad_bcast<K>(u[i]) * Bv[K].x, quad_bcast<K>(u[i]) * Bv[K].y,
+                                         quad_bcast<K>(u[i]) * Bv[K].z, quad_bcast<K>(u[i]) * Bv[K].w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) e[K][n] = h[n] = __builtin_fmaf(e[K][n], h[n], ub[n]);
+                });
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = Cv[k].x * e[k][0];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].y, e[k][1], y[k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].z, e[k][2], y[k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].w, e[k][3], y[k]);
+                // lanes with bit 1 keep tokens 2, 3, then lanes with bit 0 the odd one
+                // (every lane takes part in both sums before it chooses)
+                constexpr int SWAP2 = 0x4E, SWAP1 = 0xB1;   // quad_perm [2,3,0,1], [1,0,3,2]
+                const float a0 = quad_add<SWAP2>(y[0]), a1 = quad_add<SWAP2>(y[1]);
+                const float a2 = quad_add<SWAP2>(y[2]), a3 = quad_add<SWAP2>(y[3]);
+                const float p0 = j & 2 ? a2 : a0, p1 = j & 2 ? a3 : a1;
+                const float q0 = quad_add<SWAP1>(p0), q1 = quad_add<SWAP1>(p1);
+                r[i] = j & 1 ? q1 : q0;
+            }
+            const Rows<T> ys(yb + (int64_t)tc * D);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float gate = z[i] * sigmoid_f32(z[i]);
+                r[i] = __builtin_fmaf(skip, x[i], r[i]) * (gated ? gate : 1.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (ok && tc + 4 * i + j < te) ys.store(from_f32<T>(r[i]), (unsigned)(4 * i + j) * rb + dl, 0);
+        }
+    }
+    if (!ok) return;
+    for (int t = te + j; t < a.T; t += 4) yb[(int64_t)t * D + d] = from_f32<T>(0.f);
+    if (a.h_final)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            if (n0 + n < N) a.h_final[at_state + n] = h[n];
+}
+
 // One token: LPC lanes a channel, 4 states each, so a wavefront's states are
 // contiguous 16-byte accesses; the read and write of the states bound it.
 template <typename T, int LPC, bool VEC>
@@ -256,10 +418,23 @@ Segments plan(int B, int T, int D, int G)
     return s;
 }
 
+// Where the quad kernel's wavefronts (four a 64-channel tile)
+bool quads(int B, int T, int D, int N, int G)
+{
+    if (N > 16) return false;
+    return T <= 512 || (int64_t)B * G * channel_tiles(D, G) * 4 >= 512;
+}
+
 template <typename T, int NB, bool FULL>
 hipError_t fwd_launch(const ScanArgs &a, hipStream_t stream)
 {
     const int tiles = channel_tiles(a.D, a.G);
+    if (NB == 1 && quads(a.B, a.T, a.D, a.N, a.G)) {
+        const int64_t blocks = (int64_t)a.B * a.G * tiles;
+        if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+        kda_scan_quad_kernel<T><<<(unsigned)blocks, 256, 0, stream>>>(a, tiles);
+        return hipGetLastError();
+    }
     Segments s = plan(a.B, a.T, a.D, a.G);
     if (!a.ws || s.count == 1) {
         s.count = 1;
