@@ -75,6 +75,7 @@ kda_status_t check_scan(int B, int T, int D, int N, int G, kda_dtype_t dtype)
     if (N <= 0 || G <= 0 || D % G || !valid_dtype(dtype)) return KDA_ERR_INVALID_ARG;
     if (N > 64) return KDA_ERR_UNSUPPORTED;
     // the states' elements and the rows of B and C stay countable as well
+    if ((int64_t)G * N >= MAX_DIM) return KDA_ERR_UNSUPPORTED;
     if (D > 0 && (int64_t)B >= MAX_COUNT / ((int64_t)D * N)) return KDA_ERR_UNSUPPORTED;
     if ((int64_t)B * (T > 0 ? T : 1) >= MAX_COUNT / ((int64_t)G * N)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;

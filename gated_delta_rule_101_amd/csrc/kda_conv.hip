@@ -12,6 +12,8 @@
 #include "kda_block.h"
 #include "kda_block_device.h"
 
+#include <algorithm>
+
 namespace kda {
 namespace {
 
@@ -337,8 +339,8 @@ hipError_t by_width(int W, F2 f2, F3 f3, F4 f4)
 
 int64_t conv_bwd_workspace_floats(int B, int T, int D, int W)
 {
-    const int64_t runs = max(max(bwd_runs(B, T, D, 1), D % 4 == 0 ? bwd_runs(B, T, D, 4) : 0),
-                             D % 8 == 0 ? bwd_runs(B, T, D, 8) : 0);
+    const int64_t runs = std::max(bwd_runs(B, T, D, 1), std::max(D % 4 == 0 ? bwd_runs(B, T, D, 4) : (int64_t)0,
+                                                                 D % 8 == 0 ? bwd_runs(B, T, D, 8) : (int64_t)0));
     return (int64_t)B * runs * D * (W + 1);
 }
 

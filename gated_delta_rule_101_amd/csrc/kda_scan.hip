@@ -21,6 +21,8 @@
 #include "kda_block.h"
 #include "kda_block_device.h"
 
+#include <algorithm>
+
 namespace kda {
 namespace {
 
@@ -77,14 +79,22 @@ __global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__res
     } else {
 #pragma unroll
         for (int n = 0; n < NP; ++n) h[n] = slots[((int64_t)NP + n) * D];
-        for (int j = 2; j <= seg; ++j) {
-            const float *q = slots + (int64_t)j * NP * D;
-            const float s = sums[(int64_t)j * D];
-            float v[NP];
+        // a few segments' loads together: the chain itself is one multiply-add each
+        constexpr int JOIN = 4 / NB;
+        for (int j = 2; j <= seg; j += JOIN) {
+            float v[JOIN][NP], s[JOIN];
 #pragma unroll
-            for (int n = 0; n < NP; ++n) v[n] = q[(int64_t)n * D];
+            for (int i = 0; i < JOIN; ++i) {
+                const int q = min(j + i, seg);
+                s[i] = sums[(int64_t)q * D];
 #pragma unroll
-            for (int n = 0; n < NP; ++n) h[n] = __builtin_fmaf(fast_exp2(A2[n] * s), h[n], v[n]);
+                for (int n = 0; n < NP; ++n) v[i][n] = slots[((int64_t)q * NP + n) * D];
+            }
+#pragma unroll
+            for (int i = 0; i < JOIN; ++i)
+                if (j + i <= seg)
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) h[n] = __builtin_fmaf(fast_exp2(A2[n] * s[i]), h[n], v[i][n]);
         }
     }
 
@@ -114,6 +124,9 @@ __global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__res
             }
         };
         fetch(t0);
+        UniformRow<T, NP, FULL> Br, Cr;
+        Br.request(Bp + t0 * row, N);
+        if (!STATES_ONLY) Cr.request(Cp + t0 * row, N);
         for (int t = t0; t < te; t += UNROLL) {
             float x[UNROLL], s[UNROLL], z[UNROLL];
 #pragma unroll
@@ -126,20 +139,25 @@ __global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__res
             const Rows<T> ys(yb + (int64_t)t * D);
 #pragma unroll
             for (int i = 0; i < UNROLL; ++i) {
-                const int tt = min(t + i, te - 1);
+                const int64_t next = min(t + i + 1, te - 1) * row;
+                float Bv[NP], Cv[NP];
+                Br.take(Bv);
+                Br.arrived();
+                if constexpr (!STATES_ONLY) Cr.take(Cv);
+                scalar_fence();
+                Br.request(Bp + next, N);
+                if constexpr (!STATES_ONLY) Cr.request(Cp + next, N);
+                scalar_fence();
                 const float sp = softplus_f32(s[i]);
                 s[i] = soft ? sp : s[i];
                 if (t + i >= te) s[i] = 0.f;   // behind the end: a token that changes nothing
                 sum += s[i];
                 const float u = s[i] * x[i];
-                float Bv[NP];
-                load_row_uniform<T, NP, FULL>(Bv, Bp + tt * row, N);
 #pragma unroll
                 for (int n = 0; n < NP; ++n)
                     h[n] = __builtin_fmaf(fast_exp2(s[i] * A2[n]), h[n], u * Bv[n]);
                 if constexpr (!STATES_ONLY) {
-                    float Cv[NP], y0 = 0.f, y1 = 0.f;
-                    load_row_uniform<T, NP, FULL>(Cv, Cp + tt * row, N);
+                    float y0 = 0.f, y1 = 0.f;
 #pragma unroll
                     for (int n = 0; n < NP; n += 2) {
                         y0 = __builtin_fmaf(Cv[n], h[n], y0);
@@ -335,8 +353,8 @@ template <typename T, int LPC, bool VEC>
 __global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int64_t channels)
 {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t c = min(id / LPC, channels - 1);   // idle groups repeat the last channel
     const bool ok = id / LPC < channels;
+    const int64_t c = ok ? id / LPC : channels - 1;   // idle groups repeat the last channel
     const int l = id % LPC, D = a.D, N = a.N, n0 = 4 * l;
     const int b = (int)(c / D), d = (int)(c % D), g = d / (D / a.G);
     float *hp = a.h_final + c * N;
@@ -403,40 +421,49 @@ int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // NB
 int channel_tiles(int D, int G) { return (D / G + 63) / 64; }
 
 // Segments: as many as bring the wavefronts to four a SIMD (4096), at least
-// 16 tokens each and at most 64 of them (every segment reads the end states
-// of those in front of it).
+// 32 tokens each (16 take 84 us instead of 64 at B1 T1024 D4096) and at most 64
+// of them (every segment reads the end states of those in front of it).
 Segments plan(int B, int T, int D, int G)
 {
     const int64_t waves = (int64_t)B * G * channel_tiles(D, G);
     int64_t n = (4096 + waves - 1) / waves;
-    n = min(n, min((int64_t)64, (int64_t)(T / 16)));
+    n = std::min(n, std::min((int64_t)64, (int64_t)(T / 32)));
     Segments s{};
-    s.count = (int)max(n, (int64_t)1);
+    s.count = (int)std::max(n, (int64_t)1);
     s.tokens = (T + s.count - 1) / s.count;
     if (s.count > 1) s.tokens = (s.tokens + UNROLL - 1) / UNROLL * UNROLL;
     s.count = s.tokens > 0 ? (T + s.tokens - 1) / s.tokens : 1;
     return s;
 }
 
-// Where the quad kernel's wavefronts (four a 64-channel tile)
+// Whether four lanes a channel in one chain beat segments.  From timings on
+// MI355X at N = 16, bfloat16: the chain takes 0.104 us a token while its
+// wavefronts (4 a 64-channel tile) have a SIMD each and 0.03 + 0.067 us per
+// wavefront on a SIMD beyond; the two passes over segments about 14 us plus 0.5
+// us per token and 1024 tiles.  (B1 T64 D4096: 19 against 22 us; B1 T256 D4096:
+// 30 against 28; B2 T2048 D4096: 211 against 149; B3: 212 against 212; B4: 215
+// against 249; B8: 333 against 462.)
 bool quads(int B, int T, int D, int N, int G)
 {
     if (N > 16) return false;
-    return T <= 512 || (int64_t)B * G * channel_tiles(D, G) * 4 >= 512;
+    const double tiles = (double)B * G * channel_tiles(D, G) / 1024.0;
+    const double chain = T * std::max(0.104, 0.03 + 0.067 * 4.0 * tiles);
+    return chain <= 14.0 + 0.5 * T * tiles;
 }
 
 template <typename T, int NB, bool FULL>
 hipError_t fwd_launch(const ScanArgs &a, hipStream_t stream)
 {
     const int tiles = channel_tiles(a.D, a.G);
-    if (NB == 1 && quads(a.B, a.T, a.D, a.N, a.G)) {
+    Segments s = plan(a.B, a.T, a.D, a.G);
+    const bool cut = a.ws && s.count > 1;
+    if (NB == 1 && (!cut || quads(a.B, a.T, a.D, a.N, a.G))) {
         const int64_t blocks = (int64_t)a.B * a.G * tiles;
         if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
         kda_scan_quad_kernel<T><<<(unsigned)blocks, 256, 0, stream>>>(a, tiles);
         return hipGetLastError();
     }
-    Segments s = plan(a.B, a.T, a.D, a.G);
-    if (!a.ws || s.count == 1) {
+    if (!cut) {
         s.count = 1;
         s.tokens = a.T;
     }
@@ -487,7 +514,7 @@ template <typename T> hipError_t step_dispatch(const ScanArgs &a, hipStream_t s)
 int64_t scan_fwd_workspace_floats(int B, int T, int D, int N, int G)
 {
     const Segments s = plan(B, T, D, G);
-    return s.count > 1 ? (int64_t)B * s.count * D * (16 * state_blocks(N) + 1) : 0;
+    return s.count > 1 && !quads(B, T, D, N, G) ? (int64_t)B * s.count * D * (16 * state_blocks(N) + 1) : 0;
 }
 
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t s)

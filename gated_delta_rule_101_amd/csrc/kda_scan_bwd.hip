@@ -11,7 +11,7 @@
 //   dA = sum_t s_t g_t h_{t-1}        dD = sum gy x,   dz = dy (r + D x) silu'(z)
 //
 // Four kernels.
-//  1. Segments of SEG tokens side by side, a lane a channel as in the forward:
+//  1. Segments of 32 to 128 tokens side by side, a lane a channel as in the forward:
 //     the states it adds (from zero), stored at every chunk of 16 tokens, and,
 //     with the running decay P_t = prod a, the gradient it adds in front of
 //     itself, sum_t P_t C_t gy_t.  Both directions share each exp.
@@ -40,14 +40,14 @@ constexpr int CHUNK = 16;        // tokens a chunk: one per lane of a DPP row
 constexpr int CH = 64;           // channels a workgroup
 constexpr int WAVES = 4, QUADS = CH / WAVES / 4;
 
-constexpr int SEG_CHUNKS = 8, SEG = CHUNK * SEG_CHUNKS;
 constexpr int UNROLL = 4;        // tokens whose inputs are loaded together
 
 int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // of 16
 
 // Workspace, in floats.
 struct Layout {
-    int nseg, nchunk, tiles, np;     // segments, chunks, 64-channel tiles a group, padded states
+    int seg, nseg, nchunk;           // tokens a segment; segments, chunks
+    int tiles, np;                   // 64-channel tiles a group, padded states
     float *h, *g, *sum;              // [B][nseg][D][np] states in front / gradients behind; [B][nseg][D]
     float *hc, *sc;                  // [B][nchunk][D][np] states a segment adds up to a chunk; [B][nchunk][D]
     float *dA, *dD, *db;             // [B nseg][D][N], [B nseg][D] twice
@@ -57,9 +57,13 @@ struct Layout {
 Layout layout(float *p, int B, int T, int D, int N, int G)
 {
     Layout w;
-    w.nseg = (T + SEG - 1) / SEG;
-    w.nchunk = (T + CHUNK - 1) / CHUNK;
     w.tiles = (D / G + CH - 1) / CH;
+    // Segments of 128 tokens, of 64 or 32 where there would be under 2048 of
+    // them (two workgroups a compute unit, several rounds).
+    w.seg = 128;
+    while (w.seg > 32 && (int64_t)B * ((T + w.seg - 1) / w.seg) * G * w.tiles < 2048) w.seg /= 2;
+    w.nseg = (T + w.seg - 1) / w.seg;
+    w.nchunk = (T + CHUNK - 1) / CHUNK;
     w.np = 16 * state_blocks(N);
     const auto r4 = [](int64_t n) { return (n + 3) / 4 * 4; };   // 16-byte aligned parts
     const int64_t bs = (int64_t)B * w.nseg;
@@ -99,7 +103,7 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
     const bool ok = c < Dg;
     const int d = grp * Dg + (ok ? c : Dg - 1);
     const int len = seq_length(a.lengths, b, a.T);
-    const int t0 = seg * SEG, t1 = min(t0 + SEG, a.T), te = min(t1, len);
+    const int t0 = seg * w.seg, t1 = min(t0 + w.seg, a.T), te = min(t1, len);
 
     float A2[NP], h[NP], r[NP], P[NP];
 #pragma unroll
@@ -145,6 +149,9 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
             }
         };
         fetch(t0);
+        UniformRow<T, NP, FULL> Br, Cr;
+        Br.request(Bm + row0 + t0 * row, N);
+        Cr.request(Cm + row0 + t0 * row, N);
         for (; t < te; t += UNROLL) {
             store_chunk(t, sum);
             float x[UNROLL], s[UNROLL], gy[UNROLL], z[UNROLL];
@@ -158,16 +165,21 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
             fetch(t + UNROLL);
 #pragma unroll
             for (int i = 0; i < UNROLL; ++i) {
-                const int64_t tt = row0 + (int64_t)min(t + i, te - 1) * row;
+                const int64_t next = row0 + min(t + i + 1, te - 1) * row;
+                float Bv[NP], Cv[NP];
+                Br.take(Bv);
+                Br.arrived();
+                Cr.take(Cv);
+                scalar_fence();
+                Br.request(Bm + next, N);
+                Cr.request(Cm + next, N);
+                scalar_fence();
                 const float sp = softplus_f32(s[i]), gate = z[i] * sigmoid_f32(z[i]);
                 s[i] = soft ? sp : s[i];
                 gy[i] *= gated ? gate : 1.f;
                 if (t + i >= te) s[i] = gy[i] = 0.f;   // behind the end: a token that changes nothing
                 sum += s[i];
                 const float u = s[i] * x[i];
-                float Bv[NP], Cv[NP];
-                load_row_uniform<T, NP, FULL>(Bv, Bm + tt, N);
-                load_row_uniform<T, NP, FULL>(Cv, Cm + tt, N);
 #pragma unroll
                 for (int n = 0; n < NP; ++n) {
                     const float e = fast_exp2(s[i] * A2[n]);
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(Scan
     const int seg = id % w.nseg, b = id / w.nseg;
     const int D = a.D, N = a.N, Dg = D / a.G;
     const int len = seq_length(a.lengths, b, a.T);
-    const int t0 = seg * SEG, t1 = min(t0 + SEG, a.T), nch = (t1 - t0 + CHUNK - 1) / CHUNK;
+    const int t0 = seg * w.seg, t1 = min(t0 + w.seg, a.T), nch = (t1 - t0 + CHUNK - 1) / CHUNK;
     const int64_t bseg = (int64_t)b * w.nseg + seg;
 
     // staging role: channel `lane` of the tile, tokens 4 wave .. 4 wave + 3 of a
@@ -338,21 +350,25 @@ __global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(Scan
     const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
     const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N, row = (int64_t)a.G * N;
 
-    // h_start[i]: state in front of the segment, for the staging of l_h
-    constexpr int SLOTS = NB * CH * 16 / 256;
-    float h_seg[SLOTS];
-    unsigned chan[SLOTS];                                   // channels of the slots
+    // Slots of the [channel][16] tiles: slot k of a thread is element k 256 + tid.
+    // Channels behind the group's last repeat it.
+    constexpr int SLOTS = NB * CH * 16 / 256, NP = 16 * NB;
+    const int c0 = grp * Dg + tile * CH, cmax = Dg - 1 - tile * CH;   // the tile's first channel; last one in it
+    unsigned slot[SLOTS], chan[SLOTS];                                // [channel][np], [channel]
+    float h_seg[SLOTS];                                               // states in front of the segment
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
-        const int i = k * 256 + tid, nb = i / (CH * 16), c = i / 16 % CH, st = nb * 16 + (i & 15);
-        const int dd = grp * Dg + min(tile * CH + c, Dg - 1);
-        chan[k] = dd;
-        const int64_t at = (bseg * D + dd) * w.np + st;
-        l_A[nb][i % (CH * 16)] = st < N ? a.A[(int64_t)dd * N + st] : 0.f;
+        const int i = k * 256 + tid, nb = i / (CH * 16), c = min(i / 16 % CH, cmax), st = nb * 16 + (i & 15);
+        chan[k] = c;
+        slot[k] = c * NP + st;
+        const int64_t at = (bseg * D + c0) * NP + slot[k];
+        l_A[nb][i % (CH * 16)] = st < N ? a.A[(int64_t)(c0 + c) * N + st] : 0.f;
         h_seg[k] = w.h[at];
         l_g[nb][i % (CH * 16)] = w.g[at];
         l_dA[nb][i % (CH * 16)] = 0.f;
     }
+    // dB and dC of token 8 (row & 1) of a chunk's first wave-share, this lane's state
+    float *const dBC = (lane < 32 ? w.dB : w.dC) + (int64_t)tile * a.B * a.T * row + row0 + 8 * ((lane >> 4) & 1) * row + n;
 
     // raw inputs of one chunk, loaded a chunk ahead
     T xr[4], tr[4], gr[4], zr[4], Br[NB], Cr[NB];
@@ -370,20 +386,21 @@ __global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(Scan
             gr[i] = gs.load(dl, o);
             zr[i] = zs.load(dl, o);
         }
-        const int64_t o = row0 + (int64_t)max(min(tc + tid / 16, len - 1), 0) * row;
+        const int tr0 = max(min(tc, len - 1), 0);
+        const T *Bp = (const T *)a.Bm + row0 + tr0 * row, *Cp = (const T *)a.Cm + row0 + tr0 * row;
+        const unsigned o = (unsigned)max(min(tid / 16, len - 1 - tr0), 0) * (unsigned)row;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int st = min(nb * 16 + (tid & 15), N - 1);
-            Br[nb] = ((const T *)a.Bm)[o + st];
-            Cr[nb] = ((const T *)a.Cm)[o + st];
+            const unsigned st = min(nb * 16 + (tid & 15), N - 1);
+            Br[nb] = Bp[o + st];
+            Cr[nb] = Cp[o + st];
         }
         // (the segment's first chunk has nothing in front of it: its values go unused)
-        const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D;
-        const float *hp = w.hc + at * (16 * NB), *sp = w.sc + at;
+        const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D + c0;
+        const float *hp = w.hc + at * NP, *sp = w.sc + at;
 #pragma unroll
         for (int k = 0; k < SLOTS; ++k) {
-            const unsigned st = (k * 256 + tid) / (CH * 16) * 16 + (tid & 15);
-            hr[k] = (hp + st)[(size_t)chan[k] * (16 * NB)];
+            hr[k] = hp[slot[k]];
             sr[k] = sp[chan[k]];
         }
     };
@@ -486,14 +503,11 @@ __global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(Scan
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int t8 = i * 4 + wave, t = tc + t8 + 8 * ((lane >> 4) & 1), st = nb * 16 + n;
+                const int t8 = i * 4 + wave;
                 float s = 0.f;
 #pragma unroll
                 for (int j = 0; j < WAVES; ++j) s += flush[j][t8][lane];
-                if (t < a.T && st < N) {
-                    float *p = lane < 32 ? w.dB : w.dC;
-                    p[(int64_t)tile * a.B * a.T * row + row0 + t * row + st] = s;
-                }
+                if (tc + t8 + 8 * ((lane >> 4) & 1) < a.T && nb * 16 + n < N) dBC[(tc + t8) * row + nb * 16] = s;
             }
         }
 

@@ -541,7 +541,8 @@ kda_status_t kda_short_conv_bwd(const void *dy, const void *x, const float *w, c
  *            does not fill the device)
  *
  * N from 1 to 64, G >= 1 dividing D (KDA_ERR_INVALID_ARG if it does not);
- * 16, 32 and 64 states run fastest, other counts are padded to them.
+ * 16, 32 and 64 states run fastest, other counts are padded to them.  G N below
+ * 2^24.
  */
 size_t kda_selective_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G);
 
