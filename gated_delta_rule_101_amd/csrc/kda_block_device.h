@@ -10,25 +10,61 @@ constexpr float LN2 = 0.6931471805599453f;
 
 // V consecutive storage elements in one access: V = 16 / sizeof(T) takes a
 // 16-byte load, V = 1 a scalar one (rows whose length leaves them unaligned).
+// stream / unstream are the non-temporal forms, for data that passes once.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <typename T, int V> struct Pack;
 template <typename T> struct Pack<T, 1> {
     T a;
     __device__ __forceinline__ void load(const T *p) { a = *p; }
+    __device__ __forceinline__ void stream(const T *p) { a = __builtin_nontemporal_load(p); }
     __device__ __forceinline__ void zero() { a = T(0); }
     __device__ __forceinline__ void to_f32(float (&x)[1]) const { x[0] = kda::to_f32(a); }
     static __device__ __forceinline__ void store(T *p, const float (&x)[1]) { *p = from_f32<T>(x[0]); }
+    static __device__ __forceinline__ void unstream(T *p, const float (&x)[1]) {
+        __builtin_nontemporal_store(from_f32<T>(x[0]), p);
+    }
 };
 template <> struct Pack<uint16_t, 8> : Raw8<uint16_t> {
-    static __device__ __forceinline__ void store(uint16_t *p, const float (&x)[8]) {
-        uint32_t w[4];
+    __device__ __forceinline__ void stream(const uint16_t *p) {
+        const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+        a = make_uint4(t[0], t[1], t[2], t[3]);
+    }
+    static __device__ __forceinline__ u32x4 bits(const float (&x)[8]) {
+        u32x4 w;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             w[i] = (uint32_t)f32_to_bf16(x[2 * i]) | ((uint32_t)f32_to_bf16(x[2 * i + 1]) << 16);
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        return w;
+    }
+    static __device__ __forceinline__ void store(uint16_t *p, const float (&x)[8]) { *reinterpret_cast<u32x4 *>(p) = bits(x); }
+    static __device__ __forceinline__ void unstream(uint16_t *p, const float (&x)[8]) {
+        __builtin_nontemporal_store(bits(x), reinterpret_cast<u32x4 *>(p));
+    }
+};
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <> struct Pack<uint16_t, 4> : Raw4<uint16_t> {
+    __device__ __forceinline__ void stream(const uint16_t *p) {
+        const u32x2 t = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+        a = make_uint2(t[0], t[1]);
+    }
+    static __device__ __forceinline__ u32x2 bits(const float (&x)[4]) {
+        return u32x2{(uint32_t)f32_to_bf16(x[0]) | ((uint32_t)f32_to_bf16(x[1]) << 16),
+                     (uint32_t)f32_to_bf16(x[2]) | ((uint32_t)f32_to_bf16(x[3]) << 16)};
+    }
+    static __device__ __forceinline__ void store(uint16_t *p, const float (&x)[4]) { *reinterpret_cast<u32x2 *>(p) = bits(x); }
+    static __device__ __forceinline__ void unstream(uint16_t *p, const float (&x)[4]) {
+        __builtin_nontemporal_store(bits(x), reinterpret_cast<u32x2 *>(p));
     }
 };
 template <> struct Pack<float, 4> : Raw4<float> {
+    __device__ __forceinline__ void stream(const float *p) {
+        const f32x4 t = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p));
+        a = make_float4(t[0], t[1], t[2], t[3]);
+    }
     static __device__ __forceinline__ void store(float *p, const float (&x)[4]) { store4(p, x); }
+    static __device__ __forceinline__ void unstream(float *p, const float (&x)[4]) {
+        __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(p));
+    }
 };
 template <typename T> constexpr int WIDE = 16 / (int)sizeof(T);
 

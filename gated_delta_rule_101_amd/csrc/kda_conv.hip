@@ -12,13 +12,12 @@
 #include "kda_block.h"
 #include "kda_block_device.h"
 
-#include <algorithm>
-
 namespace kda {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int BATCH = 4;   // tokens whose loads are issued together
+constexpr int BATCH = 4;   // tokens whose loads are issued together; a run is a multiple of them
+template <bool B> struct Flag { static constexpr bool value = B; };
 
 template <typename T, int W, int V>
 __device__ __forceinline__ void load_taps(float (&w)[W][V], float (&bias)[V], const float *wp, const float *bp, int d)
@@ -46,7 +45,7 @@ __device__ __forceinline__ void load_row(Pack<T, V> &r, const T *x, const T *sta
 // Run `run` covers tokens [run RT, (run + 1) RT).  The thread of run 0 also
 // writes the final state: only it reads the initial one, so the two may be
 // one buffer.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 __global__ void __launch_bounds__(THREADS) kda_conv_fwd_kernel(ConvArgs a, int RT, int nruns, int ncg, int64_t total)
 {
     const int64_t id = (int64_t)blockIdx.x * THREADS + threadIdx.x;
@@ -88,9 +87,9 @@ __global__ void __launch_bounds__(THREADS) kda_conv_fwd_kernel(ConvArgs a, int R
                     float p = bias[c];
 #pragma unroll
                     for (int j = 0; j < W; ++j) p = __builtin_fmaf(w[j][c], win[j][c], p);
-                    o[c] = a.silu ? p * sigmoid_f32(p) : p;
+                    o[c] = SILU ? p * sigmoid_f32(p) : p;
                 }
-                if (t + i < tv) Pack<T, V>::store(y + (int64_t)(t + i) * D, o);
+                if (t + i < tv) Pack<T, V>::unstream(y + (int64_t)(t + i) * D, o);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(THREADS) kda_conv_step_kernel(ConvArgs a, int 
 // W - 1 positions early, where dx is the state's gradient.  Only the run's
 // own tokens enter dw and dbias, which stay in registers and go to the
 // workspace once a run.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, int RT, int nruns, int ncg, int64_t total)
 {
     const int64_t id = (int64_t)blockIdx.x * THREADS + threadIdx.x;
@@ -183,44 +182,57 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
         else r.zero();
         r.to_f32(win[j]);
     }
-    for (int t = t0; t < t1 + W - 1; t += BATCH) {
-        Pack<T, V> xi[BATCH], gi[BATCH];
+    Pack<T, V> xn[BATCH], gn[BATCH];   // the next batch, requested while this one is computed
+    const auto fetch = [&](int t) {
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             if (t + i < min(len, t1 + W - 1)) {
-                xi[i].load(x + (int64_t)(t + i) * D);
-                gi[i].load(dy + (int64_t)(t + i) * D);
+                xn[i].load(x + (int64_t)(t + i) * D);
+                gn[i].load(dy + (int64_t)(t + i) * D);
             } else {
-                xi[i].zero();
-                gi[i].zero();
+                xn[i].zero();
+                gn[i].zero();
             }
         }
+    };
+    // One batch of tokens from t.  OWN: they belong to the run and enter dw and
+    // dbias (a token past the sequence has g = 0, and with it no share of
+    // anything); otherwise they are the W - 1 behind it.
+    const auto batch = [&](int t, auto own) {
+        Pack<T, V> xi[BATCH], gi[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-            const int tt = t + i;
+            xi[i] = xn[i];
+            gi[i] = gn[i];
+        }
+        if constexpr (decltype(own)::value) fetch(t + BATCH);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
             float g[V], out[V];
             xi[i].to_f32(win[W - 1]);
             gi[i].to_f32(g);
 #pragma unroll
             for (int c = 0; c < V; ++c) {
-                float p = bias[c];
+                float v = g[c];
+                if constexpr (SILU) {
+                    float p = bias[c];
 #pragma unroll
-                for (int j = 0; j < W; ++j) p = __builtin_fmaf(w[j][c], win[j][c], p);
-                const float sg = sigmoid_f32(p);
-                // past the end g is 0, and with it this token's share of everything
-                const float v = a.silu ? g[c] * (sg * __builtin_fmaf(p, 1.f - sg, 1.f)) : g[c];
+                    for (int j = 0; j < W; ++j) p = __builtin_fmaf(w[j][c], win[j][c], p);
+                    const float sg = sigmoid_f32(p);
+                    v *= sg * __builtin_fmaf(p, 1.f - sg, 1.f);
+                }
                 dp[W - 1][c] = v;
-                if (tt < t1) {
+                if constexpr (decltype(own)::value) {
                     db[c] += v;
 #pragma unroll
                     for (int j = 0; j < W; ++j) dw[j][c] = __builtin_fmaf(v, win[j][c], dw[j][c]);
                 }
-                float s = 0.f;
+                float s = w[0][c] * v;
 #pragma unroll
-                for (int j = 0; j < W; ++j) s = __builtin_fmaf(w[j][c], dp[W - 1 - j][c], s);
+                for (int j = 1; j < W; ++j) s = __builtin_fmaf(w[j][c], dp[W - 1 - j][c], s);
                 out[c] = s;
             }
-            const int to = tt - (W - 1);
+            const int to = t + i - (W - 1);
             if (to < t1 && (to >= t0 || run == 0)) {
                 const int r = to - len + (W - 1);   // row of the final state that this input is
                 if (dsf && r >= 0 && r < W - 1) {
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
                     if (to >= len)
 #pragma unroll
                         for (int c = 0; c < V; ++c) out[c] = 0.f;
-                    Pack<T, V>::store(dx + (int64_t)to * D, out);
+                    Pack<T, V>::unstream(dx + (int64_t)to * D, out);
                 } else if (ds0) {
                     Pack<T, V>::store(ds0 + (int64_t)(to + W - 1) * D, out);
                 }
@@ -248,7 +260,11 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
                     dp[j][c] = dp[j + 1][c];
                 }
         }
-    }
+    };
+    fetch(t0);
+    int t = t0;
+    for (; t < t1; t += BATCH) batch(t, Flag<true>{});
+    if (t < t1 + W - 1) batch(t, Flag<false>{});   // a run's length is a multiple of BATCH unless the sequence ends in it
     float *pw = a.ws + rest * ((int64_t)D * W) + (int64_t)d * W;
     float *pb = a.ws + (int64_t)a.B * nruns * D * W + rest * D + d;
 #pragma unroll
@@ -269,14 +285,16 @@ int run_tokens(int B, int T, int64_t ncg, int most, int64_t want)
     while ((int64_t)B * ((T + rt - 1) / rt) * ncg >= ((int64_t)1 << 38)) rt <<= 1;   // grid limit
     return rt;
 }
-int fwd_run(int B, int T, int64_t ncg) { return run_tokens(B, T, ncg, 64, 1 << 18); }
+int fwd_run(int B, int T, int64_t ncg) { return run_tokens(B, T, ncg, 256, 1 << 17); }
 int bwd_run(int B, int T, int64_t ncg) { return run_tokens(B, T, ncg, 256, 1 << 17); }
 
-// The backward's partial sums are sized for the widest runs' count of either
-// storage type: the one-channel walk has the most threads, hence the longest runs.
-int64_t bwd_runs(int B, int T, int D, int V)
+// The backward holds taps, windows and sums of every channel it walks: four
+// channels a thread for either type (with eight the registers leave one
+// wavefront a SIMD).
+constexpr int BWD_WIDE = 4;
+int64_t bwd_runs(int B, int T, int D)
 {
-    const int rt = bwd_run(B, T, (D + V - 1) / V);
+    const int rt = bwd_run(B, T, D % BWD_WIDE ? D : D / BWD_WIDE);
     return T > 0 ? (T + rt - 1) / rt : 1;
 }
 
@@ -289,8 +307,10 @@ hipError_t fwd_w(const ConvArgs &a, hipStream_t s)
     const int rt = fwd_run(a.B, a.T, ncg), nruns = a.T > 0 ? (a.T + rt - 1) / rt : 1;
     const int64_t total = (int64_t)a.B * nruns * ncg, blocks = (total + THREADS - 1) / THREADS;
     if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    if (wide) kda_conv_fwd_kernel<T, W, V><<<(unsigned)blocks, THREADS, 0, s>>>(a, rt, nruns, ncg, total);
-    else kda_conv_fwd_kernel<T, W, 1><<<(unsigned)blocks, THREADS, 0, s>>>(a, rt, nruns, ncg, total);
+    if (wide) (a.silu ? kda_conv_fwd_kernel<T, W, V, true> : kda_conv_fwd_kernel<T, W, V, false>)<<<(unsigned)blocks, THREADS, 0, s>>>(
+        a, rt, nruns, ncg, total);
+    else (a.silu ? kda_conv_fwd_kernel<T, W, 1, true> : kda_conv_fwd_kernel<T, W, 1, false>)<<<(unsigned)blocks, THREADS, 0, s>>>(
+        a, rt, nruns, ncg, total);
     return hipGetLastError();
 }
 
@@ -310,15 +330,16 @@ hipError_t step_w(const ConvArgs &a, hipStream_t s)
 template <typename T, int W>
 hipError_t bwd_w(const ConvBwdArgs &a, hipStream_t s)
 {
-    constexpr int V = WIDE<T>;
+    constexpr int V = BWD_WIDE;
     const bool wide = a.D % V == 0;
     const int ncg = wide ? a.D / V : a.D;
     const int rt = bwd_run(a.B, a.T, ncg), nruns = a.T > 0 ? (a.T + rt - 1) / rt : 1;
     const int64_t total = (int64_t)a.B * nruns * ncg, blocks = (total + THREADS - 1) / THREADS;
     if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     if (total > 0) {
-        if (wide) kda_conv_bwd_kernel<T, W, V><<<(unsigned)blocks, THREADS, 0, s>>>(a, rt, nruns, ncg, total);
-        else kda_conv_bwd_kernel<T, W, 1><<<(unsigned)blocks, THREADS, 0, s>>>(a, rt, nruns, ncg, total);
+        (wide ? a.silu ? kda_conv_bwd_kernel<T, W, V, true> : kda_conv_bwd_kernel<T, W, V, false>
+              : a.silu ? kda_conv_bwd_kernel<T, W, 1, true> : kda_conv_bwd_kernel<T, W, 1, false>)
+            <<<(unsigned)blocks, THREADS, 0, s>>>(a, rt, nruns, ncg, total);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -337,12 +358,7 @@ hipError_t by_width(int W, F2 f2, F3 f3, F4 f4)
 
 }  // namespace
 
-int64_t conv_bwd_workspace_floats(int B, int T, int D, int W)
-{
-    const int64_t runs = std::max(bwd_runs(B, T, D, 1), std::max(D % 4 == 0 ? bwd_runs(B, T, D, 4) : (int64_t)0,
-                                                                 D % 8 == 0 ? bwd_runs(B, T, D, 8) : (int64_t)0));
-    return (int64_t)B * runs * D * (W + 1);
-}
+int64_t conv_bwd_workspace_floats(int B, int T, int D, int W) { return (int64_t)B * bwd_runs(B, T, D) * D * (W + 1); }
 
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t s)
 {

@@ -8,8 +8,8 @@
 // the row again, and the variance does not cancel.  TPR grows with D: below a
 // wavefront the sums are shuffles, above it they also pass through LDS.
 // Groups walk rows with a stride, keeping their channels' weights and, in the
-// backward, their partial dw and db in registers; those go to the workspace
-// once a group and are summed by column afterwards.
+// backward, their partial dw and db in registers; those meet in LDS, go to the
+// workspace once a workgroup and are summed by column afterwards.
 #include "kda_block.h"
 #include "kda_block_device.h"
 
@@ -63,25 +63,31 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs
             b[j][c] = a.bias && d < D ? a.bias[d] : 0.f;
         }
     const float inv_d = 1.f / D;
-    int slot = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS) {
-        const int64_t row = r0 + threadIdx.x / TPR;
-        const bool live = row < a.rows;   // the last workgroup's idle groups repeat the last row
-        const T *x = (const T *)a.x + (live ? row : a.rows - 1) * D;
-        float v[NV][V], s = 0.f, unused = 0.f;
-        Pack<T, V> raw[NV];
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+    // The next row is requested while this one is reduced.  Groups past the
+    // last row repeat it (they take part in the barriers) and store nothing.
+    int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR;
+    Pack<T, V> raw[NV];
+    const auto fetch = [&](int64_t r) {
+        const T *x = (const T *)a.x + (r < a.rows ? r : a.rows - 1) * D;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int d = V * (j * TPR + l);
-            if (d < D) raw[j].load(x + d);
+            if (d < D) raw[j].stream(x + d);
             else raw[j].zero();
         }
+    };
+    fetch(row);
+    int slot = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step, row += step) {
+        float v[NV][V], s = 0.f, unused = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             raw[j].to_f32(v[j]);
 #pragma unroll
             for (int c = 0; c < V; ++c) s += v[j][c];
         }
+        if (r0 + step < a.rows) fetch(row + step);
         group_sum2<TPR>(s, unused, part, slot);
         const float mean = s * inv_d;
         float ss = 0.f;
@@ -96,7 +102,7 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs
         group_sum2<TPR>(ss, unused, part, slot + 1);
         slot ^= 2;
         const float r = rsqrtf(__builtin_fmaf(ss, inv_d, a.eps));
-        if (live) {
+        if (row < a.rows) {
             T *y = (T *)a.y + row * D;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -105,7 +111,7 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs
                     float o[V];
 #pragma unroll
                     for (int c = 0; c < V; ++c) o[c] = __builtin_fmaf(v[j][c] * r, w[j][c], b[j][c]);
-                    Pack<T, V>::store(y + d, o);
+                    Pack<T, V>::unstream(y + d, o);
                 }
             }
         }
@@ -128,75 +134,76 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_bwd_kernel(NormBwdA
             dw[j][c] = db[j][c] = 0.f;
         }
     const float inv_d = 1.f / D;
-    int slot = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS) {
-        const int64_t row = r0 + threadIdx.x / TPR;
-        const bool live = row < a.rows;
-        const int64_t at = (live ? row : a.rows - 1) * D;
-        Pack<T, V> xr[NV], gr[NV];
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+    int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR;   // rows and idle groups as in the forward
+    Pack<T, V> xr[NV], gr[NV];
+    const auto fetch = [&](int64_t r) {
+        const int64_t at = (r < a.rows ? r : a.rows - 1) * D;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int d = V * (j * TPR + l);
             if (d < D) {
-                xr[j].load((const T *)a.x + at + d);
-                gr[j].load((const T *)a.dy + at + d);
+                xr[j].stream((const T *)a.x + at + d);
+                gr[j].stream((const T *)a.dy + at + d);
             } else {
                 xr[j].zero();
                 gr[j].zero();
             }
         }
-        float v[NV][V], s = 0.f, sg = 0.f;
+    };
+    fetch(row);
+    int slot = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step, row += step) {
+        float v[NV][V], g[NV][V], s = 0.f, sg = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float g[V];
             xr[j].to_f32(v[j]);
-            gr[j].to_f32(g);
+            gr[j].to_f32(g[j]);
 #pragma unroll
             for (int c = 0; c < V; ++c) {
                 s += v[j][c];
-                sg = __builtin_fmaf(g[c], w[j][c], sg);
+                sg = __builtin_fmaf(g[j][c], w[j][c], sg);
             }
         }
+        if (r0 + step < a.rows) fetch(row + step);
         group_sum2<TPR>(s, sg, part, slot);
         const float mean = s * inv_d;
         float ss = 0.f, sn = 0.f;   // sum (x - mean)^2, sum g (x - mean)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (V * (j * TPR + l) < D) {
-                float g[V];
-                gr[j].to_f32(g);
 #pragma unroll
                 for (int c = 0; c < V; ++c) {
                     v[j][c] -= mean;
                     ss = __builtin_fmaf(v[j][c], v[j][c], ss);
-                    sn = __builtin_fmaf(g[c] * w[j][c], v[j][c], sn);
+                    sn = __builtin_fmaf(g[j][c] * w[j][c], v[j][c], sn);
                 }
             }
         group_sum2<TPR>(ss, sn, part, slot + 1);
         slot ^= 2;
         const float r = rsqrtf(__builtin_fmaf(ss, inv_d, a.eps));
         const float c1 = sg * inv_d, c2 = sn * r * inv_d;   // mean g, mean g n
-        if (live) {
+        if (row < a.rows) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int d = V * (j * TPR + l);
                 if (d < D) {
-                    float g[V], o[V];
-                    gr[j].to_f32(g);
+                    float o[V];
 #pragma unroll
                     for (int c = 0; c < V; ++c) {
                         const float n = v[j][c] * r;
-                        dw[j][c] = __builtin_fmaf(g[c], n, dw[j][c]);
-                        db[j][c] += g[c];
-                        o[c] = r * (__builtin_fmaf(g[c], w[j][c], -c1) - n * c2);
+                        dw[j][c] = __builtin_fmaf(g[j][c], n, dw[j][c]);
+                        db[j][c] += g[j][c];
+                        o[c] = r * (__builtin_fmaf(g[j][c], w[j][c], -c1) - n * c2);
                     }
-                    Pack<T, V>::store((T *)a.dx + at + d, o);
+                    Pack<T, V>::unstream((T *)a.dx + row * D + d, o);
                 }
             }
         }
     }
-    if (a.ws) {
-        float *p = a.ws + ((int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR) * 2 * D;
+    if (!a.ws) return;
+    float *p = a.ws + (int64_t)blockIdx.x * 2 * D;
+    if constexpr (GROUPS == 1) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -207,6 +214,25 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_bwd_kernel(NormBwdA
                     p[D + d] = db[j][c];
                 }
             }
+    } else {   // the groups' sums meet in LDS, in order
+        constexpr int WIDTH = NV * V * TPR;
+        __shared__ float sums[GROUPS][2][WIDTH];
+        const int grp = threadIdx.x / TPR;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                const int d = V * (j * TPR + l) + c;
+                sums[grp][0][d] = dw[j][c];
+                sums[grp][1][d] = db[j][c];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * D; i += BLOCK<TPR>) {
+            float s = 0.f;
+#pragma unroll
+            for (int q = 0; q < GROUPS; ++q) s += sums[q][i >= D][i >= D ? i - D : i];
+            p[i] = s;
+        }
     }
 }
 
@@ -218,13 +244,13 @@ int groups_per_block(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
 int64_t fwd_blocks(int64_t rows, int tpr)
 {
     const int64_t need = (rows + groups_per_block(tpr) - 1) / groups_per_block(tpr);
-    const int64_t most = tpr == 1024 ? 512 : 2048;
+    const int64_t most = tpr == 1024 ? 512 : 1024;
     return need < most ? need : most;
 }
 int64_t bwd_blocks(int64_t rows, int tpr)
 {
     const int64_t need = (rows + groups_per_block(tpr) - 1) / groups_per_block(tpr);
-    const int64_t most = tpr == 1024 ? 256 : 512;
+    const int64_t most = tpr == 1024 ? 256 : 768;   // three workgroups a compute unit: all resident
     return need < most ? need : most;
 }
 
@@ -265,7 +291,7 @@ template <typename T, int V> hipError_t bwd_v(const NormBwdArgs &a, hipStream_t 
 int64_t norm_bwd_workspace_floats(int64_t rows, int D)
 {
     const int tpr = threads_per_row(D);
-    return bwd_blocks(rows, tpr) * groups_per_block(tpr) * 2 * D;
+    return bwd_blocks(rows, tpr) * 2 * D;
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s)
@@ -287,7 +313,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs &args, hipStream_t s)
         if (e != hipSuccess || !sums) return e;
     }
     const int tpr = threads_per_row(a.D);
-    const int64_t n = a.rows > 0 ? bwd_blocks(a.rows, tpr) * groups_per_block(tpr) : 0;
+    const int64_t n = a.rows > 0 ? bwd_blocks(a.rows, tpr) : 0;
     const ColumnSum jobs[] = {{a.ws, a.dweight, n, a.D, 2 * (int64_t)a.D, false},
                               {n ? a.ws + a.D : nullptr, a.dbias, n, a.D, 2 * (int64_t)a.D, false}};
     return launch_column_sums(jobs, 2, s);

@@ -348,72 +348,91 @@ __global__ void __launch_bounds__(256) kda_scan_quad_kernel(ScanArgs a, int tile
 }
 
 // One token: LPC lanes a channel, 4 states each, so a wavefront's states are
-// contiguous 16-byte accesses; the read and write of the states bound it.
-template <typename T, int LPC, bool VEC>
-__global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int64_t channels)
+// contiguous 16-byte accesses; the read and write of the states bound it.  A
+// thread takes BATCH pieces 256 lanes apart, so that a workgroup moves a
+// contiguous stretch of states whose loads are all out before the first is
+// used; states pass once and are accessed non-temporally.
+template <typename T, int LPC, bool VEC, int BATCH>
+__global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int64_t lanes)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const bool ok = id / LPC < channels;
-    const int64_t c = ok ? id / LPC : channels - 1;   // idle groups repeat the last channel
-    const int l = id % LPC, D = a.D, N = a.N, n0 = 4 * l;
-    const int b = (int)(c / D), d = (int)(c % D), g = d / (D / a.G);
-    float *hp = a.h_final + c * N;
-    const int64_t row = ((int64_t)b * a.G + g) * N;
-    const T *Bp = (const T *)a.Bm + row, *Cp = (const T *)a.Cm + row;
-    const float *Ap = a.A + (int64_t)d * N;
+    constexpr int STEP = 256 / LPC;   // channels between a thread's pieces
+    const int l = threadIdx.x % LPC, D = a.D, N = a.N, n0 = 4 * l, Dg = D / a.G;
+    const int64_t first = (int64_t)blockIdx.x * 256 * BATCH + threadIdx.x, channels = lanes / LPC;
+    const int64_t c0 = first / LPC;
+    const bool in4 = n0 < N;
 
-    float h[4], A[4], B[4], C[4];
-    if constexpr (VEC) {
-        if (n0 < N) {
-            Raw4<float> r;
+    float A2[BATCH][4], h[BATCH][4], B[BATCH][4], C[BATCH][4], x[BATCH], s[BATCH], z[BATCH], skip[BATCH];
+    Pack<float, 4> hr[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {   // pieces behind the last channel repeat it and store nothing
+        const int64_t c = c0 + i * STEP < channels ? c0 + i * STEP : channels - 1;
+        const float *hp = a.h_final + c * N;
+        if (VEC && in4) hr[i].stream(hp + n0);
+        else hr[i].zero();
+        if (!VEC)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) h[i][n] = n0 + n < N ? hp[n0 + n] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+        const int64_t c = c0 + i * STEP < channels ? c0 + i * STEP : channels - 1;
+        const int b = (int)(c / D), d = (int)(c - (int64_t)b * D);
+        const int64_t row = ((int64_t)b * a.G + d / Dg) * N;
+        const T *Bp = (const T *)a.Bm + row + n0, *Cp = (const T *)a.Cm + row + n0;
+        const float *Ap = a.A + (int64_t)d * N + n0;
+        if constexpr (VEC) {
             Raw4<T> q;
-            r.load(hp + n0);
-            r.to_f32(h);
-            r.load(Ap + n0);
-            r.to_f32(A);
-            q.load(Bp + n0);
-            q.to_f32(B);
-            q.load(Cp + n0);
-            q.to_f32(C);
+            Raw4<float> r;
+            q.zero();
+            r.zero();
+            if (in4) q.load(Bp);
+            q.to_f32(B[i]);
+            if (in4) q.load(Cp);
+            q.to_f32(C[i]);
+            if (in4) r.load(Ap);
+            r.to_f32(A2[i]);
+        } else {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                B[i][n] = n0 + n < N ? to_f32(Bp[n]) : 0.f;
+                C[i][n] = n0 + n < N ? to_f32(Cp[n]) : 0.f;
+                A2[i][n] = n0 + n < N ? Ap[n] : 0.f;
+            }
         }
+        x[i] = to_f32(((const T *)a.x)[c]);
+        s[i] = to_f32(((const T *)a.dt)[c]) + (a.dt_bias ? a.dt_bias[d] : 0.f);
+        z[i] = a.z ? to_f32(((const T *)a.z)[c]) : 0.f;
+        skip[i] = a.Dskip ? a.Dskip[d] : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool in = n0 + i < N;
-        if (!VEC || !in) {
-            h[i] = in ? hp[n0 + i] : 0.f;
-            A[i] = in ? Ap[n0 + i] : 0.f;
-            B[i] = in ? to_f32(Bp[n0 + i]) : 0.f;
-            C[i] = in ? to_f32(Cp[n0 + i]) : 0.f;
+    for (int i = 0; i < BATCH; ++i) {
+        if (VEC) hr[i].to_f32(h[i]);
+        if (a.softplus) s[i] = softplus_f32(s[i]);
+        const float u = s[i] * x[i], s2 = s[i] * LOG2E;
+        float y = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            h[i][n] = __builtin_fmaf(fast_exp2(s2 * A2[i][n]), h[i][n], u * B[i][n]);
+            y = __builtin_fmaf(C[i][n], h[i][n], y);
         }
-    }
-    const float x = to_f32(((const T *)a.x)[c]);
-    float s = to_f32(((const T *)a.dt)[c]) + (a.dt_bias ? a.dt_bias[d] : 0.f);
-    if (a.softplus) s = softplus_f32(s);
-    const float u = s * x, s2 = s * LOG2E;
-    float y = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = __builtin_fmaf(fast_exp2(s2 * A[i]), h[i], u * B[i]);
-        y = __builtin_fmaf(C[i], h[i], y);
-    }
+        for (int m = 1; m < LPC; m <<= 1) y += __shfl_xor(y, m, LPC);
+        const int64_t c = c0 + i * STEP;
+        if (c < channels) {
+            float *hp = a.h_final + c * N;
+            if (VEC) {
+                if (in4) Pack<float, 4>::unstream(hp + n0, h[i]);
+            } else {
 #pragma unroll
-    for (int m = 1; m < LPC; m <<= 1) y += __shfl_xor(y, m, LPC);
-    if (!ok) return;
-    if (VEC) {
-        if (n0 < N) store4(hp + n0, h);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n0 + i < N) hp[n0 + i] = h[i];
-    }
-    if (l == 0) {
-        if (a.Dskip) y = __builtin_fmaf(a.Dskip[d], x, y);
-        if (a.z) {
-            const float z = to_f32(((const T *)a.z)[c]);
-            y *= z * sigmoid_f32(z);
+                for (int n = 0; n < 4; ++n)
+                    if (n0 + n < N) hp[n0 + n] = h[i][n];
+            }
+            if (l == 0) {
+                y = __builtin_fmaf(skip[i], x[i], y);
+                if (a.z) y *= z[i] * sigmoid_f32(z[i]);
+                ((T *)a.y)[c] = from_f32<T>(y);
+            }
         }
-        ((T *)a.y)[c] = from_f32<T>(y);
     }
 }
 
@@ -491,13 +510,19 @@ template <typename T> hipError_t fwd_dispatch(const ScanArgs &a, hipStream_t s)
     }
 }
 
+template <typename T, int LPC, bool VEC, int BATCH> hipError_t step_batch(const ScanArgs &a, hipStream_t s)
+{
+    const int64_t lanes = (int64_t)a.B * a.D * LPC, blocks = (lanes + 256 * BATCH - 1) / (256 * BATCH);
+    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    kda_scan_step_kernel<T, LPC, VEC, BATCH><<<(unsigned)blocks, 256, 0, s>>>(a, lanes);
+    return hipGetLastError();
+}
+// Several pieces a thread where that still leaves several rounds of workgroups.
 template <typename T, int LPC> hipError_t step_launch(const ScanArgs &a, hipStream_t s)
 {
-    const int64_t channels = (int64_t)a.B * a.D, blocks = (channels * LPC + 255) / 256;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    if (a.N % 4 == 0) kda_scan_step_kernel<T, LPC, true><<<(unsigned)blocks, 256, 0, s>>>(a, channels);
-    else kda_scan_step_kernel<T, LPC, false><<<(unsigned)blocks, 256, 0, s>>>(a, channels);
-    return hipGetLastError();
+    const bool many = (int64_t)a.B * a.D * LPC >= (int64_t)4 * 256 * 8192;
+    if (a.N % 4 == 0) return many ? step_batch<T, LPC, true, 4>(a, s) : step_batch<T, LPC, true, 1>(a, s);
+    return many ? step_batch<T, LPC, false, 4>(a, s) : step_batch<T, LPC, false, 1>(a, s);
 }
 
 template <typename T> hipError_t step_dispatch(const ScanArgs &a, hipStream_t s)
