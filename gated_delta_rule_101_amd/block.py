@@ -18,37 +18,67 @@ runs on (`stream`, or the current one of the tensors' device).
 
 from __future__ import annotations
 
-import contextlib
 from typing import Dict, Optional, Tuple
 
 import torch
 
-from .kda import _check_dev, _dtype_code, _nbytes, _ptr, _raise, load_library
+from .kda import _dtype_code, _nbytes, _ptr, _raise, load_library
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
-    """Makes the tensors' device, and `stream` if one is given, current: the
-    launch goes there and what is allocated meanwhile belongs to that stream."""
-    if stream is not None and stream.device != device:
-        raise ValueError("stream must be of the tensors' device")
-    if stream is None and torch.cuda.current_device() == device.index:
-        yield torch.cuda.current_stream(device).cuda_stream
-        return
-    with torch.cuda.device(device):
+class _on:
+    """Makes the tensors' device, and `stream` if one is given, current inside
+    the block (the launch goes there and what is allocated meanwhile belongs to
+    that stream); enters with the stream's handle.  Nothing has to be switched
+    in the common case, no stream given on the current device."""
+
+    __slots__ = ("handle", "inner")
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        self.inner = None
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
+            if torch.cuda.current_device() != device.index:
+                self.inner = torch.cuda.device(device)
+            self.handle = torch.cuda.current_stream(device.index).cuda_stream
         else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+            if stream.device != device:
+                raise ValueError("stream must be of the tensors' device")
+            self.inner = torch.cuda.stream(stream)   # switches the device as well
+            self.handle = stream.cuda_stream
+
+    def __enter__(self) -> int:
+        if self.inner is not None:
+            self.inner.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
+
+
+def _device(*ts: Optional[torch.Tensor]) -> torch.device:
+    """The GPU that holds all the tensors given, each contiguous."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        d = t.device
+        if dev is None:
+            if d.type != "cuda":
+                raise ValueError("all tensors must be on the GPU")
+            dev = d
+        elif d != dev:
+            raise ValueError("all tensors must be on one device")
+        if not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+    return dev
 
 
 def _shape(t: Optional[torch.Tensor], shape, what: str, dtype: Optional[torch.dtype] = None):
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
 
 
@@ -89,7 +119,7 @@ def kda_short_conv_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Te
     [B,W-1,D] or None); state_final may be passed and may be state0 itself."""
     lib = load_library()
     B, T, D, W = _conv_shapes(x, w, bias, state0, lengths, False)
-    dev = _check_dev(x, w, bias, state0, lengths, y, state_final)
+    dev = _device(x, w, bias, state0, lengths, y, state_final)
     _shape(y, x.shape, "y", x.dtype)
     _shape(state_final, (B, W - 1, D), "state_final", x.dtype)
     with _on(dev, stream) as handle:
@@ -111,7 +141,7 @@ def kda_short_conv_step(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.T
     lib = load_library()
     B, _, D, W = _conv_shapes(x, w, bias, state, None, True)
     _shape(y, x.shape, "y", x.dtype)
-    dev = _check_dev(x, w, bias, state, y)
+    dev = _device(x, w, bias, state, y)
     with _on(dev, stream) as handle:
         if y is None:
             y = torch.empty_like(x)
@@ -138,7 +168,7 @@ def kda_short_conv_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias:
     B, T, D, W = _conv_shapes(x, w, bias, state0, lengths, False)
     _shape(dy, x.shape, "dy", x.dtype)
     _shape(dstate_final, (B, W - 1, D), "dstate_final", x.dtype)
-    dev = _check_dev(dy, x, w, bias, state0, dstate_final, lengths, workspace)
+    dev = _device(dy, x, w, bias, state0, dstate_final, lengths, workspace)
     with _on(dev, stream) as handle:
         out = {"dx": torch.empty_like(x), "dw": torch.empty_like(w),
                "dbias": torch.empty((D,), dtype=torch.float32, device=dev)}
@@ -200,7 +230,7 @@ def kda_selective_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B
     B, T, C, N, G = _scan_shapes(x, dt, A, Bm, Cm, h0, D, z, dt_bias, lengths, False)
     _shape(y, x.shape, "y", x.dtype)
     _shape(h_final, (B, C, N), "h_final", torch.float32)
-    dev = _check_dev(x, dt, A, Bm, Cm, h0, D, z, dt_bias, lengths, y, h_final, workspace)
+    dev = _device(x, dt, A, Bm, Cm, h0, D, z, dt_bias, lengths, y, h_final, workspace)
     with _on(dev, stream) as handle:
         if y is None:
             y = torch.empty_like(x)
@@ -224,7 +254,7 @@ def kda_selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, 
     lib = load_library()
     B, _, C, N, G = _scan_shapes(x, dt, A, Bm, Cm, h, D, z, dt_bias, None, True)
     _shape(y, x.shape, "y", x.dtype)
-    dev = _check_dev(x, dt, A, Bm, Cm, h, D, z, dt_bias, y)
+    dev = _device(x, dt, A, Bm, Cm, h, D, z, dt_bias, y)
     with _on(dev, stream) as handle:
         if y is None:
             y = torch.empty_like(x)
@@ -255,7 +285,7 @@ def kda_selective_scan_bwd(dy: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, 
     B, T, C, N, G = _scan_shapes(x, dt, A, Bm, Cm, h0, D, z, dt_bias, lengths, False)
     _shape(dy, x.shape, "dy", x.dtype)
     _shape(dh_final, (B, C, N), "dh_final", torch.float32)
-    dev = _check_dev(dy, x, dt, A, Bm, Cm, h0, D, z, dt_bias, dh_final, lengths, workspace)
+    dev = _device(dy, x, dt, A, Bm, Cm, h0, D, z, dt_bias, dh_final, lengths, workspace)
     with _on(dev, stream) as handle:
         out = {"dx": torch.empty_like(x), "ddt": torch.empty_like(x), "dA": torch.empty_like(A),
                "dB": torch.empty_like(Bm), "dC": torch.empty_like(Cm)}
@@ -294,7 +324,7 @@ def kda_layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     _shape(weight, (D,), "weight", torch.float32)
     _shape(bias, (D,), "bias", torch.float32)
     _shape(y, x.shape, "y", x.dtype)
-    dev = _check_dev(x, weight, bias, y)
+    dev = _device(x, weight, bias, y)
     with _on(dev, stream) as handle:
         if y is None:
             y = torch.empty_like(x)
@@ -325,7 +355,7 @@ def kda_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch
     _shape(dy, x.shape, "dy", x.dtype)
     _shape(weight, (D,), "weight", torch.float32)
     _shape(dx, x.shape, "dx", x.dtype)
-    dev = _check_dev(dy, x, weight, dx, workspace)
+    dev = _device(dy, x, weight, dx, workspace)
     with _on(dev, stream) as handle:
         if dx is None:
             dx = torch.empty_like(x)

@@ -58,9 +58,9 @@ Layout layout(float *p, int B, int T, int D, int N, int G)
 {
     Layout w;
     w.tiles = (D / G + CH - 1) / CH;
-    // Segments of 128 tokens, of 64 or 32 where there would be under 2048 of
+    // Segments of 256 tokens, halved down to 32 where there would be under 2048 of
     // them (two workgroups a compute unit, several rounds).
-    w.seg = 128;
+    w.seg = 256;
     while (w.seg > 32 && (int64_t)B * ((T + w.seg - 1) / w.seg) * G * w.tiles < 2048) w.seg /= 2;
     w.nseg = (T + w.seg - 1) / w.seg;
     w.nchunk = (T + CHUNK - 1) / CHUNK;
