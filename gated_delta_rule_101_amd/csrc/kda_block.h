@@ -88,10 +88,10 @@ struct NormBwdArgs {
     bool bf16;
 };
 
-// Column sums out[m] = sum_r in[r * stride + m], m < cols, of up to four
-// matrices in one launch; rows == 0 gives zeros.
+// Column sums out[m] = sum_r in[r * stride + m], m < cols, of up to five
+// matrices; rows == 0 gives zeros.  The matrices may be overwritten.
 struct ColumnSum {
-    const float *in;
+    float *in;
     void *out;
     int64_t rows, cols, stride;
     bool out_bf16;

@@ -46,6 +46,11 @@ __device__ __forceinline__ void group_sum2(float &a, float &b, float2 (*part)[BL
     }
 }
 
+// 1024 threads leave 128 registers each: there a row is requested when its turn
+// comes, and the weights are read again for every row (with both kept, the
+// widest rows spilled).
+template <int TPR> constexpr bool AHEAD = TPR < 1024;
+
 // Channels of vector j of thread l: V j TPR + V l ..; live while below D.
 template <typename T, int V, int NV, int TPR>
 __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs a)
@@ -53,15 +58,18 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs
     constexpr int GROUPS = BLOCK<TPR> / TPR;
     __shared__ float2 part[4][BLOCK<TPR> / 64];
     const int l = threadIdx.x % TPR, D = a.D;
-    float w[NV][V], b[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
+    float w[AHEAD<TPR> ? NV : 1][V], b[AHEAD<TPR> ? NV : 1][V];
+    const auto params = [&](int j, float (&wj)[V], float (&bj)[V]) {
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             const int d = V * (j * TPR + l) + c;
-            w[j][c] = a.weight && d < D ? a.weight[d] : 1.f;
-            b[j][c] = a.bias && d < D ? a.bias[d] : 0.f;
+            wj[c] = a.weight && d < D ? a.weight[d] : 1.f;
+            bj[c] = a.bias && d < D ? a.bias[d] : 0.f;
         }
+    };
+    if constexpr (AHEAD<TPR>)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) params(j, w[j], b[j]);
     const float inv_d = 1.f / D;
     const int64_t step = (int64_t)gridDim.x * GROUPS;
     // The next row is requested while this one is reduced.  Groups past the
@@ -77,9 +85,10 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs
             else raw[j].zero();
         }
     };
-    fetch(row);
+    if (AHEAD<TPR>) fetch(row);
     int slot = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step, row += step) {
+        if (!AHEAD<TPR>) fetch(row);
         float v[NV][V], s = 0.f, unused = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -87,7 +96,7 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs
 #pragma unroll
             for (int c = 0; c < V; ++c) s += v[j][c];
         }
-        if (r0 + step < a.rows) fetch(row + step);
+        if (AHEAD<TPR> && r0 + step < a.rows) fetch(row + step);
         group_sum2<TPR>(s, unused, part, slot);
         const float mean = s * inv_d;
         float ss = 0.f;
@@ -108,9 +117,11 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_fwd_kernel(NormArgs
             for (int j = 0; j < NV; ++j) {
                 const int d = V * (j * TPR + l);
                 if (d < D) {
+                    constexpr int K = AHEAD<TPR> ? 1 : 0;
                     float o[V];
+                    if constexpr (!AHEAD<TPR>) params(j, w[0], b[0]);
 #pragma unroll
-                    for (int c = 0; c < V; ++c) o[c] = __builtin_fmaf(v[j][c] * r, w[j][c], b[j][c]);
+                    for (int c = 0; c < V; ++c) o[c] = __builtin_fmaf(v[j][c] * r, w[K * j][c], b[K * j][c]);
                     Pack<T, V>::unstream(y + d, o);
                 }
             }
@@ -124,15 +135,18 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_bwd_kernel(NormBwdA
     constexpr int GROUPS = BLOCK<TPR> / TPR;
     __shared__ float2 part[4][BLOCK<TPR> / 64];
     const int l = threadIdx.x % TPR, D = a.D;
-    float w[NV][V], dw[NV][V], db[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
+    constexpr int K = AHEAD<TPR> ? 1 : 0;
+    float w[AHEAD<TPR> ? NV : 1][V], dw[NV][V] = {}, db[NV][V] = {};
+    const auto params = [&](int j, float (&wj)[V]) {
 #pragma unroll
         for (int c = 0; c < V; ++c) {
             const int d = V * (j * TPR + l) + c;
-            w[j][c] = a.weight && d < D ? a.weight[d] : 1.f;
-            dw[j][c] = db[j][c] = 0.f;
+            wj[c] = a.weight && d < D ? a.weight[d] : 1.f;
         }
+    };
+    if constexpr (AHEAD<TPR>)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) params(j, w[j]);
     const float inv_d = 1.f / D;
     const int64_t step = (int64_t)gridDim.x * GROUPS;
     int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR;   // rows and idle groups as in the forward
@@ -151,32 +165,35 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_bwd_kernel(NormBwdA
             }
         }
     };
-    fetch(row);
+    if (AHEAD<TPR>) fetch(row);
     int slot = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step, row += step) {
+        if (!AHEAD<TPR>) fetch(row);
         float v[NV][V], g[NV][V], s = 0.f, sg = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             xr[j].to_f32(v[j]);
             gr[j].to_f32(g[j]);
+            if constexpr (!AHEAD<TPR>) params(j, w[0]);
 #pragma unroll
             for (int c = 0; c < V; ++c) {
                 s += v[j][c];
-                sg = __builtin_fmaf(g[j][c], w[j][c], sg);
+                sg = __builtin_fmaf(g[j][c], w[K * j][c], sg);
             }
         }
-        if (r0 + step < a.rows) fetch(row + step);
+        if (AHEAD<TPR> && r0 + step < a.rows) fetch(row + step);
         group_sum2<TPR>(s, sg, part, slot);
         const float mean = s * inv_d;
         float ss = 0.f, sn = 0.f;   // sum (x - mean)^2, sum g (x - mean)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (V * (j * TPR + l) < D) {
+                if constexpr (!AHEAD<TPR>) params(j, w[0]);
 #pragma unroll
                 for (int c = 0; c < V; ++c) {
                     v[j][c] -= mean;
                     ss = __builtin_fmaf(v[j][c], v[j][c], ss);
-                    sn = __builtin_fmaf(g[j][c] * w[j][c], v[j][c], sn);
+                    sn = __builtin_fmaf(g[j][c] * w[K * j][c], v[j][c], sn);
                 }
             }
         group_sum2<TPR>(ss, sn, part, slot + 1);
@@ -189,12 +206,13 @@ __global__ void __launch_bounds__(BLOCK<TPR>) kda_layer_norm_bwd_kernel(NormBwdA
                 const int d = V * (j * TPR + l);
                 if (d < D) {
                     float o[V];
+                    if constexpr (!AHEAD<TPR>) params(j, w[0]);
 #pragma unroll
                     for (int c = 0; c < V; ++c) {
                         const float n = v[j][c] * r;
                         dw[j][c] = __builtin_fmaf(g[j][c], n, dw[j][c]);
                         db[j][c] += g[j][c];
-                        o[c] = r * (__builtin_fmaf(g[j][c], w[j][c], -c1) - n * c2);
+                        o[c] = r * (__builtin_fmaf(g[j][c], w[K * j][c], -c1) - n * c2);
                     }
                     Pack<T, V>::unstream((T *)a.dx + row * D + d, o);
                 }
@@ -297,7 +315,7 @@ int64_t norm_bwd_workspace_floats(int64_t rows, int D)
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s)
 {
     (void)hipGetLastError();
-    if (a.bf16) return a.D % 8 == 0 ? fwd_v<uint16_t, 8>(a, s) : fwd_v<uint16_t, 1>(a, s);
+    if (a.bf16) return a.D % 8 == 0 ? fwd_v<uint16_t, 8>(a, s) : a.D % 4 == 0 ? fwd_v<uint16_t, 4>(a, s) : fwd_v<uint16_t, 1>(a, s);
     return a.D % 4 == 0 ? fwd_v<float, 4>(a, s) : fwd_v<float, 1>(a, s);
 }
 
@@ -308,7 +326,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs &args, hipStream_t s)
     const bool sums = a.dweight || a.dbias;
     if (!sums) a.ws = nullptr;
     if (a.rows > 0) {
-        const hipError_t e = a.bf16 ? (a.D % 8 == 0 ? bwd_v<uint16_t, 8>(a, s) : bwd_v<uint16_t, 1>(a, s))
+        const hipError_t e = a.bf16 ? (a.D % 8 == 0 ? bwd_v<uint16_t, 8>(a, s) : a.D % 4 == 0 ? bwd_v<uint16_t, 4>(a, s) : bwd_v<uint16_t, 1>(a, s))
                                     : (a.D % 4 == 0 ? bwd_v<float, 4>(a, s) : bwd_v<float, 1>(a, s));
         if (e != hipSuccess || !sums) return e;
     }

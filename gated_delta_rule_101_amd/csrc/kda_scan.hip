@@ -4,20 +4,23 @@
 //   s = softplus(dt + bias),  h[n] <- exp(s A[n]) h[n] + s x B[n],
 //   y = (sum_n C[n] h[n] + D x) silu(z)
 //
-// A lane owns a channel and keeps its states and rates in registers, a
-// wavefront 64 neighbouring channels, so every token's row of x, dt, z and y
-// is read and written in whole 128-byte (bf16) lines, the sum over n stays in
-// the lane, and the token's B and C rows are the same for all lanes: they
-// come through the scalar cache and enter the vector instructions as scalar
-// operands.  One token costs a lane 6 issue slots per state (multiply, exp2
-// at half rate, two products, two sums): the vector units bound it, not HBM.
+// A quad of lanes owns 16 states of a channel, lane j of it states 4 j .. 4 j + 3
+// in registers; a channel has NB quads.  What a channel's token costs once
+// (softplus, gate, conversions) is dealt out over the quad: lane j takes every
+// fourth token and hands its s and s x to the others by DPP quad broadcasts,
+// which ride on the multiplications, and the partial outputs of four tokens meet
+// so that lane j keeps token j's.  B and C rows go through LDS as float32, CHUNK
+// tokens at a time, read as one 16-byte broadcast per token and row.  A state
+// costs 6 issue slots a token (multiply, exp2 at half rate, two products, two
+// sums) and a channel's token about 14 slots a lane besides: the vector units
+// bound it, not HBM.
 //
-// The recurrence is a chain over tokens, and B D / 64 chains do not fill 1024
-// SIMDs.  With a workspace the tokens are cut into segments: a first pass
-// runs all but the last from a zero state (the first from h0) and stores end
-// states and sums of s, a second pass forms each segment's true starting state
-// from those (the decay of a whole segment is exp(A sum s)) and runs it again
-// with the outputs.
+// The recurrence is a chain over tokens, and few channels leave the device idle
+// (B D / 16 NB wavefronts for 1024 SIMDs).  With a workspace the tokens are then
+// cut into segments: a first pass runs all but the last from a zero state (the
+// first from h0) and stores end states and sums of s, a second pass forms each
+// segment's true starting state from those (the decay of a whole segment is
+// exp(A sum s)) and runs it again with the outputs.
 #include "kda_block.h"
 #include "kda_block_device.h"
 
@@ -26,176 +29,16 @@
 namespace kda {
 namespace {
 
-constexpr int UNROLL = 8;   // tokens whose inputs are loaded together, one batch ahead
-
-// Workspace of the segmented forward: slot 0 is a copy of h0 (h_final may be
-// h0 itself, and other wavefronts write it while segment 0 still starts), slot
-// s the state at the end of segment s - 1 and sum[s] that segment's sum of
-// time steps.  States lie as [NP][D]: lanes are neighbouring channels.
-struct Segments {
-    float *slots, *sums;
-    int count, tokens;   // segments, tokens each
-};
-
-template <typename T, int NB, bool FULL, bool STATES_ONLY>
-__global__ void __launch_bounds__(64) kda_scan_kernel(ScanArgs a, const T *__restrict__ Bm, const T *__restrict__ Cm, Segments sg, int tiles)
-{
-    constexpr int NP = 16 * NB;
-    unsigned id = blockIdx.x;
-    const int tile = id % tiles;
-    id /= tiles;
-    const int g = id % a.G;
-    id /= a.G;
-    const int runs = STATES_ONLY ? sg.count - 1 : sg.count;
-    const int seg = id % runs, b = id / runs;
-    const int D = a.D, N = a.N, Dg = D / a.G;
-    const int c = tile * 64 + threadIdx.x;
-    const bool ok = c < Dg;
-    const int d = g * Dg + (ok ? c : Dg - 1);   // idle lanes repeat the last channel
-
-    const int len = seq_length(a.lengths, b, a.T);
-    const int t0 = seg * sg.tokens, t1 = min(t0 + sg.tokens, a.T), te = min(t1, len);
-
-    float A2[NP], h[NP];   // rates in base 2
-#pragma unroll
-    for (int n = 0; n < NP; ++n) A2[n] = n < N ? a.A[(int64_t)d * N + n] * LOG2E : 0.f;
-    float *slots = sg.slots + (int64_t)b * sg.count * NP * D + d;
-    float *sums = sg.sums + (int64_t)b * sg.count * D + d;
-    const int64_t at_state = ((int64_t)b * D + d) * N;
-    if (seg == 0 || sg.count == 1) {
-        if (STATES_ONLY || sg.count == 1) {
-#pragma unroll
-            for (int n = 0; n < NP; ++n) h[n] = a.h0 && n < N ? a.h0[at_state + n] : 0.f;
-            if (STATES_ONLY && ok)
-#pragma unroll
-                for (int n = 0; n < NP; ++n) slots[(int64_t)n * D] = h[n];
-        } else {
-#pragma unroll
-            for (int n = 0; n < NP; ++n) h[n] = slots[(int64_t)n * D];
-        }
-    } else if (STATES_ONLY) {
-#pragma unroll
-        for (int n = 0; n < NP; ++n) h[n] = 0.f;
-    } else {
-#pragma unroll
-        for (int n = 0; n < NP; ++n) h[n] = slots[((int64_t)NP + n) * D];
-        // a few segments' loads together: the chain itself is one multiply-add each
-        constexpr int JOIN = 4 / NB;
-        for (int j = 2; j <= seg; j += JOIN) {
-            float v[JOIN][NP], s[JOIN];
-#pragma unroll
-            for (int i = 0; i < JOIN; ++i) {
-                const int q = min(j + i, seg);
-                s[i] = sums[(int64_t)q * D];
-#pragma unroll
-                for (int n = 0; n < NP; ++n) v[i][n] = slots[((int64_t)q * NP + n) * D];
-            }
-#pragma unroll
-            for (int i = 0; i < JOIN; ++i)
-                if (j + i <= seg)
-#pragma unroll
-                    for (int n = 0; n < NP; ++n) h[n] = __builtin_fmaf(fast_exp2(A2[n] * s[i]), h[n], v[i][n]);
-        }
-    }
-
-    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
-    // Without a gate z reads x, unused: uniform selects below, no branches.
-    const bool gated = a.z != nullptr, soft = a.softplus;
-    const int64_t base = (int64_t)b * a.T * D;   // uniform; a lane adds its channel
-    const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *zb = (const T *)(gated ? a.z : a.x) + base;
-    T *yb = (T *)a.y + base;
-    const int64_t rows = ((int64_t)b * a.T * a.G + g) * N;
-    const T *Bp = Bm + rows, *Cp = Cm + rows;
-    const int64_t row = (int64_t)a.G * N;
-    const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
-
-    float sum = 0.f;
-    if (t0 < te) {
-        T xr[UNROLL], tr[UNROLL], zr[UNROLL];
-        const auto fetch = [&](int t) {
-            const int tf = min(t, te - 1);   // past the end: the last token again, unused
-            const Rows<T> xs(xb + (int64_t)tf * D), ts(tb + (int64_t)tf * D), zs(zb + (int64_t)tf * D);
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                const unsigned o = (unsigned)min(i, te - 1 - tf) * rb;
-                xr[i] = xs.load(dl, o);
-                tr[i] = ts.load(dl, o);
-                if (!STATES_ONLY) zr[i] = zs.load(dl, o);
-            }
-        };
-        fetch(t0);
-        UniformRow<T, NP, FULL> Br, Cr;
-        Br.request(Bp + t0 * row, N);
-        if (!STATES_ONLY) Cr.request(Cp + t0 * row, N);
-        for (int t = t0; t < te; t += UNROLL) {
-            float x[UNROLL], s[UNROLL], z[UNROLL];
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                x[i] = to_f32(xr[i]);
-                s[i] = to_f32(tr[i]) + bias;
-                if (!STATES_ONLY) z[i] = to_f32(zr[i]);
-            }
-            fetch(t + UNROLL);
-            const Rows<T> ys(yb + (int64_t)t * D);
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                const int64_t next = min(t + i + 1, te - 1) * row;
-                float Bv[NP], Cv[NP];
-                Br.take(Bv);
-                Br.arrived();
-                if constexpr (!STATES_ONLY) Cr.take(Cv);
-                scalar_fence();
-                Br.request(Bp + next, N);
-                if constexpr (!STATES_ONLY) Cr.request(Cp + next, N);
-                scalar_fence();
-                const float sp = softplus_f32(s[i]);
-                s[i] = soft ? sp : s[i];
-                if (t + i >= te) s[i] = 0.f;   // behind the end: a token that changes nothing
-                sum += s[i];
-                const float u = s[i] * x[i];
-#pragma unroll
-                for (int n = 0; n < NP; ++n)
-                    h[n] = __builtin_fmaf(fast_exp2(s[i] * A2[n]), h[n], u * Bv[n]);
-                if constexpr (!STATES_ONLY) {
-                    float y0 = 0.f, y1 = 0.f;
-#pragma unroll
-                    for (int n = 0; n < NP; n += 2) {
-                        y0 = __builtin_fmaf(Cv[n], h[n], y0);
-                        y1 = __builtin_fmaf(Cv[n + 1], h[n + 1], y1);
-                    }
-                    const float gate = z[i] * sigmoid_f32(z[i]);
-                    const float y = __builtin_fmaf(skip, x[i], y0 + y1) * (gated ? gate : 1.f);
-                    if (ok && t + i < te) ys.store(from_f32<T>(y), dl, i * rb);
-                }
-            }
-        }
-    }
-    if (!ok) return;
-    if constexpr (STATES_ONLY) {
-        float *q = slots + (int64_t)(seg + 1) * NP * D;
-#pragma unroll
-        for (int n = 0; n < NP; ++n) q[(int64_t)n * D] = h[n];
-        sums[(int64_t)(seg + 1) * D] = sum;
-    } else {
-        for (int t = max(t0, te); t < t1; ++t) Rows<T>(yb + (int64_t)t * D).store(from_f32<T>(0.f), dl, 0);
-        if (a.h_final && seg == sg.count - 1)
-#pragma unroll
-            for (int n = 0; n < NP; ++n)
-                if (n < N) a.h_final[at_state + n] = h[n];
-    }
-}
-
-// One chain per channel with four lanes to it (N <= 16): lane j of a quad owns
-// states 4 j .. 4 j + 3, so there are four times the wavefronts of the kernel
-// above and a token costs each a quarter of the states.  What a channel's token
-// costs once (softplus, gate, conversions) is dealt out over the quad: lane j
-// takes every fourth token and hands its s and u to the others by DPP quad
-// broadcasts, and the partial sums of four tokens' outputs meet so that lane j
-// keeps token j's.  B and C rows go through LDS as float32, CHUNK tokens at a
-// time, read as one 16-byte broadcast per token and row.
 constexpr int CHUNK = 16;
 
 template <int K> struct Const { static constexpr int value = K; };
+template <typename F> __device__ __forceinline__ void each4(F f)
+{
+    f(Const<0>{});
+    f(Const<1>{});
+    f(Const<2>{});
+    f(Const<3>{});
+}
 template <int K> __device__ __forceinline__ float quad_bcast(float x)
 {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), K * 0x55, 0xF, 0xF, true));
@@ -205,36 +48,71 @@ template <int CTRL> __device__ __forceinline__ float quad_add(float x)
     return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
 }
 
-template <typename F> __device__ __forceinline__ void each4(F f)
-{
-    f(Const<0>{});
-    f(Const<1>{});
-    f(Const<2>{});
-    f(Const<3>{});
-}
+// Segments of the forward and their workspace: slot 0 is a copy of h0 (h_final
+// may be h0 itself, and other wavefronts write it while segment 0 still
+// starts), slot s the state at the end of segment s - 1, [B][count][D][NP], and
+// sums[s] that segment's sum of time steps, [B][count][D].
+struct Segments {
+    int count, tokens;   // segments, tokens each (a multiple of CHUNK)
+    float *slots, *sums;
+};
 
-template <typename T>
-__global__ void __launch_bounds__(256) kda_scan_quad_kernel(ScanArgs a, int tiles)
+template <typename T, int NB, bool STATES_ONLY>
+__global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, int tiles)
 {
-    __shared__ __attribute__((aligned(16))) float rows[2][2][CHUNK * 16];   // [buffer][B, C][token][state]
-    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * j;
+    constexpr int NP = 16 * NB, LANES = 4 * NB, CHANNELS = 256 / LANES;
+    __shared__ __attribute__((aligned(16))) float rows[2][2][CHUNK * NP];   // [buffer][B, C][token][state]
+    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * (tid % LANES);
     unsigned id = blockIdx.x;
     const int tile = id % tiles;
     id /= tiles;
-    const int g = id % a.G, b = id / a.G;
+    const int g = id % a.G;
+    id /= a.G;
+    const int runs = STATES_ONLY ? sg.count - 1 : sg.count;
+    const int seg = id % runs, b = id / runs;
     const int D = a.D, N = a.N, Dg = D / a.G;
-    const int c = tile * 64 + tid / 4;
+    const int c = tile * CHANNELS + tid / LANES;
     const bool ok = c < Dg;
-    const int d = g * Dg + (ok ? c : Dg - 1);   // idle quads repeat the last channel
-    const int te = seq_length(a.lengths, b, a.T);
+    const int d = g * Dg + (ok ? c : Dg - 1);   // idle lanes repeat the last channel
+    const int len = seq_length(a.lengths, b, a.T);
+    const int t0 = seg * sg.tokens, t1 = min(t0 + sg.tokens, a.T), te = min(t1, len);
 
-    float A2[4], h[4];
-    const int64_t at_state = ((int64_t)b * D + d) * N + n0;
+    float A2[4], h[4];   // rates in base 2; states
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        A2[n] = n0 + n < N ? a.A[(int64_t)d * N + n0 + n] * LOG2E : 0.f;
-        h[n] = a.h0 && n0 + n < N ? a.h0[at_state + n] : 0.f;
+    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? a.A[(int64_t)d * N + n0 + n] * LOG2E : 0.f;
+    const int64_t at_state = ((int64_t)b * D + d) * N + n0;
+    float *slots = sg.slots + ((int64_t)b * sg.count * D + d) * NP + n0, *sums = sg.sums + (int64_t)b * sg.count * D + d;
+    const int64_t next_slot = (int64_t)D * NP;
+    const auto load_slot = [&](int s, float (&v)[4]) {
+        const float4 q = *reinterpret_cast<const float4 *>(slots + s * next_slot);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    };
+    if (seg == 0 && (STATES_ONLY || sg.count == 1)) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) h[n] = a.h0 && n0 + n < N ? a.h0[at_state + n] : 0.f;
+        if (STATES_ONLY && ok) store4(slots, h);
+    } else if (STATES_ONLY) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) h[n] = 0.f;
+    } else {
+        load_slot(min(seg, 1), h);
+        // a few segments' loads together: the chain itself is one multiply-add each
+        constexpr int JOIN = 8;
+        for (int i = 2; i <= seg; i += JOIN) {
+            float v[JOIN][4], s[JOIN];
+#pragma unroll
+            for (int k = 0; k < JOIN; ++k) {
+                load_slot(min(i + k, seg), v[k]);
+                s[k] = sums[(int64_t)min(i + k, seg) * D];
+            }
+#pragma unroll
+            for (int k = 0; k < JOIN; ++k)
+                if (i + k <= seg)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) h[n] = __builtin_fmaf(fast_exp2(A2[n] * s[k]), h[n], v[k][n]);
+        }
     }
+
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
     const bool gated = a.z != nullptr, soft = a.softplus;   // without a gate z reads x, unused
     const int64_t base = (int64_t)b * a.T * D;
@@ -242,10 +120,11 @@ __global__ void __launch_bounds__(256) kda_scan_quad_kernel(ScanArgs a, int tile
     T *yb = (T *)a.y + base;
     const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
     const int64_t row = (int64_t)a.G * N, row0 = ((int64_t)b * a.T * a.G + g) * N;
-    const int rt = tid / 16, rn = tid & 15;   // staging of B and C: token, state
+    const int rt = tid / 16, rn = tid & 15;   // staging of B and C: token, state of a block
 
-    if (te > 0) {
-        T xr[4], tr[4], zr[4], Br, Cr;
+    float sum = 0.f;   // of this lane's tokens
+    if (t0 < te) {
+        T xr[4], tr[4], zr[4], Br[NB], Cr[NB];
         const auto fetch = [&](int tc) {      // tokens past the end: the last one again, masked later
             const int tf = min(tc, te - 1);
             const int64_t at = (int64_t)tf * D;
@@ -255,45 +134,54 @@ __global__ void __launch_bounds__(256) kda_scan_quad_kernel(ScanArgs a, int tile
                 const unsigned o = (unsigned)min(4 * i + j, te - 1 - tf) * rb + dl;
                 xr[i] = xs.load(o, 0);
                 tr[i] = ts.load(o, 0);
-                zr[i] = zs.load(o, 0);
+                if (!STATES_ONLY) zr[i] = zs.load(o, 0);
             }
-            const int64_t o = row0 + (int64_t)min(tc + rt, te - 1) * row + min(rn, N - 1);
-            Br = ((const T *)a.Bm)[o];
-            Cr = ((const T *)a.Cm)[o];
+            const int64_t o = row0 + (int64_t)min(tc + rt, te - 1) * row;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int st = min(16 * nb + rn, N - 1);
+                Br[nb] = ((const T *)a.Bm)[o + st];
+                if (!STATES_ONLY) Cr[nb] = ((const T *)a.Cm)[o + st];
+            }
         };
-        fetch(0);
-        for (int tc = 0; tc < te; tc += CHUNK) {
-            float (&Bs)[CHUNK * 16] = rows[(tc / CHUNK) & 1][0], (&Cs)[CHUNK * 16] = rows[(tc / CHUNK) & 1][1];
-            Bs[tid] = rn < N ? to_f32(Br) : 0.f;
-            Cs[tid] = rn < N ? to_f32(Cr) : 0.f;
-            float x[4], s[4], z[4];
+        fetch(t0);
+        for (int tc = t0; tc < te; tc += CHUNK) {
+            float (&Bs)[CHUNK * NP] = rows[(tc / CHUNK) & 1][0], (&Cs)[CHUNK * NP] = rows[(tc / CHUNK) & 1][1];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const bool in = 16 * nb + rn < N;
+                Bs[rt * NP + 16 * nb + rn] = in ? to_f32(Br[nb]) : 0.f;
+                if (!STATES_ONLY) Cs[rt * NP + 16 * nb + rn] = in ? to_f32(Cr[nb]) : 0.f;
+            }
+            float x[4], s[4], z[4], u[4], r[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[i] = to_f32(xr[i]);
                 s[i] = to_f32(tr[i]) + bias;
-                z[i] = to_f32(zr[i]);
+                if (!STATES_ONLY) z[i] = to_f32(zr[i]);
             }
             // one barrier a chunk: the buffer written next was last read a chunk earlier
             lds_barrier();
             fetch(tc + CHUNK);
-            float u[4], r[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float sp = softplus_f32(s[i]);
-                s[i] = tc + 4 * i + j < te ? (soft ? sp : s[i]) : 0.f;
+                s[i] = tc + 4 * i + j < te ? (soft ? sp : s[i]) : 0.f;   // behind the end: changes nothing
                 u[i] = s[i] * x[i];
+                sum += s[i];
             }
             // Four tokens at a time: all their rows and decays first, then the
             // chain.  Few wavefronts share a SIMD here, so the order has to give
-            // each instruction independent neighbours; the barriers keep it.
+            // each instruction independent neighbours; the barrier keeps it.
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float4 Bv[4], Cv[4];
                 float e[4][4], y[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) Bv[k] = *reinterpret_cast<const float4 *>(Bs + (4 * i + k) * 16 + n0);
+                for (int k = 0; k < 4; ++k) Bv[k] = *reinterpret_cast<const float4 *>(Bs + (4 * i + k) * NP + n0);
+                if (!STATES_ONLY)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) Cv[k] = *reinterpret_cast<const float4 *>(Cs + (4 * i + k) * 16 + n0);
+                    for (int k = 0; k < 4; ++k) Cv[k] = *reinterpret_cast<const float4 *>(Cs + (4 * i + k) * NP + n0);
                 each4([&](auto k) {
                     constexpr int K = decltype(k)::value;
 #pragma unroll
@@ -311,40 +199,56 @@ __global__ void __launch_bounds__(256) kda_scan_quad_kernel(ScanArgs a, int tile
 #pragma unroll
                     for (int n = 0; n < 4; ++n) e[K][n] = h[n] = __builtin_fmaf(e[K][n], h[n], ub[n]);
                 });
+                if constexpr (!STATES_ONLY) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = Cv[k].x * e[k][0];
+                    for (int k = 0; k < 4; ++k) y[k] = Cv[k].x * e[k][0];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].y, e[k][1], y[k]);
+                    for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].y, e[k][1], y[k]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].z, e[k][2], y[k]);
+                    for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].z, e[k][2], y[k]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].w, e[k][3], y[k]);
-                // lanes with bit 1 keep tokens 2, 3, then lanes with bit 0 the odd one
-                // (every lane takes part in both sums before it chooses)
-                constexpr int SWAP2 = 0x4E, SWAP1 = 0xB1;   // quad_perm [2,3,0,1], [1,0,3,2]
-                const float a0 = quad_add<SWAP2>(y[0]), a1 = quad_add<SWAP2>(y[1]);
-                const float a2 = quad_add<SWAP2>(y[2]), a3 = quad_add<SWAP2>(y[3]);
-                const float p0 = j & 2 ? a2 : a0, p1 = j & 2 ? a3 : a1;
-                const float q0 = quad_add<SWAP1>(p0), q1 = quad_add<SWAP1>(p1);
-                r[i] = j & 1 ? q1 : q0;
+                    for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].w, e[k][3], y[k]);
+                    // lanes with bit 1 keep tokens 2, 3, then lanes with bit 0 the odd one
+                    // (every lane takes part in both sums before it chooses)
+                    constexpr int SWAP2 = 0x4E, SWAP1 = 0xB1;   // quad_perm [2,3,0,1], [1,0,3,2]
+                    const float a0 = quad_add<SWAP2>(y[0]), a1 = quad_add<SWAP2>(y[1]);
+                    const float a2 = quad_add<SWAP2>(y[2]), a3 = quad_add<SWAP2>(y[3]);
+                    const float p0 = j & 2 ? a2 : a0, p1 = j & 2 ? a3 : a1;
+                    const float q0 = quad_add<SWAP1>(p0), q1 = quad_add<SWAP1>(p1);
+                    r[i] = j & 1 ? q1 : q0;
+                    // the channel's other quads
+#pragma unroll
+                    for (int m = 4; m < LANES; m <<= 1) r[i] += __shfl_xor(r[i], m, LANES);
+                }
             }
-            const Rows<T> ys(yb + (int64_t)tc * D);
+            if constexpr (!STATES_ONLY) {
+                const Rows<T> ys(yb + (int64_t)tc * D);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float gate = z[i] * sigmoid_f32(z[i]);
-                r[i] = __builtin_fmaf(skip, x[i], r[i]) * (gated ? gate : 1.f);
+                for (int i = 0; i < 4; ++i) {
+                    const float gate = z[i] * sigmoid_f32(z[i]);
+                    r[i] = __builtin_fmaf(skip, x[i], r[i]) * (gated ? gate : 1.f);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (ok && n0 < 16 && tc + 4 * i + j < te)
+                        ys.store(from_f32<T>(r[i]), (unsigned)(4 * i + j) * rb + dl, 0);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (ok && tc + 4 * i + j < te) ys.store(from_f32<T>(r[i]), (unsigned)(4 * i + j) * rb + dl, 0);
         }
     }
-    if (!ok) return;
-    for (int t = te + j; t < a.T; t += 4) yb[(int64_t)t * D + d] = from_f32<T>(0.f);
-    if (a.h_final)
+    if constexpr (STATES_ONLY) {
+        sum = quad_add<0xB1>(quad_add<0x4E>(sum));   // the quad's tokens
+        if (!ok) return;
+        store4(slots + (seg + 1) * next_slot, h);
+        if (n0 == 0) sums[(int64_t)(seg + 1) * D] = sum;
+    } else {
+        if (!ok) return;
+        if (n0 < 16)
+            for (int t = max(t0, te) + j; t < t1; t += 4) yb[(int64_t)t * D + d] = from_f32<T>(0.f);
+        if (a.h_final && seg == sg.count - 1)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-            if (n0 + n < N) a.h_final[at_state + n] = h[n];
+            for (int n = 0; n < 4; ++n)
+                if (n0 + n < N) a.h_final[at_state + n] = h[n];
+    }
 }
 
 // One token: LPC lanes a channel, 4 states each, so a wavefront's states are
@@ -437,76 +341,65 @@ __global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int64_t 
 }
 
 int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // NB
-int channel_tiles(int D, int G) { return (D / G + 63) / 64; }
+int channel_tiles(int D, int G, int nb) { return (D / G + 64 / nb - 1) / (64 / nb); }   // of a workgroup's channels
 
-// Segments: as many as bring the wavefronts to four a SIMD (4096), at least
-// 32 tokens each (16 take 84 us instead of 64 at B1 T1024 D4096) and at most 64
-// of them (every segment reads the end states of those in front of it).
-Segments plan(int B, int T, int D, int G)
+// Segments: the power of two with the smallest estimated time, in microseconds
+// from timings on MI355X (bfloat16, N = 16).  With w wavefronts a SIMD a token
+// takes max(0.104, 0.03 + 0.067 w) with outputs and max(0.06, 0.02 + 0.05 w)
+// without; a second launch 6; and every segment reads the end states in front of
+// it, in total states x n^2 / 2 at about 20 MB/us.  One segment and the choice
+// measure: B1 T2048 D1024 218 and 31 (32 segments), B1 T16384 D4096 1725 and 477
+// (32), B2 T2048 D4096 215 and 128 (16), B4 T2048 D4096 218 and 230 (8: one is
+// kept).
+Segments plan(int B, int T, int D, int N, int G)
 {
-    const int64_t waves = (int64_t)B * G * channel_tiles(D, G);
-    int64_t n = (4096 + waves - 1) / waves;
-    n = std::min(n, std::min((int64_t)64, (int64_t)(T / 32)));
+    const int nb = state_blocks(N);
+    const double waves = 4.0 * B * G * channel_tiles(D, G, nb) / 1024.0;   // a SIMD, in one segment
+    const double states = 64.0 * nb * B * D / 2.0 / 20e6;                  // bytes of all states / 2 / rate
+    int best = 1;
+    double least = 0.0;
+    for (int n = 1; n <= 128 && (n == 1 || n * 32 <= T); n *= 2) {
+        const double w = waves * n, tokens = (double)T / n;
+        double us = tokens * std::max(0.104, 0.03 + 0.067 * w);
+        if (n > 1) us += tokens * std::max(0.06, 0.02 + 0.05 * w) + 6.0 + 0.03 * n + states * n * n;
+        if (n == 1 || us < least) {
+            best = n;
+            least = us;
+        }
+    }
     Segments s{};
-    s.count = (int)std::max(n, (int64_t)1);
-    s.tokens = (T + s.count - 1) / s.count;
-    if (s.count > 1) s.tokens = (s.tokens + UNROLL - 1) / UNROLL * UNROLL;
+    s.tokens = ((T + best - 1) / best + CHUNK - 1) / CHUNK * CHUNK;
     s.count = s.tokens > 0 ? (T + s.tokens - 1) / s.tokens : 1;
     return s;
 }
 
-// Whether four lanes a channel in one chain beat segments.  From timings on
-// MI355X at N = 16, bfloat16: the chain takes 0.104 us a token while its
-// wavefronts (4 a 64-channel tile) have a SIMD each and 0.03 + 0.067 us per
-// wavefront on a SIMD beyond; the two passes over segments about 14 us plus 0.5
-// us per token and 1024 tiles.  (B1 T64 D4096: 19 against 22 us; B1 T256 D4096:
-// 30 against 28; B2 T2048 D4096: 211 against 149; B3: 212 against 212; B4: 215
-// against 249; B8: 333 against 462.)
-bool quads(int B, int T, int D, int N, int G)
+template <typename T, int NB> hipError_t fwd_launch(const ScanArgs &a, hipStream_t stream)
 {
-    if (N > 16) return false;
-    const double tiles = (double)B * G * channel_tiles(D, G) / 1024.0;
-    const double chain = T * std::max(0.104, 0.03 + 0.067 * 4.0 * tiles);
-    return chain <= 14.0 + 0.5 * T * tiles;
-}
-
-template <typename T, int NB, bool FULL>
-hipError_t fwd_launch(const ScanArgs &a, hipStream_t stream)
-{
-    const int tiles = channel_tiles(a.D, a.G);
-    Segments s = plan(a.B, a.T, a.D, a.G);
-    const bool cut = a.ws && s.count > 1;
-    if (NB == 1 && (!cut || quads(a.B, a.T, a.D, a.N, a.G))) {
-        const int64_t blocks = (int64_t)a.B * a.G * tiles;
-        if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-        kda_scan_quad_kernel<T><<<(unsigned)blocks, 256, 0, stream>>>(a, tiles);
-        return hipGetLastError();
-    }
-    if (!cut) {
+    const int tiles = channel_tiles(a.D, a.G, NB);
+    Segments s = plan(a.B, a.T, a.D, a.N, a.G);
+    if (!a.ws) {
         s.count = 1;
         s.tokens = a.T;
     }
-    const int64_t waves = (int64_t)a.B * a.G * tiles;
-    if (waves * s.count >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    const int64_t blocks = (int64_t)a.B * a.G * tiles;
+    if (blocks * s.count >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     if (s.count > 1) {
         s.slots = a.ws;
         s.sums = a.ws + (int64_t)a.B * s.count * 16 * NB * a.D;
-        kda_scan_kernel<T, NB, FULL, true><<<(unsigned)(waves * (s.count - 1)), 64, 0, stream>>>(
-            a, (const T *)a.Bm, (const T *)a.Cm, s, tiles);
+        kda_scan_kernel<T, NB, true><<<(unsigned)(blocks * (s.count - 1)), 256, 0, stream>>>(a, s, tiles);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    kda_scan_kernel<T, NB, FULL, false><<<(unsigned)(waves * s.count), 64, 0, stream>>>(
-            a, (const T *)a.Bm, (const T *)a.Cm, s, tiles);
+    kda_scan_kernel<T, NB, false><<<(unsigned)(blocks * s.count), 256, 0, stream>>>(a, s, tiles);
     return hipGetLastError();
 }
 
 template <typename T> hipError_t fwd_dispatch(const ScanArgs &a, hipStream_t s)
 {
     switch (state_blocks(a.N)) {
-    case 1: return a.N == 16 ? fwd_launch<T, 1, true>(a, s) : fwd_launch<T, 1, false>(a, s);
-    case 2: return a.N == 32 ? fwd_launch<T, 2, true>(a, s) : fwd_launch<T, 2, false>(a, s);
-    default: return a.N == 64 ? fwd_launch<T, 4, true>(a, s) : fwd_launch<T, 4, false>(a, s);
+    case 1: return fwd_launch<T, 1>(a, s);
+    case 2: return fwd_launch<T, 2>(a, s);
+    default: return fwd_launch<T, 4>(a, s);
     }
 }
 
@@ -538,8 +431,8 @@ template <typename T> hipError_t step_dispatch(const ScanArgs &a, hipStream_t s)
 
 int64_t scan_fwd_workspace_floats(int B, int T, int D, int N, int G)
 {
-    const Segments s = plan(B, T, D, G);
-    return s.count > 1 && !quads(B, T, D, N, G) ? (int64_t)B * s.count * D * (16 * state_blocks(N) + 1) : 0;
+    const Segments s = plan(B, T, D, N, G);
+    return s.count > 1 ? (int64_t)B * s.count * D * (16 * state_blocks(N) + 1) : 0;
 }
 
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t s)

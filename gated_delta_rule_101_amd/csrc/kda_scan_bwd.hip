@@ -87,12 +87,16 @@ Layout layout(float *p, int B, int T, int D, int N, int G)
 
 // --------------------------------------------------- 1. what a segment adds
 
-template <typename T, int NB, bool FULL>
+// A wavefront takes one block of 16 states (states do not meet here).  FULL: the
+// block is whole and its rows of B and C start on 16 elements.
+template <typename T, bool FULL>
 __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a, const T *__restrict__ Bm,
                                                                   const T *__restrict__ Cm, Layout w)
 {
-    constexpr int NP = 16 * NB;
+    constexpr int NP = 16;
     unsigned id = blockIdx.x;
+    const int n0 = 16 * (id % (w.np / 16));
+    id /= w.np / 16;
     const int tile = id % w.tiles;
     id /= w.tiles;
     const int grp = id % a.G;
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
     float A2[NP], h[NP], r[NP], P[NP];
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-        A2[n] = n < N ? a.A[(int64_t)d * N + n] * LOG2E : 0.f;
+        A2[n] = n0 + n < N ? a.A[(int64_t)d * N + n0 + n] * LOG2E : 0.f;
         h[n] = r[n] = 0.f;
         P[n] = 1.f;
     }
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
     const int64_t base = (int64_t)b * a.T * D;   // uniform; a lane adds its channel
     const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *gb = (const T *)a.dy + base;
     const T *zb = (const T *)(gated ? a.z : a.x) + base;
-    const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N, row = (int64_t)a.G * N;
+    const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N + n0, row = (int64_t)a.G * N;
     const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
     const auto store_chunk = [&](int t, float s) {   // a segment's first chunk adds nothing
         if (t % CHUNK == 0 && t > t0 && ok) {
@@ -126,9 +130,9 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
 #pragma unroll
             for (int n = 0; n < NP; n += 4) {
                 const float v[4] = {h[n], h[n + 1], h[n + 2], h[n + 3]};
-                store4(w.hc + at * NP + n, v);
+                store4(w.hc + at * w.np + n0 + n, v);
             }
-            w.sc[at] = s;
+            if (n0 == 0) w.sc[at] = s;
         }
     };
     float sum = 0.f;
@@ -150,8 +154,8 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
         };
         fetch(t0);
         UniformRow<T, NP, FULL> Br, Cr;
-        Br.request(Bm + row0 + t0 * row, N);
-        Cr.request(Cm + row0 + t0 * row, N);
+        Br.request(Bm + row0 + t0 * row, N - n0);
+        Cr.request(Cm + row0 + t0 * row, N - n0);
         for (; t < te; t += UNROLL) {
             store_chunk(t, sum);
             float x[UNROLL], s[UNROLL], gy[UNROLL], z[UNROLL];
@@ -171,8 +175,8 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
                 Br.arrived();
                 Cr.take(Cv);
                 scalar_fence();
-                Br.request(Bm + next, N);
-                Cr.request(Cm + next, N);
+                Br.request(Bm + next, N - n0);
+                Cr.request(Cm + next, N - n0);
                 scalar_fence();
                 const float sp = softplus_f32(s[i]), gate = z[i] * sigmoid_f32(z[i]);
                 s[i] = soft ? sp : s[i];
@@ -196,19 +200,54 @@ __global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a,
 #pragma unroll
     for (int n = 0; n < NP; n += 4) {
         const float hv[4] = {h[n], h[n + 1], h[n + 2], h[n + 3]}, rv[4] = {r[n], r[n + 1], r[n + 2], r[n + 3]};
-        store4(w.h + at * NP + n, hv);
-        store4(w.g + at * NP + n, rv);
+        store4(w.h + at * w.np + n0 + n, hv);
+        store4(w.g + at * w.np + n0 + n, rv);
     }
-    w.sum[at] = sum;
+    if (n0 == 0) w.sum[at] = sum;
 }
 
 // --------------------------------- 2. states in front, gradients behind
 
 // In place: h[seg] becomes the state in front of segment seg, g[seg] the
-// gradient behind it.  A segment's decay is exp(A sum s).
+// gradient behind it.  A segment's decay is exp(A sum s).  A thread walks one
+// (sequence, channel, state) in one direction, the loads of JOIN segments out
+// together and a batch ahead of the chain.
+constexpr int JOIN = 8;
+template <bool BACK>
+__device__ __forceinline__ float join_walk(float *p, const float *sums, int64_t per, int64_t D, int nseg, float A2, float v)
+{
+    const auto at = [&](int i) { return BACK ? nseg - 1 - i : i; };
+    float add[JOIN], s[JOIN];
+    const auto fetch = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k) {
+            const int seg = at(min(i0 + k, nseg - 1));
+            add[k] = p[seg * per];
+            s[k] = sums[seg * D];
+        }
+    };
+    fetch(0);
+    for (int i = 0; i < nseg; i += JOIN) {
+        float e[JOIN], a[JOIN];
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k) {
+            e[k] = fast_exp2(A2 * s[k]);
+            a[k] = add[k];
+        }
+        if (i + JOIN < nseg) fetch(i + JOIN);
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k)
+            if (i + k < nseg) {
+                p[at(i + k) * per] = v;
+                v = __builtin_fmaf(e[k], v, a[k]);
+            }
+    }
+    return v;
+}
+
 __global__ void __launch_bounds__(256) kda_scan_bwd_join_kernel(ScanBwdArgs a, Layout w)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t id = (int64_t)(blockIdx.x >> 1) * 256 + threadIdx.x;
     const int64_t per = (int64_t)a.D * w.np;
     if (id >= a.B * per) return;
     const int b = (int)(id / per);
@@ -216,24 +255,14 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_join_kernel(ScanBwdArgs a, L
     const int d = (int)(dn / w.np), n = (int)(dn % w.np);
     const bool in = n < a.N;
     const float A2 = in ? a.A[(int64_t)d * a.N + n] * LOG2E : 0.f;
-    const int64_t st = ((int64_t)b * a.D + d) * a.N + n;
-    float *hp = w.h + (int64_t)b * w.nseg * per + dn, *gp = w.g + (int64_t)b * w.nseg * per + dn;
-    const float *sp = w.sum + (int64_t)b * w.nseg * a.D + d;
-    float h = in && a.h0 ? a.h0[st] : 0.f;
-#pragma unroll 4
-    for (int s = 0; s < w.nseg; ++s) {
-        const float add = hp[s * per], e = fast_exp2(A2 * sp[(int64_t)s * a.D]);
-        hp[s * per] = h;
-        h = __builtin_fmaf(e, h, add);
+    const int64_t st = ((int64_t)b * a.D + d) * a.N + n, first = (int64_t)b * w.nseg * per + dn;
+    const float *sums = w.sum + (int64_t)b * w.nseg * a.D + d;
+    if (blockIdx.x & 1) {
+        const float g = join_walk<true>(w.g + first, sums, per, a.D, w.nseg, A2, in && a.dh_final ? a.dh_final[st] : 0.f);
+        if (in && a.dh0) a.dh0[st] = g;
+    } else {
+        join_walk<false>(w.h + first, sums, per, a.D, w.nseg, A2, in && a.h0 ? a.h0[st] : 0.f);
     }
-    float g = in && a.dh_final ? a.dh_final[st] : 0.f;
-#pragma unroll 4
-    for (int s = w.nseg - 1; s >= 0; --s) {
-        const float add = gp[s * per], e = fast_exp2(A2 * sp[(int64_t)s * a.D]);
-        gp[s * per] = g;
-        g = __builtin_fmaf(e, g, add);
-    }
-    if (in && a.dh0) a.dh0[st] = g;
 }
 
 // ------------------------------------------------------- 3. the gradients
@@ -313,7 +342,7 @@ __device__ __forceinline__ int piece(int ch, int p) { return ch * 16 + 4 * (p ^ 
 __device__ __forceinline__ int token_at(int ch, int t) { return piece(ch, t >> 2) + (t & 3); }
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(ScanBwdArgs a, Layout w)
+__global__ void __launch_bounds__(256, NB <= 2 ? 2 : 1) kda_scan_bwd_kernel(ScanBwdArgs a, Layout w)
 {
     static_assert(QUADS == 4 && WAVES * QUADS * 4 == CH, "a wavefront's channels");
     static_assert(CHUNK == 16, "a token per lane of a DPP row");
@@ -354,25 +383,32 @@ __global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(Scan
     // Channels behind the group's last repeat it.
     constexpr int SLOTS = NB * CH * 16 / 256, NP = 16 * NB;
     const int c0 = grp * Dg + tile * CH, cmax = Dg - 1 - tile * CH;   // the tile's first channel; last one in it
-    unsigned slot[SLOTS], chan[SLOTS];                                // [channel][np], [channel]
-    float h_seg[SLOTS];                                               // states in front of the segment
+    const auto chan = [&](int k) { return (unsigned)min((k * 256 + tid) / 16 % CH, cmax); };
+    const auto state = [&](int k) { return (unsigned)((k * 256 + tid) / (CH * 16) * 16 + (tid & 15)); };
+    const bool joined = w.nchunk > 1;   // otherwise the segment is the sequence, and its chunk the only one
+    const auto seg_start = [&](int k) -> float {   // state in front of the segment
+        const unsigned c = chan(k), st = state(k);
+        if (joined) return w.h[(bseg * D + c0 + c) * NP + st];
+        return a.h0 && st < N ? a.h0[((int64_t)b * D + c0 + c) * N + st] : 0.f;
+    };
+    // one block of states keeps its segment's start in registers and loads the
+    // chunks' a chunk ahead; more of them would cost a wavefront a SIMD
+    constexpr bool AHEAD = NB == 1;
+    float h_seg[AHEAD ? SLOTS : 1], hr[AHEAD ? SLOTS : 1], sr[AHEAD ? SLOTS : 1];
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
-        const int i = k * 256 + tid, nb = i / (CH * 16), c = min(i / 16 % CH, cmax), st = nb * 16 + (i & 15);
-        chan[k] = c;
-        slot[k] = c * NP + st;
-        const int64_t at = (bseg * D + c0) * NP + slot[k];
-        l_A[nb][i % (CH * 16)] = st < N ? a.A[(int64_t)(c0 + c) * N + st] : 0.f;
-        h_seg[k] = w.h[at];
-        l_g[nb][i % (CH * 16)] = w.g[at];
-        l_dA[nb][i % (CH * 16)] = 0.f;
+        const unsigned c = chan(k), st = state(k);
+        const int64_t own = ((int64_t)b * D + c0 + c) * N + st;   // in dh_final
+        (&l_A[0][0])[k * 256 + tid] = st < N ? a.A[(int64_t)(c0 + c) * N + st] : 0.f;
+        (&l_g[0][0])[k * 256 + tid] = joined ? w.g[(bseg * D + c0 + c) * NP + st] : a.dh_final && st < N ? a.dh_final[own] : 0.f;
+        (&l_dA[0][0])[k * 256 + tid] = 0.f;
+        if constexpr (AHEAD) h_seg[k] = seg_start(k);
     }
     // dB and dC of token 8 (row & 1) of a chunk's first wave-share, this lane's state
     float *const dBC = (lane < 32 ? w.dB : w.dC) + (int64_t)tile * a.B * a.T * row + row0 + 8 * ((lane >> 4) & 1) * row + n;
 
     // raw inputs of one chunk, loaded a chunk ahead
     T xr[4], tr[4], gr[4], zr[4], Br[NB], Cr[NB];
-    float hr[SLOTS], sr[SLOTS];
     const auto fetch = [&](int c) {
         const int tc = t0 + c * CHUNK;
         const int tf = max(min(tc + 4 * wave, len - 1), 0);   // past the end: the last token, masked later
@@ -395,13 +431,14 @@ __global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(Scan
             Br[nb] = Bp[o + st];
             Cr[nb] = Cp[o + st];
         }
-        // (the segment's first chunk has nothing in front of it: its values go unused)
-        const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D + c0;
-        const float *hp = w.hc + at * NP, *sp = w.sc + at;
+        if constexpr (AHEAD) {   // (the segment's first chunk has nothing in front of it: its values go unused)
+            const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D + c0;
+            const float *hp = w.hc + at * NP, *sp = w.sc + at;
 #pragma unroll
-        for (int k = 0; k < SLOTS; ++k) {
-            hr[k] = hp[slot[k]];
-            sr[k] = sp[chan[k]];
+            for (int k = 0; k < SLOTS; ++k) {
+                hr[k] = hp[chan(k) * NP + state(k)];
+                sr[k] = sp[chan(k)];
+            }
         }
     };
     fetch(nch - 1);
@@ -432,10 +469,23 @@ __global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(Scan
             t_C[nb][tid] = in ? to_f32(Cr[nb]) : 0.f;
         }
         // a chunk's start: what the segment added so far, and the rest of its own start
+        const int64_t ca = ((int64_t)b * w.nchunk + tc / CHUNK) * D + c0;
 #pragma unroll
         for (int k = 0; k < SLOTS; ++k) {
-            const int i = k * 256 + tid, nb = i / (CH * 16), at = i % (CH * 16);
-            l_h[nb][at] = c > 0 ? __builtin_fmaf(fast_exp2(l_A[nb][at] * LOG2E * sr[k]), h_seg[k], hr[k]) : h_seg[k];
+            float start, add = 0.f, sum = 0.f;
+            if constexpr (AHEAD) {
+                start = h_seg[k];
+                add = hr[k];
+                sum = sr[k];
+            } else {
+                start = seg_start(k);
+                if (c > 0) {
+                    add = w.hc[(ca + chan(k)) * NP + state(k)];
+                    sum = w.sc[ca + chan(k)];
+                }
+            }
+            const float A2 = (&l_A[0][0])[k * 256 + tid] * LOG2E;
+            (&l_h[0][0])[k * 256 + tid] = c > 0 ? __builtin_fmaf(fast_exp2(A2 * sum), start, add) : start;
         }
         __syncthreads();
         fetch(max(c - 1, 0));
@@ -539,8 +589,10 @@ __global__ void __launch_bounds__(256, NB == 1 ? 2 : 1) kda_scan_bwd_kernel(Scan
     __syncthreads();
     for (int i = tid; i < NB * CH * 16; i += 256) {
         const int nb = i / (CH * 16), c = i / 16 % CH, st = nb * 16 + (i & 15);
-        if (tile * CH + c < Dg && st < N)
+        if (tile * CH + c < Dg && st < N) {
             w.dA[(bseg * D + grp * Dg + tile * CH + c) * N + st] = l_dA[nb][i % (CH * 16)];
+            if (a.dh0 && w.nchunk == 1) a.dh0[((int64_t)b * D + grp * Dg + tile * CH + c) * N + st] = l_g[nb][i % (CH * 16)];
+        }
     }
     t_s[wave * 64 + lane] = dD;
     t_u[wave * 64 + lane] = db;
@@ -567,15 +619,17 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_pass_kernel(const float *in,
 template <typename T, int NB> hipError_t run(const ScanBwdArgs &a, const Layout &w, hipStream_t s)
 {
     const int64_t blocks = (int64_t)a.B * w.nseg * a.G * w.tiles;
-    const int64_t join = ((int64_t)a.B * a.D * w.np + 255) / 256;
-    if (blocks >= ((int64_t)1 << 31) || join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    const int64_t join = ((int64_t)a.B * a.D * w.np + 255) / 256 * 2;
+    if (blocks * NB >= ((int64_t)1 << 31) || join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     const T *Bm = (const T *)a.Bm, *Cm = (const T *)a.Cm;
-    if (a.N == 16 * NB) kda_scan_bwd_segment_kernel<T, NB, true><<<(unsigned)blocks, 64, 0, s>>>(a, Bm, Cm, w);
-    else kda_scan_bwd_segment_kernel<T, NB, false><<<(unsigned)blocks, 64, 0, s>>>(a, Bm, Cm, w);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    kda_scan_bwd_join_kernel<<<(unsigned)join, 256, 0, s>>>(a, w);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipError_t e;
+    if (w.nchunk > 1) {   // a single chunk has nothing in front of it or behind it
+        if (a.N % 16 == 0) kda_scan_bwd_segment_kernel<T, true><<<(unsigned)(blocks * NB), 64, 0, s>>>(a, Bm, Cm, w);
+        else kda_scan_bwd_segment_kernel<T, false><<<(unsigned)(blocks * NB), 64, 0, s>>>(a, Bm, Cm, w);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        kda_scan_bwd_join_kernel<<<(unsigned)join, 256, 0, s>>>(a, w);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     kda_scan_bwd_kernel<T, NB><<<(unsigned)blocks, 256, 0, s>>>(a, w);
     return hipGetLastError();
 }
@@ -608,12 +662,12 @@ hipError_t launch_scan_bwd(const ScanBwdArgs &a, hipStream_t s)
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int64_t parts = (int64_t)a.B * w.nseg, DN = (int64_t)a.D * a.N, rows = (int64_t)a.B * a.T * a.G * a.N;
-    const ColumnSum params[] = {{w.dA, a.dA, parts, DN, DN, false},
-                                {w.dD, a.dDskip, parts, a.D, a.D, false},
-                                {w.db, a.ddt_bias, parts, a.D, a.D, false}};
-    if ((e = launch_column_sums(params, 3, s)) != hipSuccess) return e;
-    const ColumnSum bc[] = {{w.dB, a.dBm, w.tiles, rows, rows, a.bf16}, {w.dC, a.dCm, w.tiles, rows, rows, a.bf16}};
-    return launch_column_sums(bc, 2, s);
+    const ColumnSum jobs[] = {{w.dA, a.dA, parts, DN, DN, false},
+                              {w.dD, a.dDskip, parts, a.D, a.D, false},
+                              {w.db, a.ddt_bias, parts, a.D, a.D, false},
+                              {w.dB, a.dBm, w.tiles, rows, rows, a.bf16},
+                              {w.dC, a.dCm, w.tiles, rows, rows, a.bf16}};
+    return launch_column_sums(jobs, 5, s);
 }
 
 }  // namespace kda
