@@ -105,45 +105,26 @@ __device__ __forceinline__ float softplus_f32(float v) {
     return fmaxf(v, 0.f) + log1p_unit(fast_exp2(-fabsf(v) * LOG2E));
 }
 
-// A token's B or C row, the same for the whole wavefront, requested a token
-// ahead of its use.
-// FULL rows (N = NP) are read as 32-bit words through the scalar cache.  Other
-// N (rows that may start on any element): lane n loads element n once, and each
-// value is handed to all lanes by a lane read; the padding states' values are
-// zero.
-template <typename T, int NP, bool FULL> struct UniformRow {
-    uint32_t w[NP * sizeof(T) / 4];
-    __device__ __forceinline__ void request(const T *p, int) {
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
-#pragma unroll
-        for (int i = 0; i < (int)(NP * sizeof(T) / 4); ++i) w[i] = q[i];
-    }
-    __device__ __forceinline__ void take(float (&o)[NP]) const {
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-            if constexpr (sizeof(T) == 2) o[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-            else o[i] = __uint_as_float(w[i]);
-    }
-    // Scalar loads return in any order, so a wait for one waits for all in
-    // flight: the values asked for have to be waited for before the next
-    // request goes out.
-    __device__ __forceinline__ void arrived() { asm volatile("" : "+s"(w[0])); }
-};
-template <typename T, int NP> struct UniformRow<T, NP, false> {
-    float v;
-    __device__ __forceinline__ void request(const T *p, int N) {
-        const int lane = threadIdx.x & 63;
-        v = lane < N ? kda::to_f32(p[lane]) : 0.f;
-    }
-    __device__ __forceinline__ void take(float (&o)[NP]) const {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) o[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
-    }
-    __device__ __forceinline__ void arrived() {}
-};
-// Keeps scalar memory and scalar arithmetic on its side; vector, LDS and vector
-// memory instructions may pass.
-__device__ __forceinline__ void scalar_fence() { __builtin_amdgcn_sched_barrier(0x2 | 0x10 | 0x80); }
+// ------------------------------------------------------------ quads of lanes
+//
+// A value that lane K of each quad holds, for all four; as an operand it rides
+// on the instruction that uses it.
+template <int K> struct Const { static constexpr int value = K; };
+template <typename F> __device__ __forceinline__ void each4(F f)
+{
+    f(Const<0>{});
+    f(Const<1>{});
+    f(Const<2>{});
+    f(Const<3>{});
+}
+template <int K> __device__ __forceinline__ float quad_bcast(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), K * 0x55, 0xF, 0xF, true));
+}
+template <int CTRL> __device__ __forceinline__ float quad_add(float x)
+{
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
 
 // Tokens of sequence b: lengths[b] clamped to [0, T], or T.
 __device__ __forceinline__ int seq_length(const int *lengths, int b, int T) {

@@ -31,23 +31,6 @@ namespace {
 
 constexpr int CHUNK = 16;
 
-template <int K> struct Const { static constexpr int value = K; };
-template <typename F> __device__ __forceinline__ void each4(F f)
-{
-    f(Const<0>{});
-    f(Const<1>{});
-    f(Const<2>{});
-    f(Const<3>{});
-}
-template <int K> __device__ __forceinline__ float quad_bcast(float x)
-{
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), K * 0x55, 0xF, 0xF, true));
-}
-template <int CTRL> __device__ __forceinline__ float quad_add(float x)
-{
-    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
-}
-
 // Segments of the forward and their workspace: slot 0 is a copy of h0 (h_final
 // may be h0 itself, and other wavefronts write it while segment 0 still
 // starts), slot s the state at the end of segment s - 1, [B][count][D][NP], and

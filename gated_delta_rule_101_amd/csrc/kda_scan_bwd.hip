@@ -11,8 +11,8 @@
 //   dA = sum_t s_t g_t h_{t-1}        dD = sum gy x,   dz = dy (r + D x) silu'(z)
 //
 // Four kernels.
-//  1. Segments of 32 to 128 tokens side by side, a lane a channel as in the forward:
-//     the states it adds (from zero), stored at every chunk of 16 tokens, and,
+//  1. Segments of 32 to 256 tokens side by side, a quad of lanes per 16 states as in
+//     the forward: the states it adds (from zero), stored at every chunk of 16 tokens, and,
 //     with the running decay P_t = prod a, the gradient it adds in front of
 //     itself, sum_t P_t C_t gy_t.  Both directions share each exp.
 //  2. The true state in front of every segment and the true gradient behind it,
@@ -40,7 +40,6 @@ constexpr int CHUNK = 16;        // tokens a chunk: one per lane of a DPP row
 constexpr int CH = 64;           // channels a workgroup
 constexpr int WAVES = 4, QUADS = CH / WAVES / 4;
 
-constexpr int UNROLL = 4;        // tokens whose inputs are loaded together
 
 int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // of 16
 
@@ -87,122 +86,131 @@ Layout layout(float *p, int B, int T, int D, int N, int G)
 
 // --------------------------------------------------- 1. what a segment adds
 
-// A wavefront takes one block of 16 states (states do not meet here).  FULL: the
-// block is whole and its rows of B and C start on 16 elements.
-template <typename T, bool FULL>
-__global__ void __launch_bounds__(64) kda_scan_bwd_segment_kernel(ScanBwdArgs a, const T *__restrict__ Bm,
-                                                                  const T *__restrict__ Cm, Layout w)
+// Lanes, staging and order as in the forward's kernel (kda_scan.hip).
+template <typename T, int NB>
+__global__ void __launch_bounds__(256) kda_scan_bwd_segment_kernel(ScanBwdArgs a, Layout w, int tiles)
 {
-    constexpr int NP = 16;
+    constexpr int NP = 16 * NB, LANES = 4 * NB, CHANNELS = 256 / LANES;
+    __shared__ __attribute__((aligned(16))) float rows[2][2][CHUNK * NP];   // [buffer][B, C][token][state]
+    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * (tid % LANES);
     unsigned id = blockIdx.x;
-    const int n0 = 16 * (id % (w.np / 16));
-    id /= w.np / 16;
-    const int tile = id % w.tiles;
-    id /= w.tiles;
+    const int tile = id % tiles;
+    id /= tiles;
     const int grp = id % a.G;
     id /= a.G;
     const int seg = id % w.nseg, b = id / w.nseg;
     const int D = a.D, N = a.N, Dg = D / a.G;
-    const int c = tile * CH + threadIdx.x;
+    const int c = tile * CHANNELS + tid / LANES;
     const bool ok = c < Dg;
-    const int d = grp * Dg + (ok ? c : Dg - 1);
+    const int d = grp * Dg + (ok ? c : Dg - 1);   // idle lanes repeat the last channel
     const int len = seq_length(a.lengths, b, a.T);
     const int t0 = seg * w.seg, t1 = min(t0 + w.seg, a.T), te = min(t1, len);
 
-    float A2[NP], h[NP], r[NP], P[NP];
+    float A2[4], h[4] = {}, r[4] = {}, P[4] = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        A2[n] = n0 + n < N ? a.A[(int64_t)d * N + n0 + n] * LOG2E : 0.f;
-        h[n] = r[n] = 0.f;
-        P[n] = 1.f;
-    }
+    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? a.A[(int64_t)d * N + n0 + n] * LOG2E : 0.f;
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-    // Without a gate z reads x, unused: uniform selects below, no branches.
-    const bool gated = a.z != nullptr, soft = a.softplus;
-    const int64_t base = (int64_t)b * a.T * D;   // uniform; a lane adds its channel
+    const bool gated = a.z != nullptr, soft = a.softplus;   // without a gate z reads x, unused
+    const int64_t base = (int64_t)b * a.T * D;
     const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *gb = (const T *)a.dy + base;
     const T *zb = (const T *)(gated ? a.z : a.x) + base;
-    const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N + n0, row = (int64_t)a.G * N;
     const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
-    const auto store_chunk = [&](int t, float s) {   // a segment's first chunk adds nothing
-        if (t % CHUNK == 0 && t > t0 && ok) {
-            const int64_t at = ((int64_t)b * w.nchunk + t / CHUNK) * D + d;
-#pragma unroll
-            for (int n = 0; n < NP; n += 4) {
-                const float v[4] = {h[n], h[n + 1], h[n + 2], h[n + 3]};
-                store4(w.hc + at * w.np + n0 + n, v);
-            }
+    const int64_t row = (int64_t)a.G * N, row0 = ((int64_t)b * a.T * a.G + grp) * N;
+    const int rt = tid / 16, rn = tid & 15;   // staging of B and C: token, state of a block
+
+    float sum = 0.f;   // of this lane's tokens
+    const auto quad_sum = [&] { return quad_add<0xB1>(quad_add<0x4E>(sum)); };
+    const auto store_chunk = [&](int tc, float s) {   // a segment's first chunk has nothing in front of it
+        if (tc > t0 && ok) {
+            const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D + d;
+            store4(w.hc + at * NP + n0, h);
             if (n0 == 0) w.sc[at] = s;
         }
     };
-    float sum = 0.f;
-    int t = t0;
-    if (t0 < te) {
-        T xr[UNROLL], tr[UNROLL], gr[UNROLL], zr[UNROLL];
-        const auto fetch = [&](int t) {
-            const int tf = min(t, te - 1);   // past the end: the last token again, unused
-            const int64_t at = (int64_t)tf * D;
-            const Rows<T> xs(xb + at), ts(tb + at), gs(gb + at), zs(zb + at);
+    T xr[4], tr[4], gr[4], zr[4], Br[NB], Cr[NB];
+    const auto fetch = [&](int tc) {      // tokens past the end: the last one again, masked later
+        const int tf = min(tc, te - 1);
+        const int64_t at = (int64_t)tf * D;
+        const Rows<T> xs(xb + at), ts(tb + at), gs(gb + at), zs(zb + at);
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                const unsigned o = (unsigned)min(i, te - 1 - tf) * rb;
-                xr[i] = xs.load(dl, o);
-                tr[i] = ts.load(dl, o);
-                gr[i] = gs.load(dl, o);
-                zr[i] = zs.load(dl, o);
-            }
-        };
-        fetch(t0);
-        UniformRow<T, NP, FULL> Br, Cr;
-        Br.request(Bm + row0 + t0 * row, N - n0);
-        Cr.request(Cm + row0 + t0 * row, N - n0);
-        for (; t < te; t += UNROLL) {
-            store_chunk(t, sum);
-            float x[UNROLL], s[UNROLL], gy[UNROLL], z[UNROLL];
+        for (int i = 0; i < 4; ++i) {
+            const unsigned o = (unsigned)min(4 * i + j, te - 1 - tf) * rb + dl;
+            xr[i] = xs.load(o, 0);
+            tr[i] = ts.load(o, 0);
+            gr[i] = gs.load(o, 0);
+            zr[i] = zs.load(o, 0);
+        }
+        const int64_t o = row0 + (int64_t)min(tc + rt, te - 1) * row;
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                x[i] = to_f32(xr[i]);
-                s[i] = to_f32(tr[i]) + bias;
-                gy[i] = to_f32(gr[i]);
-                z[i] = to_f32(zr[i]);
-            }
-            fetch(t + UNROLL);
+        for (int nb = 0; nb < NB; ++nb) {
+            const int st = min(16 * nb + rn, N - 1);
+            Br[nb] = ((const T *)a.Bm)[o + st];
+            Cr[nb] = ((const T *)a.Cm)[o + st];
+        }
+    };
+    if (t0 < te) fetch(t0);
+    int tc = t0;
+    for (; tc < te; tc += CHUNK) {
+        store_chunk(tc, quad_sum());
+        float (&Bs)[CHUNK * NP] = rows[(tc / CHUNK) & 1][0], (&Cs)[CHUNK * NP] = rows[(tc / CHUNK) & 1][1];
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                const int64_t next = row0 + min(t + i + 1, te - 1) * row;
-                float Bv[NP], Cv[NP];
-                Br.take(Bv);
-                Br.arrived();
-                Cr.take(Cv);
-                scalar_fence();
-                Br.request(Bm + next, N - n0);
-                Cr.request(Cm + next, N - n0);
-                scalar_fence();
-                const float sp = softplus_f32(s[i]), gate = z[i] * sigmoid_f32(z[i]);
-                s[i] = soft ? sp : s[i];
-                gy[i] *= gated ? gate : 1.f;
-                if (t + i >= te) s[i] = gy[i] = 0.f;   // behind the end: a token that changes nothing
-                sum += s[i];
-                const float u = s[i] * x[i];
+        for (int nb = 0; nb < NB; ++nb) {
+            const bool in = 16 * nb + rn < N;
+            Bs[rt * NP + 16 * nb + rn] = in ? to_f32(Br[nb]) : 0.f;
+            Cs[rt * NP + 16 * nb + rn] = in ? to_f32(Cr[nb]) : 0.f;
+        }
+        float s[4], u[4], gy[4];
 #pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    const float e = fast_exp2(s[i] * A2[n]);
-                    h[n] = __builtin_fmaf(e, h[n], u * Bv[n]);
-                    P[n] *= e;
-                    r[n] = __builtin_fmaf(P[n], gy[i] * Cv[n], r[n]);
+        for (int i = 0; i < 4; ++i) {
+            const float v = to_f32(tr[i]) + bias, sp = softplus_f32(v), z = to_f32(zr[i]);
+            const bool in = tc + 4 * i + j < te;   // behind the end: a token that changes nothing
+            s[i] = in ? (soft ? sp : v) : 0.f;
+            u[i] = s[i] * to_f32(xr[i]);
+            gy[i] = in ? to_f32(gr[i]) * (gated ? z * sigmoid_f32(z) : 1.f) : 0.f;
+            sum += s[i];
+        }
+        // one barrier a chunk: the buffer written next was last read a chunk earlier
+        lds_barrier();
+        fetch(tc + CHUNK);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float4 Bv[4], Cv[4];
+            float e[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) Bv[k] = *reinterpret_cast<const float4 *>(Bs + (4 * i + k) * NP + n0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) Cv[k] = *reinterpret_cast<const float4 *>(Cs + (4 * i + k) * NP + n0);
+            each4([&](auto k) {
+                constexpr int K = decltype(k)::value;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) e[K][n] = quad_bcast<K>(s[i]) * A2[n];
+            });
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) e[k][n] = fast_exp2(e[k][n]);
+            __builtin_amdgcn_sched_barrier(0);
+            each4([&](auto k) {
+                constexpr int K = decltype(k)::value;
+                const float ub[4] = {quad_bcast<K>(u[i]) * Bv[K].x, quad_bcast<K>(u[i]) * Bv[K].y,
+                                     quad_bcast<K>(u[i]) * Bv[K].z, quad_bcast<K>(u[i]) * Bv[K].w};
+                const float gc[4] = {quad_bcast<K>(gy[i]) * Cv[K].x, quad_bcast<K>(gy[i]) * Cv[K].y,
+                                     quad_bcast<K>(gy[i]) * Cv[K].z, quad_bcast<K>(gy[i]) * Cv[K].w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    h[n] = __builtin_fmaf(e[K][n], h[n], ub[n]);
+                    P[n] *= e[K][n];
+                    r[n] = __builtin_fmaf(P[n], gc[n], r[n]);
                 }
-            }
+            });
         }
     }
-    for (; t < t1; t += UNROLL) store_chunk(t, sum);
+    sum = quad_sum();
+    for (; tc < t1; tc += CHUNK) store_chunk(tc, sum);
     if (!ok) return;
-    const int64_t at = (((int64_t)b * w.nseg + seg) * D + d);
-#pragma unroll
-    for (int n = 0; n < NP; n += 4) {
-        const float hv[4] = {h[n], h[n + 1], h[n + 2], h[n + 3]}, rv[4] = {r[n], r[n + 1], r[n + 2], r[n + 3]};
-        store4(w.h + at * w.np + n0 + n, hv);
-        store4(w.g + at * w.np + n0 + n, rv);
-    }
+    const int64_t at = ((int64_t)b * w.nseg + seg) * D + d;
+    store4(w.h + at * NP + n0, h);
+    store4(w.g + at * NP + n0, r);
     if (n0 == 0) w.sum[at] = sum;
 }
 
@@ -620,12 +628,13 @@ template <typename T, int NB> hipError_t run(const ScanBwdArgs &a, const Layout 
 {
     const int64_t blocks = (int64_t)a.B * w.nseg * a.G * w.tiles;
     const int64_t join = ((int64_t)a.B * a.D * w.np + 255) / 256 * 2;
-    if (blocks * NB >= ((int64_t)1 << 31) || join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    const T *Bm = (const T *)a.Bm, *Cm = (const T *)a.Cm;
+    if (blocks >= ((int64_t)1 << 31) || join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     hipError_t e;
     if (w.nchunk > 1) {   // a single chunk has nothing in front of it or behind it
-        if (a.N % 16 == 0) kda_scan_bwd_segment_kernel<T, true><<<(unsigned)(blocks * NB), 64, 0, s>>>(a, Bm, Cm, w);
-        else kda_scan_bwd_segment_kernel<T, false><<<(unsigned)(blocks * NB), 64, 0, s>>>(a, Bm, Cm, w);
+        const int tiles = (a.D / a.G + 64 / NB - 1) / (64 / NB);
+        const int64_t segments = (int64_t)a.B * w.nseg * a.G * tiles;
+        if (segments >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+        kda_scan_bwd_segment_kernel<T, NB><<<(unsigned)segments, 256, 0, s>>>(a, w, tiles);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         kda_scan_bwd_join_kernel<<<(unsigned)join, 256, 0, s>>>(a, w);
         if ((e = hipGetLastError()) != hipSuccess) return e;

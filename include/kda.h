@@ -462,7 +462,7 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const void *v, const vo
  *    D below 2^24 each (KDA_ERR_UNSUPPORTED beyond).
  *  - lengths [B] int32 (device, or NULL: all T) are the sequences' lengths in
  *    a right-padded batch, clamped to [0, T].  Tokens behind a sequence's end
- *    are never read (they may hold anything, NaN included); their outputs and
+ *    enter no result (they may hold anything, NaN included); their outputs and
  *    their gradients are written as zeros, and final states are those after
  *    the last real token.
  *  - A workspace is device memory owned by the caller, 16-byte aligned, of at
@@ -541,8 +541,7 @@ kda_status_t kda_short_conv_bwd(const void *dy, const void *x, const float *w, c
  *            does not fill the device)
  *
  * N from 1 to 64, G >= 1 dividing D (KDA_ERR_INVALID_ARG if it does not);
- * 16, 32 and 64 states run fastest, other counts are padded to them.  G N below
- * 2^24.
+ * the states are padded to 16, 32 or 64.  G N below 2^24.
  */
 size_t kda_selective_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G);
 

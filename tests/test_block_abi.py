@@ -100,6 +100,7 @@ def test_scan_refusals(lib, st):
         assert fwd(**{k: -2}) == INV and fwd(**{k: 1 << 24}) == UNS, k
     assert fwd(N=0) == INV and fwd(N=65) == UNS and fwd(G=0) == INV and fwd(G=5) == INV
     assert fwd(B=1 << 23, T=1, D=1 << 14, G=1) == UNS     # states past 2^40 elements
+    assert fwd(D=1 << 21, G=1 << 20, B=1, T=1) == UNS     # rows of B and C past 2^24 elements
     assert fwd(dtype=3) == INV
     assert fwd(B=0) == OK and fwd(D=0) == OK and fwd(T=0, hf=None) == OK
 

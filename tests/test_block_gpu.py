@@ -1,7 +1,7 @@
 """GPU parity of the short convolution, the selective scan and layer norm with
 their plain float64 forms, each value within the bound that those carry along
-(tests/block_reference.py).  Tokens behind a sequence's end hold NaN: they must
-not be read, and their outputs and gradients are zeros."""
+(tests/block_reference.py).  Tokens behind a sequence's end hold NaN: they enter
+no result, and their outputs and gradients are zeros."""
 
 import pytest
 import torch
@@ -54,6 +54,7 @@ CONV = [  # B, T, D, W, dtype, state, ragged, silu
     (2, 5, 100, 4, BF, True, False, True), (1, 64, 64, 4, BF, False, False, True),
     (5, 67, 40, 3, BF, True, True, True), (3, 300, 33, 2, F32, True, True, True),
     (2, 513, 256, 4, BF, True, False, True), (1, 1000, 1000, 4, F32, False, False, True),
+    (3, 1500, 5, 4, F32, True, True, True),   # more runs than one pass of the column sums takes
 ]
 CONV_IDS = [f"B{c[0]}_T{c[1]}_D{c[2]}_W{c[3]}_{'bf16' if c[4] == BF else 'f32'}{'_s0' * c[5]}{'_len' * c[6]}"
             for c in CONV]
@@ -136,6 +137,9 @@ SCAN = [  # B, T, D, N, G, dtype, states, ragged, gated, softplus
     (3, 257, 40, 17, 1, BF, True, True, True, True), (1, 300, 128, 32, 2, F32, True, False, False, True),
     (2, 100, 24, 33, 2, BF, True, True, True, True), (1, 150, 70, 64, 1, BF, True, False, True, True),
     (5, 385, 72, 16, 1, BF, True, True, True, True), (1, 1000, 130, 16, 1, F32, False, False, True, True),
+    (2, 700, 20, 53, 1, BF, True, True, True, True), (3, 40, 5, 16, 5, F32, True, True, True, True),
+    (9, 4000, 3, 2, 1, F32, True, True, True, True),      # parameters' gradients over more than 1024 segments
+    (2, 4100, 8, 16, 1, BF, False, False, True, True),    # B and C rows by the wide column sum
 ]
 SCAN_IDS = [f"B{c[0]}_T{c[1]}_D{c[2]}_N{c[3]}_G{c[4]}_{'bf16' if c[5] == BF else 'f32'}{'_h0' * c[6]}{'_len' * c[7]}"
             for c in SCAN]
