@@ -102,6 +102,9 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
     const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *zb = (const T *)(gated ? a.z : a.x) + base;
     T *yb = (T *)a.y + base;
     const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
+    unsigned off[4];   // of the lane's tokens in a chunk
+#pragma unroll
+    for (int i = 0; i < 4; ++i) off[i] = (unsigned)(4 * i + j) * rb + dl;
     const int64_t row = (int64_t)a.G * N, row0 = ((int64_t)b * a.T * a.G + g) * N;
     const int rt = tid / 16, rn = tid & 15;   // staging of B and C: token, state of a block
 
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
             const Rows<T> xs(xb + at), ts(tb + at), zs(zb + at);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const unsigned o = (unsigned)min(4 * i + j, te - 1 - tf) * rb + dl;
+                const unsigned o = tf + CHUNK <= te ? off[i] : (unsigned)min(4 * i + j, te - 1 - tf) * rb + dl;
                 xr[i] = xs.load(o, 0);
                 tr[i] = ts.load(o, 0);
                 if (!STATES_ONLY) zr[i] = zs.load(o, 0);
@@ -211,10 +214,16 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
                     const float gate = z[i] * sigmoid_f32(z[i]);
                     r[i] = __builtin_fmaf(skip, x[i], r[i]) * (gated ? gate : 1.f);
                 }
+                if (ok && n0 < 16) {
+                    if (tc + CHUNK <= te) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (ok && n0 < 16 && tc + 4 * i + j < te)
-                        ys.store(from_f32<T>(r[i]), (unsigned)(4 * i + j) * rb + dl, 0);
+                        for (int i = 0; i < 4; ++i) ys.store(from_f32<T>(r[i]), off[i], 0);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (tc + 4 * i + j < te) ys.store(from_f32<T>(r[i]), off[i], 0);
+                    }
+                }
             }
         }
     }

@@ -115,6 +115,9 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_segment_kernel(ScanBwdArgs a
     const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *gb = (const T *)a.dy + base;
     const T *zb = (const T *)(gated ? a.z : a.x) + base;
     const unsigned dl = (unsigned)d * sizeof(T), rb = (unsigned)D * sizeof(T);   // lane, row: bytes
+    unsigned off[4];   // of the lane's tokens in a chunk
+#pragma unroll
+    for (int i = 0; i < 4; ++i) off[i] = (unsigned)(4 * i + j) * rb + dl;
     const int64_t row = (int64_t)a.G * N, row0 = ((int64_t)b * a.T * a.G + grp) * N;
     const int rt = tid / 16, rn = tid & 15;   // staging of B and C: token, state of a block
 
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_segment_kernel(ScanBwdArgs a
         const Rows<T> xs(xb + at), ts(tb + at), gs(gb + at), zs(zb + at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned o = (unsigned)min(4 * i + j, te - 1 - tf) * rb + dl;
+            const unsigned o = tf + CHUNK <= te ? off[i] : (unsigned)min(4 * i + j, te - 1 - tf) * rb + dl;
             xr[i] = xs.load(o, 0);
             tr[i] = ts.load(o, 0);
             gr[i] = gs.load(o, 0);
