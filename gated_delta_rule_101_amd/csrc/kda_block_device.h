@@ -100,7 +100,7 @@ __device__ __forceinline__ float log1p_unit(float e) {
     p = __builtin_fmaf(q, p, 1.f);
     return 2.f * r * p;
 }
-// softplus(v) = max(v, 0) + log(1 + exp(-|v|)); `sig` is its derivative, the sigmoid of v.
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)).
 __device__ __forceinline__ float softplus_f32(float v) {
     return fmaxf(v, 0.f) + log1p_unit(fast_exp2(-fabsf(v) * LOG2E));
 }

