@@ -29,6 +29,7 @@
 #include "kda_block_device.h"
 
 #include <algorithm>
+#include <cfloat>
 
 namespace kda {
 namespace {
@@ -43,6 +44,11 @@ struct Segments {
     int count, tokens;   // segments, tokens each (a multiple of CHUNK)
     float *slots, *sums;
 };
+
+// A rate of -infinity (-exp of a large number) forgets at once; held finite, it
+// still does at every positive step and leaves a token of step 0, such as those
+// behind a sequence's end, a token that changes nothing.
+__device__ __forceinline__ float finite_rate(float A2) { return A2 < -FLT_MAX ? -FLT_MAX : A2; }
 
 template <typename T, int NB, bool STATES_ONLY>
 __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, int tiles)
@@ -66,7 +72,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
 
     float A2[4], h[4];   // rates in base 2; states
 #pragma unroll
-    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? a.A[(int64_t)d * N + n0 + n] * LOG2E : 0.f;
+    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? finite_rate(a.A[(int64_t)d * N + n0 + n] * LOG2E) : 0.f;
     const int64_t at_state = ((int64_t)b * D + d) * N + n0;
     float *slots = sg.slots + ((int64_t)b * sg.count * D + d) * NP + n0, *sums = sg.sums + (int64_t)b * sg.count * D + d;
     const int64_t next_slot = (int64_t)D * NP;
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
             float (&Bs)[CHUNK * NP] = rows[(tc / CHUNK) & 1][0], (&Cs)[CHUNK * NP] = rows[(tc / CHUNK) & 1][1];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const bool in = 16 * nb + rn < N;
+                const bool in = 16 * nb + rn < N && tc + rt < te;
                 Bs[rt * NP + 16 * nb + rn] = in ? to_f32(Br[nb]) : 0.f;
                 if (!STATES_ONLY) Cs[rt * NP + 16 * nb + rn] = in ? to_f32(Cr[nb]) : 0.f;
             }
@@ -156,10 +162,17 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float sp = softplus_f32(s[i]);
-                s[i] = tc + 4 * i + j < te ? (soft ? sp : s[i]) : 0.f;   // behind the end: changes nothing
+                s[i] = soft ? sp : s[i];
                 u[i] = s[i] * x[i];
-                sum += s[i];
             }
+            // Tokens behind the end change nothing: no step and no input.  (Their
+            // B rows are zeros and every rate is finite, so 0 times them is 0.)
+            if (tc + CHUNK > te)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (tc + 4 * i + j >= te) s[i] = u[i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += s[i];
             // Four tokens at a time: all their rows and decays first, then the
             // chain.  Few wavefronts share a SIMD here, so the order has to give
             // each instruction independent neighbours; the barrier keeps it.

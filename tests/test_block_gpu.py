@@ -293,6 +293,38 @@ def test_scan_extreme_steps_and_rates(kda):
     ref.check(h, rh, Eh, F32, "h")
 
 
+@pytest.mark.parametrize("T", [21, 700])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_scan_infinite_last_token_and_rate(kda, T, ragged):
+    """The places behind a sequence's last token, which share a chunk with it,
+    multiply nothing into the state: an infinite input stays infinite there, and a
+    rate of -infinity forgets and leaves the last token's own part."""
+    c = (2, T, 40, 16, 1, F32, True, ragged, True, True)
+    p, _, _, _, _ = _scan_case(c)
+    last = [T - 1, T - 7] if ragged else [T - 1, T - 1]
+    lengths = torch.tensor([n + 1 for n in last], dtype=torch.int32) if ragged else None
+    for k in ("x", "dt", "z", "Bm", "Cm"):
+        p[k] = torch.nan_to_num(p[k], nan=0.5)
+    for b, t in enumerate(last):
+        p["x"][b, t, 3] = float("inf")
+    p["A"][5] = float("-inf")
+    if ragged:
+        for k in ("x", "dt", "z", "Bm", "Cm"):
+            p[k][1, last[1] + 1:] = float("nan")
+    y, h = _scan_call(kda, p, True, _dev(lengths))
+    torch.cuda.synchronize()
+    for b, t in enumerate(last):
+        assert torch.equal(h[b, 3].cpu(), torch.sign(p["Bm"][b, t, 0]) * float("inf"))
+    # the other channels: a rate that every positive step turns into a factor 0
+    p["A"][5] = -1e30
+    for b, t in enumerate(last):
+        p["x"][b, t, 3] = 0.0
+    (ry, Ey), (rh, Eh), _ = ref.scan_fwd(*_scan_ref(p), True, lengths)
+    keep = [d for d in range(40) if d != 3]
+    ref.check(y[..., keep], ry[..., keep], Ey[..., keep], F32, "y")
+    ref.check(h[:, keep], rh[:, keep], Eh[:, keep], F32, "h_final")
+
+
 # ------------------------------------------------------------- layer norm
 
 NORM = [(1, 1, F32), (3, 7, BF), (37, 1111, F32), (5, 16, BF), (17, 64, BF), (9, 256, F32), (300, 257, BF),
