@@ -24,6 +24,10 @@ import torch
 
 from .kda import _dtype_code, _nbytes, _ptr, _raise, load_library
 
+# Handle of the current stream of a device.  The public form builds a Stream
+# object for it: 1.1 us against 0.1, in calls of 8 us for the smallest operators.
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # (a torch without GPUs has none)
+
 
 class _on:
     """Makes the tensors' device, and `stream` if one is given, current inside
@@ -38,7 +42,7 @@ class _on:
         if stream is None:
             if torch.cuda.current_device() != device.index:
                 self.inner = torch.cuda.device(device)
-            self.handle = torch.cuda.current_stream(device.index).cuda_stream
+            self.handle = _stream_handle(device.index)
         else:
             if stream.device != device:
                 raise ValueError("stream must be of the tensors' device")
