@@ -4,8 +4,8 @@
 //   s = softplus(dt + bias),  h[n] <- exp(s A[n]) h[n] + s x B[n],
 //   y = (sum_n C[n] h[n] + D x) silu(z)
 //
-// A quad of lanes owns 16 states of a channel, lane j of it states 4 j .. 4 j + 3
-// in registers; a channel has NB quads.  What a channel's token costs once
+// A quad of lanes owns a channel, lane j of it states 4 j .. 4 j + 3 of each 16
+// in registers.  What a channel's token costs once
 // (softplus, gate, conversions) is dealt out over the quad: lane j takes every
 // fourth token and hands its s and s x to the others by DPP quad broadcasts,
 // which ride on the multiplications, and the partial outputs of four tokens meet
@@ -16,14 +16,15 @@
 // bound it, not HBM.
 //
 // The recurrence is a chain over tokens, and few channels leave the device idle
-// (B D / 16 NB wavefronts for 1024 SIMDs).  With a workspace the tokens are then
+// (B D / 16 wavefronts for 1024 SIMDs).  With a workspace the tokens are then
 // cut into segments: a first pass runs all but the last from a zero state (the
 // first from h0) and stores end states and sums of s, a second pass forms each
 // segment's true starting state from those (the decay of a whole segment is
 // exp(A sum s)) and runs it again with the outputs.
 //
 // Measured (bfloat16, N = 16): B4 T4096 D4096, one chain of 1024 wavefronts, 0.426
-// ms; B1 T16384 D4096, 32 segments, 0.471 ms; one token of B256 D12288 0.101 ms, 4.2
+// ms (8.3 vector instructions a state and token; four wavefronts a SIMD would
+// take 0.31); B1 T16384 D4096, 32 segments, 0.467 ms; one token of B256 D12288 0.101 ms, 4.2
 // TB/s.
 #include "kda_block.h"
 #include "kda_block_device.h"
@@ -53,9 +54,9 @@ __device__ __forceinline__ float finite_rate(float A2) { return A2 < -FLT_MAX ? 
 template <typename T, int NB, bool STATES_ONLY>
 __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, int tiles)
 {
-    constexpr int NP = 16 * NB, LANES = 4 * NB, CHANNELS = 256 / LANES;
+    constexpr int NP = 16 * NB, CHANNELS = 64;
     __shared__ __attribute__((aligned(16))) float rows[2][2][CHUNK * NP];   // [buffer][B, C][token][state]
-    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * (tid % LANES);
+    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * j;   // lane of the quad; its first state of each 16
     unsigned id = blockIdx.x;
     const int tile = id % tiles;
     id /= tiles;
@@ -64,45 +65,56 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
     const int runs = STATES_ONLY ? sg.count - 1 : sg.count;
     const int seg = id % runs, b = id / runs;
     const int D = a.D, N = a.N, Dg = D / a.G;
-    const int c = tile * CHANNELS + tid / LANES;
+    const int c = tile * CHANNELS + tid / 4;
     const bool ok = c < Dg;
     const int d = g * Dg + (ok ? c : Dg - 1);   // idle lanes repeat the last channel
     const int len = seq_length(a.lengths, b, a.T);
     const int t0 = seg * sg.tokens, t1 = min(t0 + sg.tokens, a.T), te = min(t1, len);
 
-    float A2[4], h[4];   // rates in base 2; states
+    // states n0 + 16 m + n: rates in base 2, values
+    float A2[NB][4], h[NB][4];
+    const auto each_state = [&](auto f) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? finite_rate(a.A[(int64_t)d * N + n0 + n] * LOG2E) : 0.f;
-    const int64_t at_state = ((int64_t)b * D + d) * N + n0;
+        for (int m = 0; m < NB; ++m)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) f(m, n, n0 + 16 * m + n);
+    };
+    each_state([&](int m, int n, int st) { A2[m][n] = st < N ? finite_rate(a.A[(int64_t)d * N + st] * LOG2E) : 0.f; });
+    const int64_t at_state = ((int64_t)b * D + d) * N;
     float *slots = sg.slots + ((int64_t)b * sg.count * D + d) * NP + n0, *sums = sg.sums + (int64_t)b * sg.count * D + d;
     const int64_t next_slot = (int64_t)D * NP;
-    const auto load_slot = [&](int s, float (&v)[4]) {
-        const float4 q = *reinterpret_cast<const float4 *>(slots + s * next_slot);
+    const auto load_slot = [&](int s, int m, float (&v)[4]) {
+        const float4 q = *reinterpret_cast<const float4 *>(slots + s * next_slot + 16 * m);
         v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
     };
+    const auto store_slot = [&](int s) {
+#pragma unroll
+        for (int m = 0; m < NB; ++m) store4(slots + s * next_slot + 16 * m, h[m]);
+    };
     if (seg == 0 && (STATES_ONLY || sg.count == 1)) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) h[n] = a.h0 && n0 + n < N ? a.h0[at_state + n] : 0.f;
-        if (STATES_ONLY && ok) store4(slots, h);
+        each_state([&](int m, int n, int st) { h[m][n] = a.h0 && st < N ? a.h0[at_state + st] : 0.f; });
+        if (STATES_ONLY && ok) store_slot(0);
     } else if (STATES_ONLY) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) h[n] = 0.f;
+        each_state([&](int m, int n, int) { h[m][n] = 0.f; });
     } else {
-        load_slot(min(seg, 1), h);
+#pragma unroll
+        for (int m = 0; m < NB; ++m) load_slot(min(seg, 1), m, h[m]);
         // a few segments' loads together: the chain itself is one multiply-add each
-        constexpr int JOIN = 8;
+        constexpr int JOIN = 8 / NB;
         for (int i = 2; i <= seg; i += JOIN) {
-            float v[JOIN][4], s[JOIN];
+            float v[JOIN][NB][4], s[JOIN];
 #pragma unroll
             for (int k = 0; k < JOIN; ++k) {
-                load_slot(min(i + k, seg), v[k]);
+#pragma unroll
+                for (int m = 0; m < NB; ++m) load_slot(min(i + k, seg), m, v[k][m]);
                 s[k] = sums[(int64_t)min(i + k, seg) * D];
             }
 #pragma unroll
             for (int k = 0; k < JOIN; ++k)
                 if (i + k <= seg)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) h[n] = __builtin_fmaf(fast_exp2(A2[n] * s[k]), h[n], v[k][n]);
+                    each_state([&](int m, int n, int) {
+                        h[m][n] = __builtin_fmaf(fast_exp2(A2[m][n] * s[k]), h[m][n], v[k][m][n]);
+                    });
         }
     }
 
@@ -173,44 +185,51 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
                     if (tc + 4 * i + j >= te) s[i] = u[i] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum += s[i];
-            // Four tokens at a time: all their rows and decays first, then the
-            // chain.  Few wavefronts share a SIMD here, so the order has to give
-            // each instruction independent neighbours; the barrier keeps it.
+            // Four tokens and states of a lane at a time: all their rows and decays
+            // first, then the chain.  Few wavefronts share a SIMD here, so the order
+            // has to give each instruction independent neighbours; the barrier keeps it.
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float4 Bv[4], Cv[4];
-                float e[4][4], y[4];
+                float y[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) Bv[k] = *reinterpret_cast<const float4 *>(Bs + (4 * i + k) * NP + n0);
-                if (!STATES_ONLY)
+                for (int m = 0; m < NB; ++m) {
+                    float4 Bv[4], Cv[4];
+                    float e[4][4];
+                    const int at = 4 * i * NP + 16 * m + n0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) Cv[k] = *reinterpret_cast<const float4 *>(Cs + (4 * i + k) * NP + n0);
-                each4([&](auto k) {
-                    constexpr int K = decltype(k)::value;
+                    for (int k = 0; k < 4; ++k) Bv[k] = *reinterpret_cast<const float4 *>(Bs + at + k * NP);
+                    if (!STATES_ONLY)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) e[K][n] = quad_bcast<K>(s[i]) * A2[n];
-                });
+                        for (int k = 0; k < 4; ++k) Cv[k] = *reinterpret_cast<const float4 *>(Cs + at + k * NP);
+                    each4([&](auto k) {
+                        constexpr int K = decltype(k)::value;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                        for (int n = 0; n < 4; ++n) e[K][n] = quad_bcast<K>(s[i]) * A2[m][n];
+                    });
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) e[k][n] = fast_exp2(e[k][n]);
-                __builtin_amdgcn_sched_barrier(0);
-                each4([&](auto k) {
-                    constexpr int K = decltype(k)::value;
-                    const float ub[4] = {quad_bcast<K>(u[i]) * Bv[K].x, quad_bcast<K>(u[i]) * Bv[K].y,
-                                         quad_bcast<K>(u[i]) * Bv[K].z, quad_bcast<K>(u[i]) * Bv[K].w};
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) e[K][n] = h[n] = __builtin_fmaf(e[K][n], h[n], ub[n]);
-                });
+                        for (int n = 0; n < 4; ++n) e[k][n] = fast_exp2(e[k][n]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    each4([&](auto k) {
+                        constexpr int K = decltype(k)::value;
+                        const float ub[4] = {quad_bcast<K>(u[i]) * Bv[K].x, quad_bcast<K>(u[i]) * Bv[K].y,
+                                             quad_bcast<K>(u[i]) * Bv[K].z, quad_bcast<K>(u[i]) * Bv[K].w};
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) e[K][n] = h[m][n] = __builtin_fmaf(e[K][n], h[m][n], ub[n]);
+                    });
+                    if constexpr (!STATES_ONLY) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[k] = m ? __builtin_fmaf(Cv[k].x, e[k][0], y[k]) : Cv[k].x * e[k][0];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].y, e[k][1], y[k]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].z, e[k][2], y[k]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].w, e[k][3], y[k]);
+                    }
+                }
                 if constexpr (!STATES_ONLY) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = Cv[k].x * e[k][0];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].y, e[k][1], y[k]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].z, e[k][2], y[k]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(Cv[k].w, e[k][3], y[k]);
                     // lanes with bit 1 keep tokens 2, 3, then lanes with bit 0 the odd one
                     // (every lane takes part in both sums before it chooses)
                     constexpr int SWAP2 = 0x4E, SWAP1 = 0xB1;   // quad_perm [2,3,0,1], [1,0,3,2]
@@ -219,9 +238,6 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
                     const float p0 = j & 2 ? a2 : a0, p1 = j & 2 ? a3 : a1;
                     const float q0 = quad_add<SWAP1>(p0), q1 = quad_add<SWAP1>(p1);
                     r[i] = j & 1 ? q1 : q0;
-                    // the channel's other quads
-#pragma unroll
-                    for (int m = 4; m < LANES; m <<= 1) r[i] += __shfl_xor(r[i], m, LANES);
                 }
             }
             if constexpr (!STATES_ONLY) {
@@ -231,7 +247,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
                     const float gate = z[i] * sigmoid_f32(z[i]);
                     r[i] = __builtin_fmaf(skip, x[i], r[i]) * (gated ? gate : 1.f);
                 }
-                if (ok && n0 < 16) {
+                if (ok) {
                     if (tc + CHUNK <= te) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) ys.store(from_f32<T>(r[i]), off[i], 0);
@@ -247,16 +263,15 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
     if constexpr (STATES_ONLY) {
         sum = quad_add<0xB1>(quad_add<0x4E>(sum));   // the quad's tokens
         if (!ok) return;
-        store4(slots + (seg + 1) * next_slot, h);
-        if (n0 == 0) sums[(int64_t)(seg + 1) * D] = sum;
+        store_slot(seg + 1);
+        if (j == 0) sums[(int64_t)(seg + 1) * D] = sum;
     } else {
         if (!ok) return;
-        if (n0 < 16)
-            for (int t = max(t0, te) + j; t < t1; t += 4) yb[(int64_t)t * D + d] = from_f32<T>(0.f);
+        for (int t = max(t0, te) + j; t < t1; t += 4) yb[(int64_t)t * D + d] = from_f32<T>(0.f);
         if (a.h_final && seg == sg.count - 1)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-                if (n0 + n < N) a.h_final[at_state + n] = h[n];
+            each_state([&](int m, int n, int st) {
+                if (st < N) a.h_final[at_state + st] = h[m][n];
+            });
     }
 }
 
@@ -350,41 +365,41 @@ __global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int64_t 
 }
 
 int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // NB
-int channel_tiles(int D, int G, int nb) { return (D / G + 64 / nb - 1) / (64 / nb); }   // of a workgroup's channels
+int channel_tiles(int D, int G) { return (D / G + 63) / 64; }   // of a workgroup's channels
 
-// Segments: the power of two with the smallest estimated time, in microseconds
-// from timings on MI355X (bfloat16, N = 16).  With w wavefronts a SIMD a token
-// takes max(0.104, 0.03 + 0.067 w) with outputs and max(0.06, 0.02 + 0.05 w)
-// without; a second launch 6; and every segment reads the end states in front of
-// it, in total states x n^2 / 2 at about 20 MB/us.  One segment and the choice
-// measure: B1 T2048 D1024 218 and 31 (32 segments), B1 T16384 D4096 1725 and 477
-// (32), B2 T2048 D4096 215 and 128 (16), B4 T2048 D4096 218 and 230 (8: one is
-// kept).
+// Segments: of the powers of two, the one with the smallest estimated time, in
+// microseconds from timings on MI355X (bfloat16).  At N = 16, with w wavefronts
+// a SIMD, a token takes max(0.104, 0.03 + 0.067 w) with outputs and max(0.06,
+// 0.02 + 0.05 w) without; a second launch 6; and every segment reads the end
+// states in front of it, in total states x n^2 / 2 at about 20 MB/us.  One
+// segment and the choice measure: B1 T2048 D1024 218 and 28 (32 segments), B1
+// T16384 D4096 1725 and 467 (32), B2 T2048 D4096 215 and 126 (16), B4 T2048 D4096
+// 218 and 230 (8: one is kept); N = 64: B1 T2048 D1024 551 and 73 (32).
 Segments plan(int B, int T, int D, int N, int G)
 {
     const int nb = state_blocks(N);
-    const double waves = 4.0 * B * G * channel_tiles(D, G, nb) / 1024.0;   // a SIMD, in one segment
-    const double states = 64.0 * nb * B * D / 2.0 / 20e6;                  // bytes of all states / 2 / rate
-    int best = 1;
+    const double waves = 4.0 * B * G * channel_tiles(D, G) / 1024.0;   // a SIMD, in one segment
+    const double states = 64.0 * nb * B * D / 2.0 / 20e6;              // bytes of all states / 2 / rate
+    const double out = 0.4 + 0.6 * nb, in = 0.3 + 0.7 * nb;            // a token's time over that with 16 states
+    Segments s{};
     double least = 0.0;
-    for (int n = 1; n <= 128 && (n == 1 || n * 32 <= T); n *= 2) {
-        const double w = waves * n, tokens = (double)T / n;
-        double us = tokens * std::max(0.104, 0.03 + 0.067 * w);
-        if (n > 1) us += tokens * std::max(0.06, 0.02 + 0.05 * w) + 6.0 + 0.03 * n + states * n * n;
+    for (int n = 1; n <= 128 && (n == 1 || n * CHUNK <= T); n *= 2) {
+        const int tokens = (T + n * CHUNK - 1) / (n * CHUNK) * CHUNK, count = tokens > 0 ? (T + tokens - 1) / tokens : 1;
+        const double w = waves * count;
+        double us = tokens * out * std::max(0.104, 0.03 + 0.067 * w);
+        if (count > 1) us += tokens * in * std::max(0.06, 0.02 + 0.05 * w) + 6.0 + 0.03 * count + states * count * count;
         if (n == 1 || us < least) {
-            best = n;
+            s.tokens = tokens;
+            s.count = count;
             least = us;
         }
     }
-    Segments s{};
-    s.tokens = ((T + best - 1) / best + CHUNK - 1) / CHUNK * CHUNK;
-    s.count = s.tokens > 0 ? (T + s.tokens - 1) / s.tokens : 1;
     return s;
 }
 
 template <typename T, int NB> hipError_t fwd_launch(const ScanArgs &a, hipStream_t stream)
 {
-    const int tiles = channel_tiles(a.D, a.G, NB);
+    const int tiles = channel_tiles(a.D, a.G);
     Segments s = plan(a.B, a.T, a.D, a.N, a.G);
     if (!a.ws) {
         s.count = 1;

@@ -11,7 +11,7 @@
 //   dA = sum_t s_t g_t h_{t-1}        dD = sum gy x,   dz = dy (r + D x) silu'(z)
 //
 // Four kernels.
-//  1. Segments of 32 to 256 tokens side by side, a quad of lanes per 16 states as in
+//  1. Segments of 32 to 256 tokens side by side, a quad of lanes a channel as in
 //     the forward: the states it adds (from zero), stored at every chunk of 16 tokens, and,
 //     with the running decay P_t = prod a, the gradient it adds in front of
 //     itself, sum_t P_t C_t gy_t.  Both directions share each exp.
@@ -89,27 +89,35 @@ Layout layout(float *p, int B, int T, int D, int N, int G)
 
 // Lanes, staging and order as in the forward's kernel (kda_scan.hip).
 template <typename T, int NB>
-__global__ void __launch_bounds__(256) kda_scan_bwd_segment_kernel(ScanBwdArgs a, Layout w, int tiles)
+__global__ void __launch_bounds__(256) kda_scan_bwd_segment_kernel(ScanBwdArgs a, Layout w)
 {
-    constexpr int NP = 16 * NB, LANES = 4 * NB, CHANNELS = 256 / LANES;
+    constexpr int NP = 16 * NB;
+    static_assert(CH * 4 == 256, "a quad per channel");
     __shared__ __attribute__((aligned(16))) float rows[2][2][CHUNK * NP];   // [buffer][B, C][token][state]
-    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * (tid % LANES);
+    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * j;   // lane of the quad; its first state of each 16
     unsigned id = blockIdx.x;
-    const int tile = id % tiles;
-    id /= tiles;
+    const int tile = id % w.tiles;
+    id /= w.tiles;
     const int grp = id % a.G;
     id /= a.G;
     const int seg = id % w.nseg, b = id / w.nseg;
     const int D = a.D, N = a.N, Dg = D / a.G;
-    const int c = tile * CHANNELS + tid / LANES;
+    const int c = tile * CH + tid / 4;
     const bool ok = c < Dg;
     const int d = grp * Dg + (ok ? c : Dg - 1);   // idle lanes repeat the last channel
     const int len = seq_length(a.lengths, b, a.T);
     const int t0 = seg * w.seg, t1 = min(t0 + w.seg, a.T), te = min(t1, len);
 
-    float A2[4], h[4] = {}, r[4] = {}, P[4] = {1.f, 1.f, 1.f, 1.f};
+    float A2[NB][4], h[NB][4], r[NB][4], P[NB][4];   // states n0 + 16 m + n
 #pragma unroll
-    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? a.A[(int64_t)d * N + n0 + n] * LOG2E : 0.f;
+    for (int m = 0; m < NB; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int st = n0 + 16 * m + n;
+            A2[m][n] = st < N ? a.A[(int64_t)d * N + st] * LOG2E : 0.f;
+            h[m][n] = r[m][n] = 0.f;
+            P[m][n] = 1.f;
+        }
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
     const bool gated = a.z != nullptr, soft = a.softplus;   // without a gate z reads x, unused
     const int64_t base = (int64_t)b * a.T * D;
@@ -127,8 +135,9 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_segment_kernel(ScanBwdArgs a
     const auto store_chunk = [&](int tc, float s) {   // a segment's first chunk has nothing in front of it
         if (tc > t0 && ok) {
             const int64_t at = ((int64_t)b * w.nchunk + tc / CHUNK) * D + d;
-            store4(w.hc + at * NP + n0, h);
-            if (n0 == 0) w.sc[at] = s;
+#pragma unroll
+            for (int m = 0; m < NB; ++m) store4(w.hc + at * NP + 16 * m + n0, h[m]);
+            if (j == 0) w.sc[at] = s;
         }
     };
     T xr[4], tr[4], gr[4], zr[4], Br[NB], Cr[NB];
@@ -178,44 +187,51 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_segment_kernel(ScanBwdArgs a
         fetch(tc + CHUNK);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float4 Bv[4], Cv[4];
-            float e[4][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) Bv[k] = *reinterpret_cast<const float4 *>(Bs + (4 * i + k) * NP + n0);
+            for (int m = 0; m < NB; ++m) {
+                float4 Bv[4], Cv[4];
+                float e[4][4];
+                const int at = 4 * i * NP + 16 * m + n0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) Cv[k] = *reinterpret_cast<const float4 *>(Cs + (4 * i + k) * NP + n0);
-            each4([&](auto k) {
-                constexpr int K = decltype(k)::value;
+                for (int k = 0; k < 4; ++k) Bv[k] = *reinterpret_cast<const float4 *>(Bs + at + k * NP);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) e[K][n] = quad_bcast<K>(s[i]) * A2[n];
-            });
+                for (int k = 0; k < 4; ++k) Cv[k] = *reinterpret_cast<const float4 *>(Cs + at + k * NP);
+                each4([&](auto k) {
+                    constexpr int K = decltype(k)::value;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+                    for (int n = 0; n < 4; ++n) e[K][n] = quad_bcast<K>(s[i]) * A2[m][n];
+                });
 #pragma unroll
-                for (int n = 0; n < 4; ++n) e[k][n] = fast_exp2(e[k][n]);
-            __builtin_amdgcn_sched_barrier(0);
-            each4([&](auto k) {
-                constexpr int K = decltype(k)::value;
-                const float ub[4] = {quad_bcast<K>(u[i]) * Bv[K].x, quad_bcast<K>(u[i]) * Bv[K].y,
-                                     quad_bcast<K>(u[i]) * Bv[K].z, quad_bcast<K>(u[i]) * Bv[K].w};
-                const float gc[4] = {quad_bcast<K>(gy[i]) * Cv[K].x, quad_bcast<K>(gy[i]) * Cv[K].y,
-                                     quad_bcast<K>(gy[i]) * Cv[K].z, quad_bcast<K>(gy[i]) * Cv[K].w};
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    h[n] = __builtin_fmaf(e[K][n], h[n], ub[n]);
-                    P[n] *= e[K][n];
-                    r[n] = __builtin_fmaf(P[n], gc[n], r[n]);
-                }
-            });
+                    for (int n = 0; n < 4; ++n) e[k][n] = fast_exp2(e[k][n]);
+                __builtin_amdgcn_sched_barrier(0);
+                each4([&](auto k) {
+                    constexpr int K = decltype(k)::value;
+                    const float ub[4] = {quad_bcast<K>(u[i]) * Bv[K].x, quad_bcast<K>(u[i]) * Bv[K].y,
+                                         quad_bcast<K>(u[i]) * Bv[K].z, quad_bcast<K>(u[i]) * Bv[K].w};
+                    const float gc[4] = {quad_bcast<K>(gy[i]) * Cv[K].x, quad_bcast<K>(gy[i]) * Cv[K].y,
+                                         quad_bcast<K>(gy[i]) * Cv[K].z, quad_bcast<K>(gy[i]) * Cv[K].w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        h[m][n] = __builtin_fmaf(e[K][n], h[m][n], ub[n]);
+                        P[m][n] *= e[K][n];
+                        r[m][n] = __builtin_fmaf(P[m][n], gc[n], r[m][n]);
+                    }
+                });
+            }
         }
     }
     sum = quad_sum();
     for (; tc < t1; tc += CHUNK) store_chunk(tc, sum);
     if (!ok) return;
     const int64_t at = ((int64_t)b * w.nseg + seg) * D + d;
-    store4(w.h + at * NP + n0, h);
-    store4(w.g + at * NP + n0, r);
-    if (n0 == 0) w.sum[at] = sum;
+#pragma unroll
+    for (int m = 0; m < NB; ++m) {
+        store4(w.h + at * NP + 16 * m + n0, h[m]);
+        store4(w.g + at * NP + 16 * m + n0, r[m]);
+    }
+    if (j == 0) w.sum[at] = sum;
 }
 
 // --------------------------------- 2. states in front, gradients behind
@@ -635,10 +651,7 @@ template <typename T, int NB> hipError_t run(const ScanBwdArgs &a, const Layout 
     if (blocks >= ((int64_t)1 << 31) || join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     hipError_t e;
     if (w.nchunk > 1) {   // a single chunk has nothing in front of it or behind it
-        const int tiles = (a.D / a.G + 64 / NB - 1) / (64 / NB);
-        const int64_t segments = (int64_t)a.B * w.nseg * a.G * tiles;
-        if (segments >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-        kda_scan_bwd_segment_kernel<T, NB><<<(unsigned)segments, 256, 0, s>>>(a, w, tiles);
+        kda_scan_bwd_segment_kernel<T, NB><<<(unsigned)blocks, 256, 0, s>>>(a, w);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         kda_scan_bwd_join_kernel<<<(unsigned)join, 256, 0, s>>>(a, w);
         if ((e = hipGetLastError()) != hipSuccess) return e;
