@@ -24,7 +24,7 @@
 //
 // Measured (bfloat16, N = 16): B4 T4096 D4096, one chain of 1024 wavefronts, 0.426
 // ms (8.3 vector instructions a state and token; four wavefronts a SIMD would
-// take 0.31); B1 T16384 D4096, 32 segments, 0.467 ms; one token of B256 D12288 0.101 ms, 4.2
+// take 0.31); B1 T16384 D4096, 32 segments, 0.467 ms; one token of B256 D12288 0.077 ms, 5.5
 // TB/s.
 #include "kda_block.h"
 #include "kda_block_device.h"
@@ -45,6 +45,20 @@ struct Segments {
     int count, tokens;   // segments, tokens each (a multiple of CHUNK)
     float *slots, *sums;
 };
+
+// Sums of four values over a quad, lane j's the j-th: lanes with bit 1 keep values
+// 2 and 3, then lanes with bit 0 the odd one (every lane takes part in both sums
+// before it chooses).
+__device__ __forceinline__ float quad_sums(const float (&y)[4])
+{
+    constexpr int SWAP2 = 0x4E, SWAP1 = 0xB1;   // quad_perm [2,3,0,1], [1,0,3,2]
+    const int j = threadIdx.x & 3;
+    const float a0 = quad_add<SWAP2>(y[0]), a1 = quad_add<SWAP2>(y[1]);
+    const float a2 = quad_add<SWAP2>(y[2]), a3 = quad_add<SWAP2>(y[3]);
+    const float p0 = j & 2 ? a2 : a0, p1 = j & 2 ? a3 : a1;
+    const float q0 = quad_add<SWAP1>(p0), q1 = quad_add<SWAP1>(p1);
+    return j & 1 ? q1 : q0;
+}
 
 // A rate of -infinity (-exp of a large number) forgets at once; held finite, it
 // still does at every positive step and leaves a token of step 0, such as those
@@ -230,14 +244,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
                     }
                 }
                 if constexpr (!STATES_ONLY) {
-                    // lanes with bit 1 keep tokens 2, 3, then lanes with bit 0 the odd one
-                    // (every lane takes part in both sums before it chooses)
-                    constexpr int SWAP2 = 0x4E, SWAP1 = 0xB1;   // quad_perm [2,3,0,1], [1,0,3,2]
-                    const float a0 = quad_add<SWAP2>(y[0]), a1 = quad_add<SWAP2>(y[1]);
-                    const float a2 = quad_add<SWAP2>(y[2]), a3 = quad_add<SWAP2>(y[3]);
-                    const float p0 = j & 2 ? a2 : a0, p1 = j & 2 ? a3 : a1;
-                    const float q0 = quad_add<SWAP1>(p0), q1 = quad_add<SWAP1>(p1);
-                    r[i] = j & 1 ? q1 : q0;
+                    r[i] = quad_sums(y);
                 }
             }
             if constexpr (!STATES_ONLY) {
@@ -275,93 +282,132 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
     }
 }
 
-// One token: LPC lanes a channel, 4 states each, so a wavefront's states are
-// contiguous 16-byte accesses; the read and write of the states bound it.  A
-// thread takes BATCH pieces 256 lanes apart, so that a workgroup moves a
-// contiguous stretch of states whose loads are all out before the first is
-// used; states pass once and are accessed non-temporally.
-template <typename T, int LPC, bool VEC, int BATCH>
-__global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int64_t lanes)
+// One token.  L lanes (a power of two with 4 L >= N) have a channel of four
+// sequences, lane l of them states 4 l .. 4 l + 3 and, for what a channel costs
+// once, sequence l % 4 (l and l + 2, or all four, where L is 2 or 1): as in the
+// forward with sequences in the place of tokens, so rates and positions are shared
+// by the four.  The read and write of the states bound it; all their loads are out
+// before the first is used, and as they pass once they are non-temporal.
+//
+// A workgroup takes 256 / L channels; where there are fewer, sequences lie side by
+// side in it, 1 << shift threads each.  Measured (bfloat16): B256 D12288 N16 0.077
+// ms, 5.5 TB/s; 0.101 with four channels of one sequence a thread, each with its
+// own rates, positions and softplus (twice the vector instructions).
+template <int L, int I, int K> __device__ __forceinline__ float of_sequence(const float (&v)[K])
 {
-    constexpr int STEP = 256 / LPC;   // channels between a thread's pieces
-    const int l = threadIdx.x % LPC, D = a.D, N = a.N, n0 = 4 * l, Dg = D / a.G;
-    const int64_t first = (int64_t)blockIdx.x * 256 * BATCH + threadIdx.x, channels = lanes / LPC;
-    const int64_t c0 = first / LPC;
-    const bool in4 = n0 < N;
+    constexpr int PAIR = I & 1 ? 0xF5 : 0xA0;   // quad_perm [1,1,3,3] or [0,0,2,2]
+    if constexpr (L == 1) return v[I];
+    else if constexpr (L == 2)
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[I / 2]), PAIR, 0xF, 0xF, true));
+    else return quad_bcast<I>(v[0]);
+}
+template <typename T, int L, bool VEC>
+__global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int tiles, int shift)
+{
+    constexpr int K = L < 4 ? 4 / L : 1;   // sequences of which a lane does the channel's own part
+    const int tid = threadIdx.x, l = tid % L, n0 = 4 * l;
+    const int tile = blockIdx.x % tiles, per = 256 >> shift, side = tid >> shift;
+    const int64_t first = (int64_t)(blockIdx.x / tiles) * 4 * per;   // sequence
+    const int B = a.B, D = a.D, N = a.N;
+    const int c = tile * (256 / L) + (tid & ((1 << shift) - 1)) / L, d = min(c, D - 1);
+    const bool ok = c < D, in4 = n0 < N;
+    const unsigned row = (unsigned)a.G * N, g = a.G == 1 ? 0 : d / (D / a.G);
 
-    float A2[BATCH][4], h[BATCH][4], B[BATCH][4], C[BATCH][4], x[BATCH], s[BATCH], z[BATCH], skip[BATCH];
-    Pack<float, 4> hr[BATCH];
+    // states and rows of B and C of sequences first + i per + side, i < 4
+    Pack<float, 4> hr[4];
+    Raw4<T> Br[4], Cr[4];
+    float hs[4][4], Bs[4][4], Cs[4][4];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {   // pieces behind the last channel repeat it and store nothing
-        const int64_t c = c0 + i * STEP < channels ? c0 + i * STEP : channels - 1;
-        const float *hp = a.h_final + c * N;
-        if (VEC && in4) hr[i].stream(hp + n0);
-        else hr[i].zero();
-        if (!VEC)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) h[i][n] = n0 + n < N ? hp[n0 + n] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-        const int64_t c = c0 + i * STEP < channels ? c0 + i * STEP : channels - 1;
-        const int b = (int)(c / D), d = (int)(c - (int64_t)b * D);
-        const int64_t row = ((int64_t)b * a.G + d / Dg) * N;
-        const T *Bp = (const T *)a.Bm + row + n0, *Cp = (const T *)a.Cm + row + n0;
-        const float *Ap = a.A + (int64_t)d * N + n0;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t q = first + i * per < B ? first + i * per : B - 1;   // behind the last sequence: it again, not stored
+        const unsigned sd = min(side, (int)(B - 1 - q));
+        const float *hp = a.h_final + q * D * N;
+        const T *Bp = (const T *)a.Bm + q * row, *Cp = (const T *)a.Cm + q * row;
+        const unsigned at = (sd * D + d) * N + n0, rat = sd * row + g * N + n0;
         if constexpr (VEC) {
-            Raw4<T> q;
-            Raw4<float> r;
-            q.zero();
-            r.zero();
-            if (in4) q.load(Bp);
-            q.to_f32(B[i]);
-            if (in4) q.load(Cp);
-            q.to_f32(C[i]);
-            if (in4) r.load(Ap);
-            r.to_f32(A2[i]);
+            hr[i].zero();
+            Br[i].zero();
+            Cr[i].zero();
+            if (in4) {
+                hr[i].stream(hp + at);
+                Br[i].load(Bp + rat);
+                Cr[i].load(Cp + rat);
+            }
         } else {
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                B[i][n] = n0 + n < N ? to_f32(Bp[n]) : 0.f;
-                C[i][n] = n0 + n < N ? to_f32(Cp[n]) : 0.f;
-                A2[i][n] = n0 + n < N ? Ap[n] : 0.f;
+                hs[i][n] = n0 + n < N ? hp[at + n] : 0.f;
+                Bs[i][n] = n0 + n < N ? to_f32(Bp[rat + n]) : 0.f;
+                Cs[i][n] = n0 + n < N ? to_f32(Cp[rat + n]) : 0.f;
             }
         }
-        x[i] = to_f32(((const T *)a.x)[c]);
-        s[i] = to_f32(((const T *)a.dt)[c]) + (a.dt_bias ? a.dt_bias[d] : 0.f);
-        z[i] = a.z ? to_f32(((const T *)a.z)[c]) : 0.f;
-        skip[i] = a.Dskip ? a.Dskip[d] : 0.f;
+    }
+    float A2[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? finite_rate(a.A[(int64_t)d * N + n0 + n] * LOG2E) : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
+    const auto own = [&](int k) { return first + (int64_t)(l % 4 + k * L) * per + side; };
+    const auto token = [&](int k) { return (own(k) < B ? own(k) : B - 1) * D + d; };
+    float x[K], z[K], s[K], u[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        x[k] = to_f32(((const T *)a.x)[token(k)]);
+        z[k] = a.z ? to_f32(((const T *)a.z)[token(k)]) : 0.f;
+        s[k] = to_f32(((const T *)a.dt)[token(k)]) + bias;
     }
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-        if (VEC) hr[i].to_f32(h[i]);
-        if (a.softplus) s[i] = softplus_f32(s[i]);
-        const float u = s[i] * x[i], s2 = s[i] * LOG2E;
-        float y = 0.f;
+    for (int k = 0; k < K; ++k) {
+        if (a.softplus) s[k] = softplus_f32(s[k]);
+        u[k] = s[k] * x[k];
+    }
+
+    float y[4] = {};
+    each4([&](auto i) {
+        constexpr int I = decltype(i)::value;
+        const int64_t q = first + I * per;
+        float *hp = a.h_final + q * D * N + ((unsigned)side * D + d) * N + n0;
+        if constexpr (VEC) {
+            hr[I].to_f32(hs[I]);
+            Br[I].to_f32(Bs[I]);
+            Cr[I].to_f32(Cs[I]);
+        }
+        float (&h)[4] = hs[I];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            h[i][n] = __builtin_fmaf(fast_exp2(s2 * A2[i][n]), h[i][n], u * B[i][n]);
-            y = __builtin_fmaf(C[i][n], h[i][n], y);
+            h[n] = __builtin_fmaf(fast_exp2(of_sequence<L, I>(s) * A2[n]), h[n], of_sequence<L, I>(u) * Bs[I][n]);
+            y[I] = __builtin_fmaf(Cs[I][n], h[n], y[I]);
         }
-#pragma unroll
-        for (int m = 1; m < LPC; m <<= 1) y += __shfl_xor(y, m, LPC);
-        const int64_t c = c0 + i * STEP;
-        if (c < channels) {
-            float *hp = a.h_final + c * N;
-            if (VEC) {
-                if (in4) Pack<float, 4>::unstream(hp + n0, h[i]);
+        if (ok && q + side < B) {
+            if constexpr (VEC) {
+                if (in4) Pack<float, 4>::unstream(hp, h);
             } else {
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
-                    if (n0 + n < N) hp[n0 + n] = h[i][n];
-            }
-            if (l == 0) {
-                y = __builtin_fmaf(skip[i], x[i], y);
-                if (a.z) y *= z[i] * sigmoid_f32(z[i]);
-                ((T *)a.y)[c] = from_f32<T>(y);
+                    if (n0 + n < N) hp[n] = h[n];
             }
         }
+    });
+    float r[K];
+    if constexpr (L == 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) r[k] = y[k];
+    } else if constexpr (L == 2) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float p = quad_add<0xB1>(y[2 * k]), q = quad_add<0xB1>(y[2 * k + 1]);   // quad_perm [1,0,3,2]
+            r[k] = l ? q : p;
+        }
+    } else {
+        r[0] = quad_sums(y);
+#pragma unroll
+        for (int m = 4; m < L; m <<= 1) r[0] += __shfl_xor(r[0], m, L);
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (ok && l < 4 && own(k) < B) {
+            const float v = __builtin_fmaf(skip, x[k], r[k]);
+            ((T *)a.y)[token(k)] = from_f32<T>(a.z ? v * (z[k] * sigmoid_f32(z[k])) : v);
+        }
 }
 
 int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // NB
@@ -427,19 +473,16 @@ template <typename T> hipError_t fwd_dispatch(const ScanArgs &a, hipStream_t s)
     }
 }
 
-template <typename T, int LPC, bool VEC, int BATCH> hipError_t step_batch(const ScanArgs &a, hipStream_t s)
+template <typename T, int L> hipError_t step_launch(const ScanArgs &a, hipStream_t stream)
 {
-    const int64_t lanes = (int64_t)a.B * a.D * LPC, blocks = (lanes + 256 * BATCH - 1) / (256 * BATCH);
+    int shift = 0;   // threads of a sequence in a workgroup
+    while (shift < 8 && (1 << shift) < (int64_t)L * a.D) ++shift;
+    const int tiles = (a.D + 256 / L - 1) / (256 / L), group = 4 * (256 >> shift);
+    const int64_t blocks = (int64_t)tiles * (((int64_t)a.B + group - 1) / group);
     if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    kda_scan_step_kernel<T, LPC, VEC, BATCH><<<(unsigned)blocks, 256, 0, s>>>(a, lanes);
+    (a.N % 4 == 0 ? kda_scan_step_kernel<T, L, true> : kda_scan_step_kernel<T, L, false>)
+        <<<(unsigned)blocks, 256, 0, stream>>>(a, tiles, shift);
     return hipGetLastError();
-}
-// Several pieces a thread where that still leaves several rounds of workgroups.
-template <typename T, int LPC> hipError_t step_launch(const ScanArgs &a, hipStream_t s)
-{
-    const bool many = (int64_t)a.B * a.D * LPC >= (int64_t)4 * 256 * 8192;
-    if (a.N % 4 == 0) return many ? step_batch<T, LPC, true, 4>(a, s) : step_batch<T, LPC, true, 1>(a, s);
-    return many ? step_batch<T, LPC, false, 4>(a, s) : step_batch<T, LPC, false, 1>(a, s);
 }
 
 template <typename T> hipError_t step_dispatch(const ScanArgs &a, hipStream_t s)

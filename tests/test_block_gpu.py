@@ -254,6 +254,27 @@ def test_scan_steps_continue_a_prompt(kda, N, G, dt):
     ref.check(h, rh, Eh, F32, "h")
 
 
+@pytest.mark.parametrize("B,D,N,G,dt", [(1, 300, 16, 1, BF), (4, 65, 16, 5, F32), (9, 70, 13, 2, BF), (40, 3, 64, 1, F32),
+                                        (1030, 1, 3, 1, BF), (5, 600, 5, 3, F32), (130, 7, 8, 7, BF), (6, 260, 2, 1, F32),
+                                        (7, 33, 32, 1, BF), (19, 17, 40, 1, BF)])
+def test_scan_step_batches(kda, B, D, N, G, dt):
+    """Batches of any size over channels of any number, with nothing written
+    behind the last sequence's state and output."""
+    c = (B, 1, D, N, G, dt, True, False, True, True)
+    p, _, _, _, _ = _scan_case(c)
+    d = {k: _dev(v) for k, v in p.items()}
+    h = torch.full((B + 3, D, N), 7.0, device="cuda")
+    y = torch.full((B + 3, D), 7.0, device="cuda", dtype=dt)
+    h[:B] = d["h0"]
+    kda.kda_selective_scan_step(d["x"][:, 0], d["dt"][:, 0], d["A"], d["Bm"][:, 0], d["Cm"][:, 0], h[:B], D=d["D"],
+                                z=d["z"][:, 0], dt_bias=d["dt_bias"], y=y[:B])
+    torch.cuda.synchronize()
+    (ry, Ey), (rh, Eh), _ = ref.scan_fwd(*_scan_ref(p), True, None)
+    ref.check(y[:B], ry[:, 0], Ey[:, 0], dt, "y")
+    ref.check(h[:B], rh, Eh, F32, "h")
+    assert (h[B:] == 7).all() and (y[B:] == 7).all()
+
+
 def test_scan_without_tokens(kda):
     g = torch.Generator().manual_seed(1)
     D, N = 20, 16
