@@ -9,7 +9,9 @@
 // its tokens once plus W - 1 tokens in front (which its neighbour run brings
 // into the cache as well).  Rows whose length is no multiple of V are walked
 // one channel a thread.  Measured (bfloat16, W = 4): forward of B4 T16384 D4096
-// 0.209 ms, 5.1 TB/s; backward of B4 T4096 D4096 0.093 ms, 4.3 TB/s.
+// 0.209 ms, 5.1 TB/s; backward of B4 T4096 D4096 0.091 ms, 4.4 TB/s (0.094 without
+// the non-temporal loads, the same with 8 tokens requested together, 0.10 with
+// three wavefronts a SIMD instead of two).
 #include "kda_block.h"
 #include "kda_block_device.h"
 
@@ -188,8 +190,8 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             if (t + i < min(len, t1 + W - 1)) {
-                xn[i].load(x + (int64_t)(t + i) * D);
-                gn[i].load(dy + (int64_t)(t + i) * D);
+                xn[i].stream(x + (int64_t)(t + i) * D);
+                gn[i].stream(dy + (int64_t)(t + i) * D);
             } else {
                 xn[i].zero();
                 gn[i].zero();
@@ -287,8 +289,7 @@ int run_tokens(int B, int T, int64_t ncg, int most, int64_t want)
     return rt;
 }
 // (Forward of B4 T16384 D4096 in runs of 16, 32, 64, 128 and 256 tokens: 261, 227,
-// 217, 215 and 211 us; backward of B4 T4096 D4096 with four channels a thread
-// keeps 128.)
+// 217, 215 and 211 us.)
 int fwd_run(int B, int T, int64_t ncg) { return run_tokens(B, T, ncg, 256, 1 << 17); }
 int bwd_run(int B, int T, int64_t ncg) { return run_tokens(B, T, ncg, 256, 1 << 17); }
 
