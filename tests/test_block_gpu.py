@@ -370,6 +370,13 @@ def test_norm_forward_and_backward(kda, rows, D, dt):
         ref.check(got, r, E, t, k)
 
 
+@pytest.mark.parametrize("rows,D,dt", [(700, 5120, BF), (600, 12288, F32), (520, 9000, BF), (300, 8194, BF), (280, 16381, F32),
+                                       (1100, 600, F32), (2000, 200, BF)])
+def test_norm_rows_of_many_workgroups(kda, rows, D, dt):
+    """More rows than the workgroups take in one round."""
+    test_norm_forward_and_backward(kda, rows, D, dt)
+
+
 def test_norm_in_place_without_parameters_and_offset_rows(kda):
     g = torch.Generator().manual_seed(2)
     x = (_rand(g, (4, 3, 96)) + 300.0).to(F32)   # a mean far above the spread
