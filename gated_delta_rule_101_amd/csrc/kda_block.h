@@ -27,7 +27,7 @@ struct ConvBwdArgs {
     void *dx;
     float *dw, *dbias = nullptr;
     void *dstate0 = nullptr;
-    float *ws;                               // [runs][D][W + 1] partial sums
+    float *ws;                               // partial sums: dw [runs][D][W], then dbias [runs][D]
     int B, T, D, W;
     bool silu, bf16;
 };

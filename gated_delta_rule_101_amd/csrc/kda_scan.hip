@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
 #pragma unroll
         for (int m = 0; m < NB; ++m) load_slot(min(seg, 1), m, h[m]);
         // a few segments' loads together: the chain itself is one multiply-add each
-        constexpr int JOIN = 8 / NB;
+        constexpr int JOIN = NB == 1 ? 16 : 8 / NB;
         for (int i = 2; i <= seg; i += JOIN) {
             float v[JOIN][NB][4], s[JOIN];
 #pragma unroll
