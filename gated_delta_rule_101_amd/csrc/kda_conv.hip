@@ -280,12 +280,12 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
 
 // Tokens a run: as many as leave `want` threads, so that the halo (and the
 // backward's partial sums) stay small against the run; at least 4, more than
-// the W - 1 tokens of the halo.
+// the W - 1 tokens of the halo.  (A grid too large to launch is the launcher's
+// to refuse: with many channels no length of run makes it small.)
 int run_tokens(int B, int T, int64_t ncg, int most, int64_t want)
 {
     int rt = most;
     while (rt > 4 && (int64_t)B * ((T + rt - 1) / rt) * ncg < want) rt >>= 1;
-    while ((int64_t)B * ((T + rt - 1) / rt) * ncg >= ((int64_t)1 << 38)) rt <<= 1;   // grid limit
     return rt;
 }
 // (Forward of B4 T16384 D4096 in runs of 16, 32, 64, 128 and 256 tokens: 261, 227,
