@@ -97,6 +97,12 @@ struct ColumnSum {
     bool out_bf16;
 };
 hipError_t launch_column_sums(const ColumnSum *jobs, int n, hipStream_t stream);
+bool column_sums_fit(const ColumnSum *jobs, int n);      // its grids can be launched
+
+// HIP launches fewer than 2^32 threads along an axis.  Every launcher below
+// checks all its grids before the first of them and returns
+// hipErrorNotSupported, with nothing enqueued, where one is larger.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks < ((int64_t)1 << 32) / threads; }
 
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t stream);
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t stream);      // state_final is the state, T unused

@@ -81,7 +81,11 @@ kda_status_t check_scan(int B, int T, int D, int N, int G, kda_dtype_t dtype)
     return KDA_OK;
 }
 
-kda_status_t launched(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
+// A launcher's own refusal (a grid too large) and the runtime's.
+kda_status_t launched(hipError_t e)
+{
+    return e == hipSuccess ? KDA_OK : e == hipErrorNotSupported ? KDA_ERR_UNSUPPORTED : KDA_ERR_LAUNCH;
+}
 
 }  // namespace
 

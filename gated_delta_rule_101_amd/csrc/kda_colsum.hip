@@ -101,40 +101,57 @@ __global__ void __launch_bounds__(256) column_sum_kernel(Jobs jobs)
 template <bool CHUNKS> hipError_t run(const Jobs &jobs, int64_t blocks, hipStream_t stream)
 {
     if (blocks == 0) return hipSuccess;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     column_sum_kernel<CHUNKS><<<(unsigned)blocks, 256, 0, stream>>>(jobs);
     return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_column_sums(const ColumnSum *list, int n, hipStream_t stream)
-{
+// The jobs of both launches and their workgroups; false: too many to launch.
+struct Plan {
     Jobs jobs, chunks;
+    int64_t blocks, chunk_blocks;
+};
+bool plan(const ColumnSum *list, int n, Plan &p)
+{
+    Jobs &jobs = p.jobs, &chunks = p.chunks;
     jobs.n = chunks.n = 0;
-    int64_t blocks = 0, chunk_blocks = 0;
+    p.blocks = p.chunk_blocks = 0;
     for (int i = 0; i < n; ++i) {
         ColumnSum job = list[i];
         if (!job.out || job.cols <= 0) continue;
-        if (jobs.n == MAX_JOBS) return hipErrorInvalidValue;
+        if (jobs.n == MAX_JOBS) return false;
         const auto blocks_of = [&](int lanes) { return (job.cols + 4 * lanes - 1) / (4 * lanes); };
         const int lanes = blocks_of(16) < 64 ? 4 : blocks_of(16) >= 2048 && job.rows <= 1024 ? SERIAL : 16;
         const int64_t wide = blocks_of(lanes);
         if (job.rows > 16 * CHUNK && wide < 256) {
             chunks.j[chunks.n] = job;
             chunks.lanes[chunks.n] = lanes;
-            chunks.first[chunks.n++] = (unsigned)chunk_blocks;
+            chunks.first[chunks.n++] = (unsigned)p.chunk_blocks;
             job.rows = (job.rows + CHUNK - 1) / CHUNK;
-            chunk_blocks += wide * job.rows;
+            p.chunk_blocks += wide * job.rows;
             job.stride *= CHUNK;
         }
         jobs.j[jobs.n] = job;
         jobs.lanes[jobs.n] = lanes;
-        jobs.first[jobs.n++] = (unsigned)blocks;
-        blocks += wide;
+        jobs.first[jobs.n++] = (unsigned)p.blocks;
+        p.blocks += wide;
     }
-    const hipError_t e = run<true>(chunks, chunk_blocks, stream);
-    return e != hipSuccess ? e : run<false>(jobs, blocks, stream);
+    return grid_fits(p.blocks, 256) && grid_fits(p.chunk_blocks, 256);
+}
+
+}  // namespace
+
+bool column_sums_fit(const ColumnSum *list, int n)
+{
+    Plan p;
+    return plan(list, n, p);
+}
+
+hipError_t launch_column_sums(const ColumnSum *list, int n, hipStream_t stream)
+{
+    Plan p;
+    if (!plan(list, n, p)) return hipErrorNotSupported;
+    const hipError_t e = run<true>(p.chunks, p.chunk_blocks, stream);
+    return e != hipSuccess ? e : run<false>(p.jobs, p.blocks, stream);
 }
 
 }  // namespace kda

@@ -311,7 +311,7 @@ hipError_t fwd_w(const ConvArgs &a, hipStream_t s)
     const int ncg = wide ? a.D / V : a.D;
     const int rt = fwd_run(a.B, a.T, ncg), nruns = a.T > 0 ? (a.T + rt - 1) / rt : 1;
     const int64_t total = (int64_t)a.B * nruns * ncg, blocks = (total + THREADS - 1) / THREADS;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(blocks, THREADS)) return hipErrorNotSupported;
     if (wide) (a.silu ? kda_conv_fwd_kernel<T, W, V, true> : kda_conv_fwd_kernel<T, W, V, false>)<<<(unsigned)blocks, THREADS, 0, s>>>(
         a, rt, nruns, ncg, total);
     else (a.silu ? kda_conv_fwd_kernel<T, W, 1, true> : kda_conv_fwd_kernel<T, W, 1, false>)<<<(unsigned)blocks, THREADS, 0, s>>>(
@@ -326,7 +326,7 @@ hipError_t step_w(const ConvArgs &a, hipStream_t s)
     const bool wide = a.D % V == 0;
     const int ncg = wide ? a.D / V : a.D;
     const int64_t total = (int64_t)a.B * ncg, blocks = (total + THREADS - 1) / THREADS;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(blocks, THREADS)) return hipErrorNotSupported;
     if (wide) kda_conv_step_kernel<T, W, V><<<(unsigned)blocks, THREADS, 0, s>>>(a, ncg, total);
     else kda_conv_step_kernel<T, W, 1><<<(unsigned)blocks, THREADS, 0, s>>>(a, ncg, total);
     return hipGetLastError();
@@ -340,7 +340,10 @@ hipError_t bwd_w(const ConvBwdArgs &a, hipStream_t s)
     const int ncg = wide ? a.D / V : a.D;
     const int rt = bwd_run(a.B, a.T, ncg), nruns = a.T > 0 ? (a.T + rt - 1) / rt : 1;
     const int64_t total = (int64_t)a.B * nruns * ncg, blocks = (total + THREADS - 1) / THREADS;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    const int64_t rows = (int64_t)a.B * nruns, cols = (int64_t)a.D * W;
+    const ColumnSum jobs[] = {{a.ws, a.dw, rows, cols, cols, false},
+                              {a.ws + rows * cols, a.dbias, rows, a.D, a.D, false}};
+    if (!grid_fits(blocks, THREADS) || !column_sums_fit(jobs, 2)) return hipErrorNotSupported;
     if (total > 0) {
         (wide ? a.silu ? kda_conv_bwd_kernel<T, W, V, true> : kda_conv_bwd_kernel<T, W, V, false>
               : a.silu ? kda_conv_bwd_kernel<T, W, 1, true> : kda_conv_bwd_kernel<T, W, 1, false>)
@@ -348,9 +351,6 @@ hipError_t bwd_w(const ConvBwdArgs &a, hipStream_t s)
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const int64_t rows = (int64_t)a.B * nruns, cols = (int64_t)a.D * W;
-    const ColumnSum jobs[] = {{a.ws, a.dw, rows, cols, cols, false},
-                              {a.ws + rows * cols, a.dbias, rows, a.D, a.D, false}};
     return launch_column_sums(jobs, 2, s);
 }
 

@@ -452,7 +452,7 @@ template <typename T, int NB> hipError_t fwd_launch(const ScanArgs &a, hipStream
         s.tokens = a.T;
     }
     const int64_t blocks = (int64_t)a.B * a.G * tiles;
-    if (blocks * s.count >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(blocks * s.count, 256)) return hipErrorNotSupported;
     if (s.count > 1) {
         s.slots = a.ws;
         s.sums = a.ws + (int64_t)a.B * s.count * 16 * NB * a.D;
@@ -479,7 +479,7 @@ template <typename T, int L> hipError_t step_launch(const ScanArgs &a, hipStream
     while (shift < 8 && (1 << shift) < (int64_t)L * a.D) ++shift;
     const int tiles = (a.D + 256 / L - 1) / (256 / L), group = 4 * (256 >> shift);
     const int64_t blocks = (int64_t)tiles * (((int64_t)a.B + group - 1) / group);
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(blocks, 256)) return hipErrorNotSupported;
     (a.N % 4 == 0 ? kda_scan_step_kernel<T, L, true> : kda_scan_step_kernel<T, L, false>)
         <<<(unsigned)blocks, 256, 0, stream>>>(a, tiles, shift);
     return hipGetLastError();

@@ -648,7 +648,7 @@ template <typename T, int NB> hipError_t run(const ScanBwdArgs &a, const Layout 
 {
     const int64_t blocks = (int64_t)a.B * w.nseg * a.G * w.tiles;
     const int64_t join = ((int64_t)a.B * a.D * w.np + 255) / 256 * 2;
-    if (blocks >= ((int64_t)1 << 31) || join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(blocks, 256) || !grid_fits(join, 256)) return hipErrorNotSupported;
     hipError_t e;
     if (w.nchunk > 1) {   // a single chunk has nothing in front of it or behind it
         kda_scan_bwd_segment_kernel<T, NB><<<(unsigned)blocks, 256, 0, s>>>(a, w);
@@ -677,22 +677,23 @@ hipError_t launch_scan_bwd(const ScanBwdArgs &a, hipStream_t s)
 {
     (void)hipGetLastError();
     const Layout w = layout(a.ws, a.B, a.T, a.D, a.N, a.G);
-    hipError_t e;
-    if (a.B > 0 && a.T > 0) {
-        e = a.bf16 ? dispatch<uint16_t>(a, w, s) : dispatch<float>(a, w, s);
-        if (e != hipSuccess) return e;
-    } else if (a.dh0 && a.B > 0) {
-        const int64_t n = (int64_t)a.B * a.D * a.N, blocks = (n + 255) / 256;
-        if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-        kda_scan_bwd_pass_kernel<<<(unsigned)blocks, 256, 0, s>>>(a.dh_final, a.dh0, n);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
     const int64_t parts = (int64_t)a.B * w.nseg, DN = (int64_t)a.D * a.N, rows = (int64_t)a.B * a.T * a.G * a.N;
     const ColumnSum jobs[] = {{w.dA, a.dA, parts, DN, DN, false},
                               {w.dD, a.dDskip, parts, a.D, a.D, false},
                               {w.db, a.ddt_bias, parts, a.D, a.D, false},
                               {w.dB, a.dBm, w.tiles, rows, rows, a.bf16},
                               {w.dC, a.dCm, w.tiles, rows, rows, a.bf16}};
+    if (!column_sums_fit(jobs, 5)) return hipErrorNotSupported;
+    hipError_t e;
+    if (a.B > 0 && a.T > 0) {
+        e = a.bf16 ? dispatch<uint16_t>(a, w, s) : dispatch<float>(a, w, s);
+        if (e != hipSuccess) return e;
+    } else if (a.dh0 && a.B > 0) {
+        const int64_t n = (int64_t)a.B * a.D * a.N, blocks = (n + 255) / 256;
+        if (!grid_fits(blocks, 256)) return hipErrorNotSupported;
+        kda_scan_bwd_pass_kernel<<<(unsigned)blocks, 256, 0, s>>>(a.dh_final, a.dh0, n);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     return launch_column_sums(jobs, 5, s);
 }
 

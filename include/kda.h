@@ -459,7 +459,11 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const void *v, const vo
  *  - D (channels) and T are any size >= 0; a call with nothing to compute
  *    still writes what its contract defines (states copied, gradients zero).
  *    B T D, and every tensor's element count, must stay below 2^40, B, T and
- *    D below 2^24 each (KDA_ERR_UNSUPPORTED beyond).
+ *    D below 2^24 each (KDA_ERR_UNSUPPORTED beyond).  So is a call whose grid
+ *    would reach HIP's limit of 2^32 threads, before anything is enqueued: a
+ *    convolution has one thread per sequence, run of 4 to 256 tokens and 1 to
+ *    8 channels, a scan 256 per sequence, group, 64 channels and segment, its
+ *    gradients 2 per sequence, channel and padded state besides.
  *  - lengths [B] int32 (device, or NULL: all T) are the sequences' lengths in
  *    a right-padded batch, clamped to [0, T].  Tokens behind a sequence's end
  *    enter no result (they may hold anything, NaN included); their outputs and
