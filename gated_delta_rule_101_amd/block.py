@@ -293,6 +293,9 @@ def kda_selective_scan_bwd(dy: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, 
     with _on(dev, stream) as handle:
         out = {"dx": torch.empty_like(x), "ddt": torch.empty_like(x), "dA": torch.empty_like(A),
                "dB": torch.empty_like(Bm), "dC": torch.empty_like(Cm)}
+        if C == 0:   # the library has nothing to launch; the rows of B and C still have gradients, of no channel
+            out["dB"].zero_()
+            out["dC"].zero_()
         if D is not None:
             out["dD"] = torch.empty_like(D)
         if z is not None:

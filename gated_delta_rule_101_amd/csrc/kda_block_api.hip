@@ -229,7 +229,7 @@ kda_status_t kda_selective_scan_bwd(const void *dy, const void *x, const void *d
 {
     const kda_status_t st = check_scan(B, T, D, N, G, dtype);
     if (st != KDA_OK) return st;
-    if (D == 0) return KDA_OK;
+    if (D == 0) return KDA_OK;   // as declared: dBm and dCm, the only outputs with elements, are the caller's
     const size_t e = dsize(dtype), tok = (size_t)B * T * D * e, rows = (size_t)B * T * G * N * e;
     const size_t state = (size_t)B * D * N * 4, need = kda_selective_scan_bwd_workspace_bytes(B, T, D, N, G);
     if (workspace_bytes < need) return KDA_ERR_INVALID_ARG;

@@ -458,6 +458,9 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const void *v, const vo
  *    sums and states are float32; each output is rounded once, when stored.
  *  - D (channels) and T are any size >= 0; a call with nothing to compute
  *    still writes what its contract defines (states copied, gradients zero).
+ *    Without channels (D = 0) a call returns at once and writes nothing; that
+ *    leaves dBm and dCm of the scan's gradients, zeros by the formula, to the
+ *    caller (the Python binding fills them).
  *    B T D, and every tensor's element count, must stay below 2^40, B, T and
  *    D below 2^24 each (KDA_ERR_UNSUPPORTED beyond).  So is a call whose grid
  *    would reach HIP's limit of 2^32 threads, before anything is enqueued: a

@@ -1,0 +1,85 @@
+"""The block operators where a value overflows, a sequence ends inside a chunk
+or states are padded: what does not belong to a sequence or does not exist must
+not reach a sum, not even as 0 times infinity.
+
+Expectations come from the formulas.  Most results do not depend on the one
+value that is infinite here; those are compared with the float64 form of the
+same inputs with that value 0, in the bounds of tests/block_reference.py."""
+
+import pytest
+import torch
+
+import block_reference as ref
+from block_reference import f64
+from gpu_support import say
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def kda():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import gated_delta_rule_101_amd as m
+    m.load_library()
+    return m
+
+
+def _dev(t):
+    return None if t is None else t.cuda()
+
+
+def _scan_params(B, T, D, N, G, dt, seed):
+    g = torch.Generator().manual_seed(seed)
+
+    def r(*shape, scale=1.0, dtype=F32):
+        return (torch.randn(shape, generator=g) * scale).to(dtype)
+
+    return dict(x=r(B, T, D, dtype=dt), dt=r(B, T, D, scale=0.5, dtype=dt), A=-torch.rand((D, N), generator=g) - 0.1,
+                Bm=r(B, T, G, N, dtype=dt), Cm=r(B, T, G, N, dtype=dt), h0=r(B, D, N), D=r(D), z=r(B, T, D, dtype=dt),
+                dt_bias=r(D) - 2.0, dy=r(B, T, D, dtype=dt), dh=r(B, D, N))
+
+
+def _scan_bwd(kda, p, lengths):
+    d = {k: _dev(v) for k, v in p.items()}
+    got = kda.kda_selective_scan_bwd(d["dy"], d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], d["h0"], D=d["D"], z=d["z"],
+                                     dt_bias=d["dt_bias"], dh_final=d["dh"], lengths=_dev(lengths), want_dh0=True)
+    torch.cuda.synchronize()
+    return {k: v.cpu() for k, v in got.items()}
+
+
+def _scan_ref(p, lengths):
+    args = [f64(p[k]) for k in ("x", "dt", "A", "Bm", "Cm", "h0", "D", "z", "dt_bias")]
+    return ref.scan_bwd(f64(p["dy"]), *args, True, f64(p["dh"]), lengths)
+
+
+def _scan_fwd(kda, p, lengths=None):
+    d = {k: _dev(v) for k, v in p.items()}
+    y, h = kda.kda_selective_scan_fwd(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], d["h0"], D=d["D"], z=d["z"],
+                                      dt_bias=d["dt_bias"], lengths=_dev(lengths))
+    torch.cuda.synchronize()
+    return y.cpu(), h.cpu()
+
+
+def _check(got, want, where, name):
+    r, E = want
+    ref.check(got[where], r[where], E[where], got.dtype, name)
+
+
+# ----------------------------------------------------------- nothing to sum
+
+@pytest.mark.parametrize("G", [1, 3])
+def test_scan_backward_without_channels(kda, G):
+    """dB and dC have rows without any channel: zeros."""
+    x, A = torch.empty((2, 3, 0), device="cuda"), torch.empty((0, 4), device="cuda")
+    bc = torch.ones((2, 3, G, 4), device="cuda")
+    stale = [torch.full_like(bc, 7.0) for _ in range(8)]   # what fresh allocations would find
+    torch.cuda.synchronize()
+    del stale
+    got = kda.kda_selective_scan_bwd(x, x, x, A, bc, bc, want_dh0=True)
+    torch.cuda.synchronize()
+    assert got["dB"].shape == bc.shape and not got["dB"].any() and not got["dC"].any()
+    assert got["dx"].shape == x.shape and got["dA"].shape == A.shape and got["dh0"].shape == (2, 0, 4)
