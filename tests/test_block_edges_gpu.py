@@ -69,6 +69,41 @@ def _check(got, want, where, name):
     ref.check(got[where], r[where], E[where], got.dtype, name)
 
 
+# ------------------------------------------- behind a sequence's last token
+
+@pytest.mark.parametrize("T,short,N,dt", [(21, 0, 16, F32), (21, 6, 16, F32), (21, 17, 16, BF), (37, 20, 20, F32), (64, 1, 16, F32),
+                                          (700, 0, 16, F32), (700, 7, 16, BF), (700, 333, 40, F32), (700, 1, 17, F32)])
+def test_scan_backward_infinite_last_token(kda, T, short, N, dt):
+    """An infinite last input x of one channel enters that token's ddt, dz, dB and dC
+    and the sums dD and ddt_bias; dx, dA and dh0 do not depend on it, and neither
+    do the other tokens, which behind the end are zeros."""
+    B, D, ch = 2, 40, 3
+    p = _scan_params(B, T, D, N, 1, dt, T + short)
+    last = T - 1 - short
+    lengths = torch.tensor([T, last + 1], dtype=torch.int32) if short else None
+    for k in ("x", "dt", "z", "Bm", "Cm", "dy"):
+        p[k][1, last + 1:] = float("nan")
+    p["x"][1, last, ch] = 0.0
+    want = _scan_ref(p, lengths)
+    p["x"][1, last, ch] = INF
+    say(f"[scan bwd, infinite last token] T={T} length={last + 1} N={N}")
+    got = _scan_bwd(kda, p, lengths)
+    for k in ("dx", "dA", "dh0"):
+        _check(got[k], want[k], (slice(None),), k)
+    others = [d for d in range(D) if d != ch]
+    for k in ("dD", "ddt_bias"):
+        _check(got[k], want[k], others, k)
+        assert torch.isinf(got[k][ch]), k
+    for k in ("ddt", "dz"):
+        _check(got[k], want[k], (slice(None), slice(None), others), k)
+        assert not torch.isfinite(got[k][1, last, ch]), k   # (dz takes infinities of both signs)
+    for k in ("ddt", "dz", "dB", "dC"):
+        _check(got[k], want[k], (0,), k)
+        _check(got[k], want[k], (1, slice(0, last)), k)
+        assert (got[k][1, last + 1:] == 0).all(), k
+    assert torch.isinf(got["dB"][1, last]).all() and torch.isinf(got["dC"][1, last]).all()
+
+
 # ----------------------------------------------------------- nothing to sum
 
 @pytest.mark.parametrize("G", [1, 3])
