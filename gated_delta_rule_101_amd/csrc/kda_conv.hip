@@ -199,9 +199,11 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
         }
     };
     // One batch of tokens from t.  OWN: they belong to the run and enter dw and
-    // dbias (a token past the sequence has g = 0, and with it no share of
-    // anything); otherwise they are the W - 1 behind it.
-    const auto batch = [&](int t, auto own) {
+    // dbias; otherwise they are the W - 1 behind it.  A token past the sequence
+    // has no share of anything: its g is 0, but the inputs in its window may be
+    // infinite, so unless all are known to be INSIDE its dpre is chosen to be 0
+    // and dw takes nothing of it.
+    const auto batch = [&](int t, auto own, auto inside) {
         Pack<T, V> xi[BATCH], gi[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
@@ -211,6 +213,7 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
         if constexpr (decltype(own)::value) fetch(t + BATCH);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
+            const bool in = decltype(inside)::value || t + i < len;
             float g[V], out[V];
             xi[i].to_f32(win[W - 1]);
             gi[i].to_f32(g);
@@ -222,19 +225,21 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
 #pragma unroll
                     for (int j = 0; j < W; ++j) p = __builtin_fmaf(w[j][c], win[j][c], p);
                     const float sg = sigmoid_f32(p);
-                    v *= sg * __builtin_fmaf(p, 1.f - sg, 1.f);
+                    v = in ? v * (sg * __builtin_fmaf(p, 1.f - sg, 1.f)) : 0.f;
                 }
                 dp[W - 1][c] = v;
-                if constexpr (decltype(own)::value) {
-                    db[c] += v;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][c] = __builtin_fmaf(v, win[j][c], dw[j][c]);
-                }
                 float s = w[0][c] * v;
 #pragma unroll
                 for (int j = 1; j < W; ++j) s = __builtin_fmaf(w[j][c], dp[W - 1 - j][c], s);
                 out[c] = s;
             }
+            if (decltype(own)::value && in)
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    db[c] += dp[W - 1][c];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][c] = __builtin_fmaf(dp[W - 1][c], win[j][c], dw[j][c]);
+                }
             const int to = t + i - (W - 1);
             if (to < t1 && (to >= t0 || run == 0)) {
                 const int r = to - len + (W - 1);   // row of the final state that this input is
@@ -266,8 +271,17 @@ __global__ void __launch_bounds__(THREADS) kda_conv_bwd_kernel(ConvBwdArgs a, in
     };
     fetch(t0);
     int t = t0;
-    for (; t < t1; t += BATCH) batch(t, Flag<true>{});
-    if (t < t1 + W - 1) batch(t, Flag<false>{});   // a run's length is a multiple of BATCH unless the sequence ends in it
+    // The loops end at the last token that has a share of a gradient, W - 1 behind
+    // the run's or the sequence's last.  (A run's length is a multiple of BATCH
+    // unless the sequence ends in it.)
+    for (; t + BATCH <= min(t1, len); t += BATCH) batch(t, Flag<true>{}, Flag<true>{});
+    for (; t < min(t1, len + W - 1); t += BATCH) batch(t, Flag<true>{}, Flag<false>{});
+    if (t < min(t1, len) + W - 1) {
+        batch(t, Flag<false>{}, Flag<false>{});
+        t += BATCH;
+    }
+    const float zero[V] = {};
+    for (t = max(t - (W - 1), t0); t < t1; ++t) Pack<T, V>::unstream(dx + (int64_t)t * D, zero);
     float *pw = a.ws + rest * ((int64_t)D * W) + (int64_t)d * W;
     float *pb = a.ws + (int64_t)a.B * nruns * D * W + rest * D + d;
 #pragma unroll

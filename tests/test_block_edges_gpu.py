@@ -104,6 +104,31 @@ def test_scan_backward_infinite_last_token(kda, T, short, N, dt):
     assert torch.isinf(got["dB"][1, last]).all() and torch.isinf(got["dC"][1, last]).all()
 
 
+@pytest.mark.parametrize("T,short,W", [(5, 0, 4), (9, 3, 4), (14, 1, 3), (300, 0, 2), (301, 40, 4)])
+@pytest.mark.parametrize("value", [INF, float("nan")])
+def test_conv_backward_infinite_last_token(kda, T, short, W, value):
+    """Without the SiLU only dw's last tap takes the last input."""
+    B, D, ch = 2, 12, 5
+    g = torch.Generator().manual_seed(T)
+    x, dy = torch.randn((B, T, D), generator=g), torch.randn((B, T, D), generator=g)
+    w, s0, dsf = (torch.randn(s, generator=g) for s in ((D, W), (B, W - 1, D), (B, W - 1, D)))
+    last = T - 1 - short
+    lengths = torch.tensor([T, last + 1], dtype=torch.int32) if short else None
+    x[1, last + 1:] = dy[1, last + 1:] = float("nan")
+    x[1, last, ch] = 0.0
+    want = ref.conv_bwd(f64(dy), f64(x), f64(w), None, f64(s0), f64(dsf), lengths, False)
+    x[1, last, ch] = value
+    say(f"[conv bwd, {value} last token] T={T} length={last + 1} W={W}")
+    got = kda.kda_short_conv_bwd(_dev(dy), _dev(x), _dev(w), None, _dev(s0), silu=False, dstate_final=_dev(dsf),
+                                 lengths=_dev(lengths), want_dstate0=True)
+    torch.cuda.synchronize()
+    got = {k: v.cpu() for k, v in got.items()}
+    assert not torch.isfinite(got["dw"][ch, W - 1])
+    got["dw"][ch, W - 1] = want["dw"][0][ch, W - 1].float()
+    for k in want:
+        _check(got[k], want[k], (slice(None),), k)
+
+
 # ----------------------------------------------------------- nothing to sum
 
 @pytest.mark.parametrize("G", [1, 3])
