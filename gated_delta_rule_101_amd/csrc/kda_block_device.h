@@ -126,6 +126,30 @@ template <int CTRL> __device__ __forceinline__ float quad_add(float x)
     return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
 }
 
+// ----------------------------------------------------- states and places
+//
+// N states of a channel in NP places of registers, NP (a power of two) >= N.  Where
+// places are left they hold a state once more: a place that held none would
+// take part in the arithmetic with zeros, and 0 times an infinite s x is NaN.
+// With G the power of two in [N, 2 N), place p holds state p mod G, or that
+// less N; so a state has NP / G places, those in front of G - N twice as many,
+// each with the same values.  Sums over the states take each place's share of
+// its state, one over their number: exact, as that is a power of two.
+template <bool FILL> struct Places {
+    int n, g, places;
+    __device__ __forceinline__ Places(int N, int NP) : n(N), g(NP), places(NP) {
+        if (FILL)
+            while (g >= 2 * n) g >>= 1;
+    }
+    __device__ __forceinline__ int state(int p) const {
+        const int q = p & (g - 1);
+        return !FILL ? p : q < n ? q : q - n;
+    }
+    __device__ __forceinline__ float share(int p) const {
+        return !FILL ? 1.f : (state(p) < g - n ? 0.5f : 1.f) * (float)g / (float)places;
+    }
+};
+
 // Tokens of sequence b: lengths[b] clamped to [0, T], or T.
 __device__ __forceinline__ int seq_length(const int *lengths, int b, int T) {
     return lengths ? min(max(lengths[b], 0), T) : T;

@@ -1,10 +1,11 @@
 // Selective state space scan for gfx950, forward over a sequence and one token.
 //
-// Per channel d with N states (padded to NP = 16 NB):
+// Per channel d with N states (in NP = 16 NB places; where N is smaller, some states
+// have more than one, see Places):
 //   s = softplus(dt + bias),  h[n] <- exp(s A[n]) h[n] + s x B[n],
 //   y = (sum_n C[n] h[n] + D x) silu(z)
 //
-// A quad of lanes owns a channel, lane j of it states 4 j .. 4 j + 3 of each 16
+// A quad of lanes owns a channel, lane j of it places 4 j .. 4 j + 3 of each 16
 // in registers.  What a channel's token costs once
 // (softplus, gate, conversions) is dealt out over the quad: lane j takes every
 // fourth token and hands its s and s x to the others by DPP quad broadcasts,
@@ -65,12 +66,12 @@ __device__ __forceinline__ float quad_sums(const float (&y)[4])
 // behind a sequence's end, a token that changes nothing.
 __device__ __forceinline__ float finite_rate(float A2) { return A2 < -FLT_MAX ? -FLT_MAX : A2; }
 
-template <typename T, int NB, bool STATES_ONLY>
+template <typename T, int NB, bool STATES_ONLY, bool FILL>
 __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, int tiles)
 {
     constexpr int NP = 16 * NB, CHANNELS = 64;
-    __shared__ __attribute__((aligned(16))) float rows[2][2][CHUNK * NP];   // [buffer][B, C][token][state]
-    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * j;   // lane of the quad; its first state of each 16
+    __shared__ __attribute__((aligned(16))) float rows[2][2][CHUNK * NP];   // [buffer][B, C][token][place]
+    const int tid = threadIdx.x, j = tid & 3, n0 = 4 * j;   // lane of the quad; its first place of each 16
     unsigned id = blockIdx.x;
     const int tile = id % tiles;
     id /= tiles;
@@ -85,15 +86,16 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
     const int len = seq_length(a.lengths, b, a.T);
     const int t0 = seg * sg.tokens, t1 = min(t0 + sg.tokens, a.T), te = min(t1, len);
 
-    // states n0 + 16 m + n: rates in base 2, values
+    // places n0 + 16 m + n: their states' rates in base 2, values
     float A2[NB][4], h[NB][4];
-    const auto each_state = [&](auto f) {
+    const Places<FILL> places(N, NP);
+    const auto each_place = [&](auto f) {
 #pragma unroll
         for (int m = 0; m < NB; ++m)
 #pragma unroll
             for (int n = 0; n < 4; ++n) f(m, n, n0 + 16 * m + n);
     };
-    each_state([&](int m, int n, int st) { A2[m][n] = st < N ? finite_rate(a.A[(int64_t)d * N + st] * LOG2E) : 0.f; });
+    each_place([&](int m, int n, int s) { A2[m][n] = finite_rate(a.A[(int64_t)d * N + places.state(s)] * LOG2E); });
     const int64_t at_state = ((int64_t)b * D + d) * N;
     float *slots = sg.slots + ((int64_t)b * sg.count * D + d) * NP + n0, *sums = sg.sums + (int64_t)b * sg.count * D + d;
     const int64_t next_slot = (int64_t)D * NP;
@@ -106,10 +108,10 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
         for (int m = 0; m < NB; ++m) store4(slots + s * next_slot + 16 * m, h[m]);
     };
     if (seg == 0 && (STATES_ONLY || sg.count == 1)) {
-        each_state([&](int m, int n, int st) { h[m][n] = a.h0 && st < N ? a.h0[at_state + st] : 0.f; });
+        each_place([&](int m, int n, int s) { h[m][n] = a.h0 ? a.h0[at_state + places.state(s)] : 0.f; });
         if (STATES_ONLY && ok) store_slot(0);
     } else if (STATES_ONLY) {
-        each_state([&](int m, int n, int) { h[m][n] = 0.f; });
+        each_place([&](int m, int n, int) { h[m][n] = 0.f; });
     } else {
 #pragma unroll
         for (int m = 0; m < NB; ++m) load_slot(min(seg, 1), m, h[m]);
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
 #pragma unroll
             for (int k = 0; k < JOIN; ++k)
                 if (i + k <= seg)
-                    each_state([&](int m, int n, int) {
+                    each_place([&](int m, int n, int) {
                         h[m][n] = __builtin_fmaf(fast_exp2(A2[m][n] * s[k]), h[m][n], v[k][m][n]);
                     });
         }
@@ -142,7 +144,14 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) off[i] = (unsigned)(4 * i + j) * rb + dl;
     const int64_t row = (int64_t)a.G * N, row0 = ((int64_t)b * a.T * a.G + g) * N;
-    const int rt = tid / 16, rn = tid & 15;   // staging of B and C: token, state of a block
+    const int rt = tid / 16, rn = tid & 15;   // staging of B and C: token, place of a block
+    int from[NB];                             // the states there, and their shares
+    float share[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        from[nb] = places.state(16 * nb + rn);
+        share[nb] = places.share(16 * nb + rn);
+    }
 
     float sum = 0.f;   // of this lane's tokens
     if (t0 < te) {
@@ -161,9 +170,8 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
             const int64_t o = row0 + (int64_t)min(tc + rt, te - 1) * row;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const int st = min(16 * nb + rn, N - 1);
-                Br[nb] = ((const T *)a.Bm)[o + st];
-                if (!STATES_ONLY) Cr[nb] = ((const T *)a.Cm)[o + st];
+                Br[nb] = ((const T *)a.Bm)[o + from[nb]];
+                if (!STATES_ONLY) Cr[nb] = ((const T *)a.Cm)[o + from[nb]];
             }
         };
         fetch(t0);
@@ -171,9 +179,9 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
             float (&Bs)[CHUNK * NP] = rows[(tc / CHUNK) & 1][0], (&Cs)[CHUNK * NP] = rows[(tc / CHUNK) & 1][1];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const bool in = 16 * nb + rn < N && tc + rt < te;
+                const bool in = tc + rt < te;
                 Bs[rt * NP + 16 * nb + rn] = in ? to_f32(Br[nb]) : 0.f;
-                if (!STATES_ONLY) Cs[rt * NP + 16 * nb + rn] = in ? to_f32(Cr[nb]) : 0.f;
+                if (!STATES_ONLY) Cs[rt * NP + 16 * nb + rn] = in ? to_f32(Cr[nb]) * share[nb] : 0.f;
             }
             float x[4], s[4], z[4], u[4], r[4];
 #pragma unroll
@@ -276,8 +284,8 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
         if (!ok) return;
         for (int t = max(t0, te) + j; t < t1; t += 4) yb[(int64_t)t * D + d] = from_f32<T>(0.f);
         if (a.h_final && seg == sg.count - 1)
-            each_state([&](int m, int n, int st) {
-                if (st < N) a.h_final[at_state + st] = h[m][n];
+            each_place([&](int m, int n, int s) {
+                if (!FILL || s < N) a.h_final[at_state + s] = h[m][n];
             });
     }
 }
@@ -374,9 +382,11 @@ __global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int tile
         float (&h)[4] = hs[I];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            h[n] = __builtin_fmaf(fast_exp2(of_sequence<L, I>(s) * A2[n]), h[n], of_sequence<L, I>(u) * Bs[I][n]);
+            const float v = __builtin_fmaf(fast_exp2(of_sequence<L, I>(s) * A2[n]), h[n], of_sequence<L, I>(u) * Bs[I][n]);
+            h[n] = VEC || n0 + n < N ? v : 0.f;   // (with an infinite s x not 0 by itself)
             y[I] = __builtin_fmaf(Cs[I][n], h[n], y[I]);
         }
+        if (VEC && !in4) y[I] = 0.f;
         if (ok && q + side < B) {
             if constexpr (VEC) {
                 if (in4) Pack<float, 4>::unstream(hp, h);
@@ -456,11 +466,13 @@ template <typename T, int NB> hipError_t fwd_launch(const ScanArgs &a, hipStream
     if (s.count > 1) {
         s.slots = a.ws;
         s.sums = a.ws + (int64_t)a.B * s.count * 16 * NB * a.D;
-        kda_scan_kernel<T, NB, true><<<(unsigned)(blocks * (s.count - 1)), 256, 0, stream>>>(a, s, tiles);
+        (a.N == 16 * NB ? kda_scan_kernel<T, NB, true, false> : kda_scan_kernel<T, NB, true, true>)
+            <<<(unsigned)(blocks * (s.count - 1)), 256, 0, stream>>>(a, s, tiles);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    kda_scan_kernel<T, NB, false><<<(unsigned)(blocks * s.count), 256, 0, stream>>>(a, s, tiles);
+    (a.N == 16 * NB ? kda_scan_kernel<T, NB, false, false> : kda_scan_kernel<T, NB, false, true>)
+        <<<(unsigned)(blocks * s.count), 256, 0, stream>>>(a, s, tiles);
     return hipGetLastError();
 }
 

@@ -551,7 +551,7 @@ kda_status_t kda_short_conv_bwd(const void *dy, const void *x, const float *w, c
  *            does not fill the device)
  *
  * N from 1 to 64, G >= 1 dividing D (KDA_ERR_INVALID_ARG if it does not);
- * the states are padded to 16, 32 or 64.  G N below 2^24.
+ * the states take the room of 16, 32 or 64.  G N below 2^24.
  */
 size_t kda_selective_scan_fwd_workspace_bytes(int B, int T, int D, int N, int G);
 

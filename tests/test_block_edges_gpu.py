@@ -129,6 +129,71 @@ def test_conv_backward_infinite_last_token(kda, T, short, W, value):
         _check(got[k], want[k], (slice(None),), k)
 
 
+# ------------------------------------------------------------ padded states
+
+def _positive(p):
+    """Signs for which no two infinities meet with opposite ones; rates that keep a state."""
+    for k in ("x", "Bm", "Cm", "z", "dy", "h0", "D", "dh"):
+        p[k] = p[k].abs() + 0.1
+    p["A"] = p["A"] * 1e-4
+    return p
+
+
+@pytest.mark.parametrize("T", [3, 40, 700])
+@pytest.mark.parametrize("N", [1, 5, 16, 17, 33, 53])
+def test_scan_forward_infinite_input(kda, N, T):
+    """One infinite input makes its channel's outputs infinite from there on, for
+    any number of states; the other channels do not see it."""
+    B, D, ch, at = 2, 40, 2, T // 2
+    p = _positive(_scan_params(B, T, D, N, 1, F32, N + T))
+    p["x"][0, at, ch] = 0.0
+    args = [f64(p[k]) for k in ("x", "dt", "A", "Bm", "Cm", "h0", "D", "z", "dt_bias")]
+    want_y, want_h, _ = ref.scan_fwd(*args, True, None)
+    p["x"][0, at, ch] = INF
+    say(f"[scan fwd, infinite input] T={T} N={N}")
+    y, h = _scan_fwd(kda, p)
+    assert (y[0, at:, ch] == INF).all() and (h[0, ch] == INF).all()
+    others = [d for d in range(D) if d != ch]
+    _check(y, want_y, (slice(None), slice(None), others), "y")
+    _check(y, want_y, (1,), "y")
+    _check(y, want_y, (0, slice(0, at)), "y")
+    _check(h, want_h, (slice(None), others), "h_final")
+    _check(h, want_h, (1,), "h_final")
+
+
+@pytest.mark.parametrize("T", [21, 700])
+def test_scan_forward_infinite_time_step(kda, T):
+    """An infinite time step forgets the state; its own infinite input stays."""
+    B, D, N, ch, at = 1, 20, 5, 2, T // 2
+    p = _positive(_scan_params(B, T, D, N, 1, F32, T))
+    p["dt"][0, at, ch] = INF
+    say(f"[scan fwd, infinite step] T={T}")
+    y, h = _scan_fwd(kda, p)
+    assert (y[0, at:, ch] == INF).all() and (h[0, ch] == INF).all()
+    assert torch.isfinite(y[:, :, [d for d in range(D) if d != ch]]).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("N", [1, 3, 5, 6, 12, 16, 20, 33, 48])
+def test_scan_step_infinite_input(kda, N, dt):
+    B, D, ch = 5, 36, 2
+    p = _positive(_scan_params(B, 1, D, N, 1, dt, N))
+    p["x"][1, 0, ch] = 0.0
+    args = [f64(p[k]) for k in ("x", "dt", "A", "Bm", "Cm", "h0", "D", "z", "dt_bias")]
+    (ry, Ey), (rh, Eh), _ = ref.scan_fwd(*args, True, None)
+    p["x"][1, 0, ch] = INF
+    d = {k: _dev(v) for k, v in p.items()}
+    say(f"[scan step, infinite input] N={N}")
+    y = kda.kda_selective_scan_step(d["x"][:, 0], d["dt"][:, 0], d["A"], d["Bm"][:, 0], d["Cm"][:, 0], d["h0"],
+                                    D=d["D"], z=d["z"][:, 0], dt_bias=d["dt_bias"])
+    torch.cuda.synchronize()
+    y, h = y.cpu(), d["h0"].cpu()
+    assert y[1, ch] == INF and (h[1, ch] == INF).all()
+    y[1, ch], h[1, ch] = ry[1, 0, ch].to(dt), rh[1, ch].float()
+    _check(y, (ry[:, 0], Ey[:, 0]), (slice(None),), "y")
+    _check(h, (rh, Eh), (slice(None),), "h")
+
+
 # ----------------------------------------------------------- nothing to sum
 
 @pytest.mark.parametrize("G", [1, 3])
