@@ -145,9 +145,10 @@ template <bool FILL> struct Places {
         const int q = p & (g - 1);
         return !FILL ? p : q < n ? q : q - n;
     }
-    __device__ __forceinline__ float share(int p) const {
-        return !FILL ? 1.f : (state(p) < g - n ? 0.5f : 1.f) * (float)g / (float)places;
+    __device__ __forceinline__ float places_of(int p) const {   // of p's state
+        return !FILL ? 1.f : (float)(places / g * (state(p) < g - n ? 2 : 1));
     }
+    __device__ __forceinline__ float share(int p) const { return 1.f / places_of(p); }
 };
 
 // Tokens of sequence b: lengths[b] clamped to [0, T], or T.

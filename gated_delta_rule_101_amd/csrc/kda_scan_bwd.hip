@@ -48,7 +48,7 @@ int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }   // of 16
 // Workspace, in floats.
 struct Layout {
     int seg, nseg, nchunk;           // tokens a segment; segments, chunks
-    int tiles, np;                   // 64-channel tiles a group, padded states
+    int tiles, np;                   // 64-channel tiles a group, room for the states (16, 32 or 64)
     float *h, *g, *sum;              // [B][nseg][D][np] states in front / gradients behind; [B][nseg][D]
     float *hc, *sc;                  // [B][nchunk][D][np] states a segment adds up to a chunk; [B][nchunk][D]
     float *dA, *dD, *db;             // [B nseg][D][N], [B nseg][D] twice
@@ -396,7 +396,13 @@ template <int NB> struct Tiles {
 // token.  Chunks of such places only get zeros.  In the chunk of the last token
 // they carry on a state and a gradient that may be infinite, so what they would
 // add is chosen to be 0 and not multiplied by 0.
-template <typename T, int NB, bool TAIL>
+//
+// FILL: N is below NP, and states have several places (see Places).  Here the
+// gradients of the states, linear in C and in the gradient behind the segment,
+// carry the places' shares: with both times the share, the sums over places of
+// r, p1 and p2 are those over states, and dA, dB and dh0 of a place are divided
+// by it again.
+template <typename T, int NB, bool TAIL, bool FILL>
 __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &w, const Tiles<NB> &m, int tile, int grp,
                                             int seg, int b)
 {
@@ -432,12 +438,14 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
     constexpr int SLOTS = NB * CH * 16 / 256, NP = 16 * NB;
     const int c0 = grp * Dg + tile * CH, cmax = Dg - 1 - tile * CH;   // the tile's first channel; last one in it
     const auto chan = [&](int k) { return (unsigned)min((k * 256 + tid) / 16 % CH, cmax); };
-    const auto state = [&](int k) { return (unsigned)((k * 256 + tid) / (CH * 16) * 16 + (tid & 15)); };
+    const Places<FILL> places(N, NP);
+    const auto place = [&](int k) { return (k * 256 + tid) / (CH * 16) * 16 + (tid & 15); };
+    const auto state = [&](int k) { return (unsigned)places.state(place(k)); };
     const bool joined = w.nchunk > 1;   // otherwise the segment is the sequence, and its chunk the only one
     const auto seg_start = [&](int k) -> float {   // state in front of the segment
         const unsigned c = chan(k), st = state(k);
         if (joined) return w.h[(bseg * D + c0 + c) * NP + st];
-        return a.h0 && st < N ? a.h0[((int64_t)b * D + c0 + c) * N + st] : 0.f;
+        return a.h0 ? a.h0[((int64_t)b * D + c0 + c) * N + st] : 0.f;
     };
     // one block of states keeps its segment's start in registers and loads the
     // chunks' a chunk ahead; more of them would cost a wavefront a SIMD
@@ -447,8 +455,9 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
     for (int k = 0; k < SLOTS; ++k) {
         const unsigned c = chan(k), st = state(k);
         const int64_t own = ((int64_t)b * D + c0 + c) * N + st;   // in dh_final
-        (&l_A[0][0])[k * 256 + tid] = st < N ? a.A[(int64_t)(c0 + c) * N + st] : 0.f;
-        (&l_g[0][0])[k * 256 + tid] = joined ? w.g[(bseg * D + c0 + c) * NP + st] : a.dh_final && st < N ? a.dh_final[own] : 0.f;
+        const float behind = joined ? w.g[(bseg * D + c0 + c) * NP + st] : a.dh_final ? a.dh_final[own] : 0.f;
+        (&l_A[0][0])[k * 256 + tid] = a.A[(int64_t)(c0 + c) * N + st];
+        (&l_g[0][0])[k * 256 + tid] = behind * places.share(place(k));
         (&l_dA[0][0])[k * 256 + tid] = 0.f;
         if constexpr (AHEAD) h_seg[k] = seg_start(k);
     }
@@ -476,7 +485,7 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
         const unsigned o = (unsigned)max(min(tid / 16, len - 1 - tr0), 0) * (unsigned)row;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const unsigned st = min(nb * 16 + (tid & 15), N - 1);
+            const unsigned st = places.state(nb * 16 + (tid & 15));
             Br[nb] = Bp[o + st];
             Cr[nb] = Cp[o + st];
         }
@@ -532,9 +541,9 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
         store4(t_g + piece(lane, wave), g4);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const bool in = tid / 16 < nv && nb * 16 + (tid & 15) < N;
+            const bool in = tid / 16 < nv;
             t_B[nb][tid] = in ? to_f32(Br[nb]) : 0.f;
-            t_C[nb][tid] = in ? to_f32(Cr[nb]) : 0.f;
+            t_C[nb][tid] = in ? to_f32(Cr[nb]) * places.share(nb * 16 + (tid & 15)) : 0.f;
         }
         // a chunk's start: what the segment added so far, and the rest of its own start
         const int64_t ca = ((int64_t)b * w.nchunk + tc / CHUNK) * D + c0;
@@ -630,7 +639,8 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
 #pragma unroll
                 for (int j = 0; j < WAVES; ++j) s += flush[j][t8][lane];
                 const int t = t8 + 8 * ((lane >> 4) & 1);
-                if ((!TAIL || tc + t < a.T) && nb * 16 + n < N) dBC[(tc + t8) * row + nb * 16] = t < nv ? s : 0.f;
+                if (FILL && lane < 32) s *= places.places_of(nb * 16 + n);   // dB
+                if ((!TAIL || tc + t < a.T) && (!FILL || nb * 16 + n < N)) dBC[(tc + t8) * row + nb * 16] = t < nv ? s : 0.f;
             }
         }
 
@@ -665,9 +675,10 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
     __syncthreads();
     for (int i = tid; i < NB * CH * 16; i += 256) {
         const int nb = i / (CH * 16), c = i / 16 % CH, st = nb * 16 + (i & 15);
-        if (tile * CH + c < Dg && st < N) {
-            w.dA[(bseg * D + grp * Dg + tile * CH + c) * N + st] = l_dA[nb][i % (CH * 16)];
-            if (a.dh0 && w.nchunk == 1) a.dh0[((int64_t)b * D + grp * Dg + tile * CH + c) * N + st] = l_g[nb][i % (CH * 16)];
+        if (tile * CH + c < Dg && (!FILL || st < N)) {
+            const float f = places.places_of(st);
+            w.dA[(bseg * D + grp * Dg + tile * CH + c) * N + st] = l_dA[nb][i % (CH * 16)] * f;
+            if (a.dh0 && w.nchunk == 1) a.dh0[((int64_t)b * D + grp * Dg + tile * CH + c) * N + st] = l_g[nb][i % (CH * 16)] * f;
         }
     }
     t_s[wave * 64 + lane] = dD;
@@ -685,7 +696,7 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
     }
 }
 
-template <typename T, int NB>
+template <typename T, int NB, bool FILL>
 __global__ void __launch_bounds__(256, NB <= 2 ? 2 : 1) kda_scan_bwd_kernel(ScanBwdArgs a, Layout w)
 {
     __shared__ __attribute__((aligned(16))) float t_s[CH * 16], t_u[CH * 16], t_g[CH * 16];
@@ -703,8 +714,8 @@ __global__ void __launch_bounds__(256, NB <= 2 ? 2 : 1) kda_scan_bwd_kernel(Scan
     const int seg = id % w.nseg, b = id / w.nseg;
     const int t0 = seg * w.seg, chunks = (min(w.seg, a.T - t0) + CHUNK - 1) / CHUNK;
     // (Two bodies: with the choices of the second in one, B4 T4096 D4096 N16 took 5% longer.)
-    if (t0 + chunks * CHUNK <= seq_length(a.lengths, b, a.T)) bwd_segment<T, NB, false>(a, w, m, tile, grp, seg, b);
-    else bwd_segment<T, NB, true>(a, w, m, tile, grp, seg, b);
+    if (t0 + chunks * CHUNK <= seq_length(a.lengths, b, a.T)) bwd_segment<T, NB, false, FILL>(a, w, m, tile, grp, seg, b);
+    else bwd_segment<T, NB, true, FILL>(a, w, m, tile, grp, seg, b);
 }
 
 // Without tokens the state's gradient passes through.
@@ -726,7 +737,7 @@ template <typename T, int NB> hipError_t run(const ScanBwdArgs &a, const Layout 
         kda_scan_bwd_join_kernel<<<(unsigned)join, 256, 0, s>>>(a, w);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    kda_scan_bwd_kernel<T, NB><<<(unsigned)blocks, 256, 0, s>>>(a, w);
+    (a.N == w.np ? kda_scan_bwd_kernel<T, NB, false> : kda_scan_bwd_kernel<T, NB, true>)<<<(unsigned)blocks, 256, 0, s>>>(a, w);
     return hipGetLastError();
 }
 

@@ -466,7 +466,7 @@ kda_status_t kda_chunk_bwd(const void *q, const void *k, const void *v, const vo
  *    would reach HIP's limit of 2^32 threads, before anything is enqueued: a
  *    convolution has one thread per sequence, run of 4 to 256 tokens and 1 to
  *    8 channels, a scan 256 per sequence, group, 64 channels and segment, its
- *    gradients 2 per sequence, channel and padded state besides.
+ *    gradients 2 per sequence, channel and 16, 32 or 64 states besides.
  *  - lengths [B] int32 (device, or NULL: all T) are the sequences' lengths in
  *    a right-padded batch, clamped to [0, T].  Tokens behind a sequence's end
  *    enter no result (they may hold anything, NaN included); their outputs and

@@ -194,6 +194,47 @@ def test_scan_step_infinite_input(kda, N, dt):
     _check(h, (rh, Eh), (slice(None),), "h")
 
 
+@pytest.mark.parametrize("T", [7, 40, 700])
+@pytest.mark.parametrize("N", [1, 5, 16, 17, 33, 53])
+def test_scan_backward_infinite_upstream(kda, N, T):
+    """One infinite dy makes its channel's dx and that token's dB and dC infinite from
+    there backwards, and that token's dz; the other channels do not see it."""
+    B, D, ch, at = 2, 40, 2, T // 2
+    p = _positive(_scan_params(B, T, D, N, 1, F32, N + T))
+    p["dy"][0, at, ch] = 0.0
+    want = _scan_ref(p, None)
+    p["dy"][0, at, ch] = INF
+    say(f"[scan bwd, infinite upstream] T={T} N={N}")
+    got = _scan_bwd(kda, p, None)
+    assert (got["dx"][0, :at + 1, ch] == INF).all() and got["dz"][0, at, ch] == INF
+    assert (got["dB"][0, :at + 1] == INF).all() and (got["dC"][0, at] == INF).all()
+    assert (got["dA"][ch] == INF).all() and (got["dh0"][0, ch] == INF).all() and got["dD"][ch] == INF
+    others = [d for d in range(D) if d != ch]
+    for k in ("dx", "ddt", "dz"):
+        _check(got[k], want[k], (slice(None), slice(None), others), k)
+    for k in ("dx", "ddt", "dz", "dB"):
+        _check(got[k], want[k], (0, slice(at + 1, T)), k)
+        _check(got[k], want[k], (1,), k)
+    _check(got["dC"], want["dC"], (0, [t for t in range(T) if t != at]), "dC")
+    _check(got["dC"], want["dC"], (1,), "dC")
+    for k in ("dA", "dD", "ddt_bias"):
+        _check(got[k], want[k], others, k)
+    _check(got["dh0"], want["dh0"], (slice(None), others), "dh0")
+
+
+@pytest.mark.parametrize("N", [1, 5, 17, 33])
+def test_scan_backward_infinite_input_and_padded_states(kda, N):
+    """dz takes the read of the infinite state, which is infinite and not NaN."""
+    B, T, D, ch = 1, 32, 20, 2
+    p = _positive(_scan_params(B, T, D, N, 1, F32, N))
+    p["x"][0, T - 1, ch] = INF
+    say(f"[scan bwd, infinite input] N={N}")
+    got = _scan_bwd(kda, p, None)
+    assert got["dz"][0, T - 1, ch] == INF and got["ddt"][0, T - 1, ch] == INF
+    for k in ("dx", "dA", "dh0"):
+        assert torch.isfinite(got[k]).all(), k
+
+
 # ----------------------------------------------------------- nothing to sum
 
 @pytest.mark.parametrize("G", [1, 3])
