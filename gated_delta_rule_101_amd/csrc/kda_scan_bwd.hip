@@ -434,10 +434,12 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
     const int64_t row0 = ((int64_t)b * a.T * a.G + grp) * N, row = (int64_t)a.G * N;
 
     // Slots of the [channel][16] tiles: slot k of a thread is element k 256 + tid.
-    // Channels behind the group's last repeat it.
+    // Channels behind the group's last read it, but hold states and gradients of 0
+    // (0 times infinite ones would make NaN of dB and dC).
     constexpr int SLOTS = NB * CH * 16 / 256, NP = 16 * NB;
     const int c0 = grp * Dg + tile * CH, cmax = Dg - 1 - tile * CH;   // the tile's first channel; last one in it
     const auto chan = [&](int k) { return (unsigned)min((k * 256 + tid) / 16 % CH, cmax); };
+    const auto live = [&](int k) { return (k * 256 + tid) / 16 % CH <= cmax; };
     const Places<FILL> places(N, NP);
     const auto place = [&](int k) { return (k * 256 + tid) / (CH * 16) * 16 + (tid & 15); };
     const auto state = [&](int k) { return (unsigned)places.state(place(k)); };
@@ -457,7 +459,7 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
         const int64_t own = ((int64_t)b * D + c0 + c) * N + st;   // in dh_final
         const float behind = joined ? w.g[(bseg * D + c0 + c) * NP + st] : a.dh_final ? a.dh_final[own] : 0.f;
         (&l_A[0][0])[k * 256 + tid] = a.A[(int64_t)(c0 + c) * N + st];
-        (&l_g[0][0])[k * 256 + tid] = behind * places.share(place(k));
+        (&l_g[0][0])[k * 256 + tid] = live(k) ? behind * places.share(place(k)) : 0.f;
         (&l_dA[0][0])[k * 256 + tid] = 0.f;
         if constexpr (AHEAD) h_seg[k] = seg_start(k);
     }
@@ -562,7 +564,8 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
                 }
             }
             const float A2 = (&l_A[0][0])[k * 256 + tid] * LOG2E;
-            (&l_h[0][0])[k * 256 + tid] = c > 0 ? __builtin_fmaf(fast_exp2(A2 * sum), start, add) : start;
+            const float front = c > 0 ? __builtin_fmaf(fast_exp2(A2 * sum), start, add) : start;
+            (&l_h[0][0])[k * 256 + tid] = live(k) ? front : 0.f;
         }
         __syncthreads();
         fetch(max(c - 1, 0));

@@ -235,6 +235,26 @@ def test_scan_backward_infinite_input_and_padded_states(kda, N):
         assert torch.isfinite(got[k]).all(), k
 
 
+@pytest.mark.parametrize("T", [5, 32, 300])
+@pytest.mark.parametrize("D,G,N", [(1, 1, 16), (40, 1, 16), (65, 1, 16), (100, 2, 5), (130, 1, 33)])
+def test_scan_backward_infinite_last_channel(kda, D, G, N, T):
+    """Lanes behind a group's last channel repeat it; what is infinite in it enters the
+    rows of B and C once, as infinity."""
+    p = _positive(_scan_params(2, T, D, N, G, F32, D + T))
+    say(f"[scan bwd, infinite last channel] D={D} G={G} T={T}")
+    at = T // 2
+    p["x"][0, at, D - 1] = INF                 # from there on the state is infinite
+    p["dy"][1, at, D - 1] = INF                # back from there its gradient is
+    got = _scan_bwd(kda, p, None)
+    assert (got["dB"][0, at, G - 1] == INF).all() and (got["dC"][0, at:, G - 1] == INF).all()
+    assert (got["dB"][1, :at + 1, G - 1] == INF).all() and (got["dC"][1, at, G - 1] == INF).all()
+    for t in [t for t in range(T) if t != at]:
+        assert torch.isfinite(got["dB"][0, t]).all() and torch.isfinite(got["dC"][1, t]).all(), t
+    assert torch.isfinite(got["dB"][1, at + 1:]).all() and torch.isfinite(got["dC"][0, :at]).all()
+    for g in range(G - 1):
+        assert torch.isfinite(got["dB"][:, :, g]).all() and torch.isfinite(got["dC"][:, :, g]).all()
+
+
 # ----------------------------------------------------------- nothing to sum
 
 @pytest.mark.parametrize("G", [1, 3])
