@@ -126,6 +126,15 @@ template <int CTRL> __device__ __forceinline__ float quad_add(float x)
     return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
 }
 
+// Rates are used in base 2, and held where that is finite.  A lower one, -infinity
+// (-exp of a large number) among them, then still forgets at every positive step,
+// and leaves a token of step 0, such as those behind a sequence's end, a token
+// that changes nothing.
+__device__ __forceinline__ float finite_rate(float A) {
+    constexpr float LOWEST = -2.3586e38f;   // times LOG2E: -3.4027e38
+    return A < LOWEST ? LOWEST : A;
+}
+
 // ----------------------------------------------------- states and places
 //
 // N states of a channel in NP places of registers, NP (a power of two) >= N.  Where

@@ -31,7 +31,6 @@
 #include "kda_block_device.h"
 
 #include <algorithm>
-#include <cfloat>
 
 namespace kda {
 namespace {
@@ -60,11 +59,6 @@ __device__ __forceinline__ float quad_sums(const float (&y)[4])
     const float q0 = quad_add<SWAP1>(p0), q1 = quad_add<SWAP1>(p1);
     return j & 1 ? q1 : q0;
 }
-
-// A rate of -infinity (-exp of a large number) forgets at once; held finite, it
-// still does at every positive step and leaves a token of step 0, such as those
-// behind a sequence's end, a token that changes nothing.
-__device__ __forceinline__ float finite_rate(float A2) { return A2 < -FLT_MAX ? -FLT_MAX : A2; }
 
 template <typename T, int NB, bool STATES_ONLY, bool FILL>
 __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, int tiles)
@@ -95,7 +89,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
 #pragma unroll
             for (int n = 0; n < 4; ++n) f(m, n, n0 + 16 * m + n);
     };
-    each_place([&](int m, int n, int s) { A2[m][n] = finite_rate(a.A[(int64_t)d * N + places.state(s)] * LOG2E); });
+    each_place([&](int m, int n, int s) { A2[m][n] = finite_rate(a.A[(int64_t)d * N + places.state(s)]) * LOG2E; });
     const int64_t at_state = ((int64_t)b * D + d) * N;
     float *slots = sg.slots + ((int64_t)b * sg.count * D + d) * NP + n0, *sums = sg.sums + (int64_t)b * sg.count * D + d;
     const int64_t next_slot = (int64_t)D * NP;
@@ -352,7 +346,7 @@ __global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int tile
     }
     float A2[4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? finite_rate(a.A[(int64_t)d * N + n0 + n] * LOG2E) : 0.f;
+    for (int n = 0; n < 4; ++n) A2[n] = n0 + n < N ? finite_rate(a.A[(int64_t)d * N + n0 + n]) * LOG2E : 0.f;
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
     const auto own = [&](int k) { return first + (int64_t)(l % 4 + k * L) * per + side; };
     const auto token = [&](int k) { return (own(k) < B ? own(k) : B - 1) * D + d; };

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_segment_kernel(ScanBwdArgs a
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int st = n0 + 16 * m + n;
-            A2[m][n] = st < N ? a.A[(int64_t)d * N + st] * LOG2E : 0.f;
+            A2[m][n] = st < N ? finite_rate(a.A[(int64_t)d * N + st]) * LOG2E : 0.f;
             h[m][n] = r[m][n] = 0.f;
             P[m][n] = 1.f;
         }
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(256) kda_scan_bwd_join_kernel(ScanBwdArgs a, L
     const int64_t dn = id % per;
     const int d = (int)(dn / w.np), n = (int)(dn % w.np);
     const bool in = n < a.N;
-    const float A2 = in ? a.A[(int64_t)d * a.N + n] * LOG2E : 0.f;
+    const float A2 = in ? finite_rate(a.A[(int64_t)d * a.N + n]) * LOG2E : 0.f;
     const int64_t st = ((int64_t)b * a.D + d) * a.N + n, first = (int64_t)b * w.nseg * per + dn;
     const float *sums = w.sum + (int64_t)b * w.nseg * a.D + d;
     if (blockIdx.x & 1) {
@@ -458,7 +458,7 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
         const unsigned c = chan(k), st = state(k);
         const int64_t own = ((int64_t)b * D + c0 + c) * N + st;   // in dh_final
         const float behind = joined ? w.g[(bseg * D + c0 + c) * NP + st] : a.dh_final ? a.dh_final[own] : 0.f;
-        (&l_A[0][0])[k * 256 + tid] = a.A[(int64_t)(c0 + c) * N + st];
+        (&l_A[0][0])[k * 256 + tid] = finite_rate(a.A[(int64_t)(c0 + c) * N + st]);
         (&l_g[0][0])[k * 256 + tid] = live(k) ? behind * places.share(place(k)) : 0.f;
         (&l_dA[0][0])[k * 256 + tid] = 0.f;
         if constexpr (AHEAD) h_seg[k] = seg_start(k);

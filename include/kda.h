@@ -534,10 +534,11 @@ kda_status_t kda_short_conv_bwd(const void *dy, const void *x, const float *w, c
  *   y[d] = (sum_n Cm[g, n] h[d, n] + Dskip[d] x[d]) * (z[d] sigmoid(z[d]))
  *
  *   x, dt    [B, T, D]     dtype
- *   A        [D, N] float32; A <= 0 keeps the states bounded (not checked).  -infinity
- *            counts as the lowest finite rate (the gradients need finite rates); with
- *            A > 0 a segment's decay may overflow, and its states be NaN, earlier than
- *            token by token
+ *   A        [D, N] float32; A <= 0 keeps the states bounded (not checked).  Rates below
+ *            -2.3586e38, -infinity among them, count as that one, which forgets at
+ *            every positive step.  Where a segment's decay overflows (A > 0) or
+ *            underflows in front of an infinite state, the state may be NaN earlier
+ *            than token by token
  *   Bm, Cm   [B, T, G, N]  dtype; G groups of D / G channels each share them
  *   Dskip    [D] float32 or NULL (0);  dt_bias [D] float32 or NULL (0)
  *   z        [B, T, D]     dtype, or NULL: no gate

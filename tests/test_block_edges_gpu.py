@@ -255,6 +255,37 @@ def test_scan_backward_infinite_last_channel(kda, D, G, N, T):
         assert torch.isfinite(got["dB"][:, :, g]).all() and torch.isfinite(got["dC"][:, :, g]).all()
 
 
+# -------------------------------------------------------------------- rates
+
+@pytest.mark.parametrize("T,short", [(1, 0), (21, 0), (21, 6), (700, 0), (700, 400)])
+def test_scan_backward_lowest_finite_rates(kda, T, short):
+    """A finite rate whose base-2 form is not finite forgets at every positive step and
+    changes nothing in the places without one."""
+    B, D, N = 2, 20, 16
+    p = _scan_params(B, T, D, N, 1, F32, T + short)
+    p["A"][4] = -3e38
+    p["A"][7, ::3] = torch.finfo(F32).min
+    lengths = torch.tensor([T, T - short], dtype=torch.int32) if short else None
+    say(f"[scan bwd, lowest rates] T={T} length={T - short}")
+    got, want = _scan_bwd(kda, p, lengths), _scan_ref(p, lengths)
+    for k in want:
+        _check(got[k], want[k], (slice(None),), k)
+
+
+@pytest.mark.parametrize("T", [21, 300])
+def test_scan_backward_infinite_rates(kda, T):
+    """-infinity, which forgets at once: the gradients of the lowest finite rate."""
+    p = _scan_params(2, T, 20, 16, 1, F32, T)
+    lengths = torch.tensor([T, T - 6], dtype=torch.int32)
+    p["A"][4] = -3e38
+    want = _scan_ref(p, lengths)
+    p["A"][4] = -INF
+    say(f"[scan bwd, infinite rates] T={T}")
+    got = _scan_bwd(kda, p, lengths)
+    for k in want:
+        _check(got[k], want[k], (slice(None),), k)
+
+
 # ----------------------------------------------------------- nothing to sum
 
 @pytest.mark.parametrize("G", [1, 3])
