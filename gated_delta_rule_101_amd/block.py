@@ -24,9 +24,15 @@ import torch
 
 from .kda import _dtype_code, _nbytes, _ptr, _raise, load_library
 
-# Handle of the current stream of a device.  The public form builds a Stream
-# object for it: 1.1 us against 0.1, in calls of 8 us for the smallest operators.
-_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # (a torch without GPUs has none)
+
+def _stream_handle(index: int) -> int:
+    """Handle of the current stream of a device."""
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The same without a Stream object, where torch has it: 0.1 us against 1.1, in
+# calls of 8 us for the smallest operators.
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_handle)
 
 
 class _on:
