@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
     }
 
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
-    const bool gated = a.z != nullptr, soft = a.softplus;   // without a gate z reads x, unused
+    // without a gate z reads x, unused; without a skip nothing is added, not 0 times x
+    const bool gated = a.z != nullptr, skips = a.Dskip != nullptr, soft = a.softplus;
     const int64_t base = (int64_t)b * a.T * D;
     const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *zb = (const T *)(gated ? a.z : a.x) + base;
     T *yb = (T *)a.y + base;
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float gate = z[i] * sigmoid_f32(z[i]);
-                    r[i] = __builtin_fmaf(skip, x[i], r[i]) * (gated ? gate : 1.f);
+                    r[i] = (skips ? __builtin_fmaf(skip, x[i], r[i]) : r[i]) * (gated ? gate : 1.f);
                 }
                 if (ok) {
                     if (tc + CHUNK <= te) {
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int tile
 #pragma unroll
     for (int k = 0; k < K; ++k)
         if (ok && l < 4 && own(k) < B) {
-            const float v = __builtin_fmaf(skip, x[k], r[k]);
+            const float v = a.Dskip ? __builtin_fmaf(skip, x[k], r[k]) : r[k];
             ((T *)a.y)[token(k)] = from_f32<T>(a.z ? v * (z[k] * sigmoid_f32(z[k])) : v);
         }
 }

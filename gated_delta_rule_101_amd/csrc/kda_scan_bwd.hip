@@ -425,7 +425,8 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
     const bool ok = tile * CH + lane < Dg;
     const int d = grp * Dg + (ok ? tile * CH + lane : Dg - 1);
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
-    const bool gated = a.z != nullptr, soft = a.softplus;   // without a gate z reads x, unused
+    // without a gate z reads x, unused; without a skip nothing is added, not 0 times something
+    const bool gated = a.z != nullptr, skips = a.Dskip != nullptr, soft = a.softplus;
     const int64_t base = (int64_t)b * a.T * D;              // uniform; a lane adds its channel
     const T *xb = (const T *)a.x + base, *tb = (const T *)a.dt + base, *gb = (const T *)a.dy + base;
     const T *zb = (const T *)(gated ? a.z : a.x) + base;
@@ -661,8 +662,8 @@ __device__ __forceinline__ void bwd_segment(const ScanBwdArgs &a, const Layout &
         for (int i = 0; i < 4; ++i) {
             const bool in = 4 * wave + i < nv;
             const float ddt = in ? __builtin_fmaf(x4[i], p1[i], p2[i]) * ds4[i] : 0.f;
-            const float dx = in ? __builtin_fmaf(s4[i], p1[i], skip * g4[i]) : 0.f;
-            const float dz = in ? dz4[i] * __builtin_fmaf(skip, x4[i], r4[i]) : 0.f;
+            const float dx = in ? __builtin_fmaf(s4[i], p1[i], skips ? skip * g4[i] : 0.f) : 0.f;
+            const float dz = in ? dz4[i] * (skips ? __builtin_fmaf(skip, x4[i], r4[i]) : r4[i]) : 0.f;
             dD = __builtin_fmaf(g4[i], x4[i], dD);
             db += ddt;
             if (ok && (!TAIL || tc + 4 * wave + i < t1)) {

@@ -255,6 +255,50 @@ def test_scan_backward_infinite_last_channel(kda, D, G, N, T):
         assert torch.isfinite(got["dB"][:, :, g]).all() and torch.isfinite(got["dC"][:, :, g]).all()
 
 
+# ------------------------------------------------------ without skip and gate
+
+@pytest.mark.parametrize("N", [1, 16, 20])
+@pytest.mark.parametrize("gated", [False, True])
+def test_scan_infinite_input_without_skip(kda, gated, N):
+    """No D: nothing is added to the read, not 0 times an infinite input; nor is anything to dx and dz."""
+    B, T, D, ch, at = 2, 40, 24, 2, 20
+    p = _positive(_scan_params(B, T, D, N, 1, F32, N))
+    p["D"] = None
+    if not gated:
+        p["z"] = None
+    p["x"][0, at, ch] = INF
+    say(f"[scan without D, infinite input] N={N} gated={gated}")
+    y, h = _scan_fwd(kda, p)
+    assert (y[0, at:, ch] == INF).all() and (h[0, ch] == INF).all()
+    assert torch.isfinite(y[1]).all() and torch.isfinite(y[0, :at]).all()
+    d = {k: _dev(v) for k, v in p.items()}
+    h = d["h0"].clone()
+    one = {k: None if d[k] is None else d[k][:, at].contiguous() for k in ("x", "dt", "Bm", "Cm", "z")}
+    y = kda.kda_selective_scan_step(one["x"], one["dt"], d["A"], one["Bm"], one["Cm"], h, z=one["z"],
+                                    dt_bias=d["dt_bias"])
+    torch.cuda.synchronize()
+    assert y[0, ch] == INF and torch.isfinite(y[1]).all()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_scan_backward_infinite_upstream_without_skip(kda, gated):
+    B, T, D, N, ch, at = 2, 40, 24, 16, 2, 20
+    p = _positive(_scan_params(B, T, D, N, 1, F32, 3))
+    p["D"] = None
+    if not gated:
+        p["z"] = None
+    p["dy"][0, at, ch] = INF
+    p["x"][1, T - 1, ch] = INF
+    say(f"[scan bwd without D, infinite upstream and input] gated={gated}")
+    got = _scan_bwd(kda, p, None)
+    assert (got["dx"][0, :at + 1, ch] == INF).all() and torch.isfinite(got["dx"][1]).all()
+    if gated:
+        assert got["dz"][0, at, ch] == INF and got["dz"][1, T - 1, ch] == INF
+    else:
+        assert "dz" not in got
+    assert "dD" not in got
+
+
 # -------------------------------------------------------------------- rates
 
 @pytest.mark.parametrize("T,short", [(1, 0), (21, 0), (21, 6), (700, 0), (700, 400)])
