@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
                 tr[i] = ts.load(o, 0);
                 if (!STATES_ONLY) zr[i] = zs.load(o, 0);
             }
+            __builtin_amdgcn_sched_barrier(0);   // the order in which they are used
             const int64_t o = row0 + (int64_t)min(tc + rt, te - 1) * row;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
