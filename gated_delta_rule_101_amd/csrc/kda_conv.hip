@@ -9,9 +9,8 @@
 // its tokens once plus W - 1 tokens in front (which its neighbour run brings
 // into the cache as well).  Rows whose length is no multiple of V are walked
 // one channel a thread.  Measured (bfloat16, W = 4): forward of B4 T16384 D4096
-// 0.209 ms, 5.1 TB/s; backward of B4 T4096 D4096 0.091 ms, 4.4 TB/s (0.094 without
-// the non-temporal loads, the same with 8 tokens requested together, 0.10 with
-// three wavefronts a SIMD instead of two).
+// 0.209 ms, 5.1 TB/s; backward of B4 T4096 D4096 0.085 ms, 4.7 TB/s (0.003 more without
+// the non-temporal loads, the same with 8 tokens requested together).
 #include "kda_block.h"
 #include "kda_block_device.h"
 

@@ -293,7 +293,7 @@ int64_t bwd_blocks(int64_t rows, int tpr)
 }
 
 // f(integral constants V, NV, TPR): 16 / sizeof(T) elements an access where
-// D allows it; 8 or 16 elements a thread.
+// D allows it; 8 or 16 elements a thread, 16 or 32 above 4096 channels.
 template <int N> struct Int { static constexpr int value = N; };
 template <typename T, int V, typename F> hipError_t by_size(int D, int tpr, F f)
 {

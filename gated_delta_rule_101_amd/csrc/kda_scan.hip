@@ -23,10 +23,10 @@
 // segment's true starting state from those (the decay of a whole segment is
 // exp(A sum s)) and runs it again with the outputs.
 //
-// Measured (bfloat16, N = 16): B4 T4096 D4096, one chain of 1024 wavefronts, 0.426
-// ms (8.3 vector instructions a state and token; four wavefronts a SIMD would
-// take 0.31); B1 T16384 D4096, 32 segments, 0.467 ms; one token of B256 D12288 0.077 ms, 5.5
-// TB/s.
+// Measured (bfloat16, N = 16): B4 T4096 D4096, one chain of 1024 wavefronts, 0.432
+// ms (8.1 vector instructions a state and token; four wavefronts a SIMD would
+// take 0.31); B1 T16384 D4096, 32 segments, 0.464 ms; one token of B256 D12288 0.076
+// ms, 5.7 TB/s.
 #include "kda_block.h"
 #include "kda_block_device.h"
 
@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(256) kda_scan_kernel(ScanArgs a, Segments sg, 
 // before the first is used, and as they pass once they are non-temporal.
 //
 // A workgroup takes 256 / L channels; where there are fewer, sequences lie side by
-// side in it, 1 << shift threads each.  Measured (bfloat16): B256 D12288 N16 0.077
-// ms, 5.5 TB/s; 0.101 with four channels of one sequence a thread, each with its
+// side in it, 1 << shift threads each.  Measured (bfloat16): B256 D12288 N16 0.076
+// ms, 5.7 TB/s; 0.101 with four channels of one sequence a thread, each with its
 // own rates, positions and softplus (twice the vector instructions).
 template <int L, int I, int K> __device__ __forceinline__ float of_sequence(const float (&v)[K])
 {

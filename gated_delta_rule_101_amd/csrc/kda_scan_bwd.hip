@@ -29,9 +29,9 @@
 //     and enter the arithmetic as DPP row
 //     broadcasts, without instructions of their own.
 //  4. Column sums of the workgroups' partial dA, dD, dbias, dB, dC.
-// Bound by vector instructions, 25 per token, channel and state in kernel 3 and 9
-// in kernel 1.  Measured: B4 T4096 D4096 N16 bfloat16 1.23 ms (kernels 1 to 4 under
-// a trace, at lower clocks: 0.36, 0.015, 0.92 and 0.03).
+// Bound by vector instructions, 26 per token, channel and state in kernel 3 and 10
+// in kernel 1.  Measured: B4 T4096 D4096 N16 bfloat16 1.24 ms (kernels 1 to 4 under
+// a trace, at lower clocks: 0.36, 0.015, 0.94 and 0.03).
 #include "kda_block.h"
 #include "kda_block_device.h"
 

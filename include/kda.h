@@ -599,7 +599,11 @@ kda_status_t kda_selective_scan_bwd(const void *dy, const void *x, const void *d
  *
  *   x, y   [rows, D] dtype; y may be x itself
  *   weight [D] float32 or NULL (1), bias [D] float32 or NULL (0)
- *   eps    >= 0, finite (a constant row with eps = 0 is NaN, as the formula is)
+ *   eps    >= 0, finite.  With eps = 0 a row of one value has no defined result (0 / 0
+ *          by the formula; NaN, or what rounding leaves of the mean, magnified)
+ *
+ * Centred values are squared in float32: their squares' sum has to stay below its
+ * 3.4e38 (beyond, the variance is infinite and y is bias).
  *
  * D from 1 to 16384 (KDA_ERR_UNSUPPORTED beyond), rows below 2^40.
  */
