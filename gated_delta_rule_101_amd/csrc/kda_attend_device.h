@@ -1,0 +1,296 @@
+// Device pieces of attention over the 8-bit paged cache, shared by the kernel
+// for few queries a sequence and the one for prompts.
+#pragma once
+
+#include "kda_attn.h"
+#include "kda_code8.h"
+
+namespace kda {
+
+__device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
+
+// A sequence of the call: its first query row, queries and tokens in the cache.
+// Held inside the buffers whatever the device's numbers say.
+struct Sequence {
+    int first, queries, context;
+};
+__device__ __forceinline__ Sequence sequence(const AttendArgs &a, int b)
+{
+    Sequence s;
+    if (a.q_start) {
+        const int x = min(max(a.q_start[b], 0), a.tokens), y = min(max(a.q_start[b + 1], x), a.tokens);
+        s.first = x;
+        s.queries = y - x;
+    } else {
+        s.first = b;
+        s.queries = 1;
+    }
+    const int64_t room = (int64_t)a.per * a.page;
+    const int c = max(a.context[b], 0);
+    s.context = c < room ? c : (int)room;
+    return s;
+}
+
+// The page of a token, -1 where there is none: behind the last token, or an
+// entry that names no page of the cache.
+__device__ __forceinline__ int page_of(const AttendArgs &a, const int *table, int token, int context, int shift)
+{
+    if (token >= context) return -1;
+    const int id = table[token >> shift];
+    return (unsigned)id < (unsigned)a.pages ? id : -1;
+}
+
+// Over the four lanes that hold one query (m, m + 16, m + 32, m + 48).
+__device__ __forceinline__ float quarters_max(float x)
+{
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+__device__ __forceinline__ float quarters_sum(float x)
+{
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+// 8 values as SPLIT float16 parts: nearest, then nearest of what is left.
+template <int SPLIT, typename F> __device__ __forceinline__ void split_f16(const float *x, F part)
+{
+    f16x8 y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = (_Float16)x[i];
+    part(0) = y;
+    if constexpr (SPLIT == 2) {
+        f16x8 z;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = (_Float16)(x[i] - (float)y[i]);
+        part(1) = z;
+    }
+}
+
+// e with most 2^e in [2^14, 2^15), by the exponent's bits; 0 where most is 0 or not finite.
+__device__ __forceinline__ int range_exponent(float most)
+{
+    const int ex = (int)(__float_as_uint(most) >> 23);
+    return ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
+}
+
+// One query row (zeros unless `real`) as the second operand of the score products,
+// scaled into float16's range; returns what the products are to be multiplied
+// by.  A lane's channels are 64 c + 16 quarter + 0 .. 15 for each c, which are
+// inner steps 2 c and 2 c + 1: the order in which it reads keys.
+template <typename T, int D, int SPLIT, int KS, typename F>
+__device__ __forceinline__ float load_query(const T *p, bool real, int quarter, F part)
+{
+    float x[D / 64][16], most = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+            Raw8<T> raw;
+            raw.load(p + 64 * c + 16 * quarter + e);
+            float v[8];
+            raw.to_f32(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[c][e + i] = real ? v[i] : 0.f;
+                most = fmaxf(most, fabsf(x[c][e + i]));
+            }
+        }
+    most = quarters_max(most);
+    const int e = range_exponent(most);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __builtin_ldexpf(x[c][8 * k + i], e);
+            split_f16<SPLIT>(v, [&](int s) -> f16x8 & { return part(s, 2 * c + k); });
+        }
+    return __builtin_ldexpf(1.f, -e);
+}
+
+// The same for 32x32x16 products: a lane's channels are 16 k + 8 half + 0 .. 7.
+// The sign of the softmax's scale goes with the query, so that maxima of the
+// products are maxima of the scores.
+template <typename T, int D, int SPLIT>
+__device__ __forceinline__ float load_row(const T *p, bool real, int half, bool negative, f16x8 (&q)[SPLIT][D / 16])
+{
+    float x[D / 16][8], most = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        Raw8<T> raw;
+        raw.load(p + 16 * k + 8 * half);
+        raw.to_f32(x[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[k][i] = !real ? 0.f : negative ? -x[k][i] : x[k][i];
+            most = fmaxf(most, fabsf(x[k][i]));
+        }
+    }
+    const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(most), __float_as_uint(most), false, false);
+    most = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+    const int e = range_exponent(most);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k][i] = __builtin_ldexpf(x[k][i], e);
+        split_f16<SPLIT>(x[k], [&](int s) -> f16x8 & { return q[s][k]; });
+    }
+    return __builtin_ldexpf(1.f, -e);
+}
+
+// The page's value scale as a fraction of the wave's reference, which is twice
+// the largest scale met and moves (with the outputs, which are in its units)
+// when a larger one comes.  Not below 2^-40: what such a page adds is lost in
+// rounding anyway, and its weights still count in the sum.  Times 2^14, which
+// leaves float16 normal weights down to 2^-28.  Scales that are not finite pass
+// as 0 here: the weights of their tokens are made NaN behind the sum.
+constexpr float VALUE_GAIN = 0x1p14f, VALUE_REST = 0x1p-14f;
+__device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+template <int NR, int DT>
+__device__ __forceinline__ float value_ratio(float scale, float &reference, f32x4 (&o)[NR][DT])
+{
+    const float most = quarters_max(scale);
+    if (__any(most > reference)) {
+        const float next = 2.f * most, f = reference / next;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][d][i] *= f;
+        reference = next;
+    }
+    const float r = reference > 0.f ? scale / reference : 1.f;
+    return VALUE_GAIN * fmaxf(r, 0x1p-40f);
+}
+
+// 16 bytes with those from place n on cleared.
+__device__ __forceinline__ uint4 keep_bytes(uint4 x, int n)
+{
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = n - 4 * i;
+        w[i] = k >= 4 ? w[i] : k <= 0 ? 0u : w[i] & ((1u << (8 * k)) - 1u);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A call's pieces in its workspace: one record a workgroup, then two pieces each.
+struct Record {      // a row of units that is cut: its first piece is this workgroup's
+    int b, h, block, last;                   // last: the workgroup of its last piece, -1: none
+};
+constexpr int SHARES = 512;                  // workgroups that share the line of units, at most
+// Floats of one piece: output rows, then maxima and sums.
+template <int D, int ROWS> constexpr int PIECE = ROWS * (D + 2);
+
+// Four channels of a finished row (index i G + g): o / l, 0 where nothing was
+// seen; with the first, the row's log of the weights' sum.
+template <typename T>
+__device__ __forceinline__ void write_row(const AttendArgs &a, const Sequence &s, int h, int G, int r, int d, int D,
+                                          const float (&y)[4], float best, float l)
+{
+    const int i = r / G, g = r - i * G;
+    const int64_t at = (int64_t)(s.first + i) * a.Hq + h * G + g;
+    const bool none = l == 0.f;                // a row that saw something has its maximum's weight, 1, in l
+    const float inv = 1.f / l;
+    const float z[4] = {none ? 0.f : y[0] * inv, none ? 0.f : y[1] * inv, none ? 0.f : y[2] * inv, none ? 0.f : y[3] * inv};
+    store4((T *)a.out + at * D + d, z);
+    if (a.lse && d == 0) a.lse[at] = none ? -__builtin_inff() : (best + fast_log2(l)) * LN2;
+}
+
+// A value that all lanes hold, as the scalar it is.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x)
+{
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x));
+}
+
+// The line of units: 64 tokens of one sequence, key head and block of query rows,
+// sequences, heads, blocks and tokens in that order.  A workgroup's share of it.
+struct Line {
+    int b;                                   // sequence of the next unit
+    int64_t u;                               // the unit's place among its sequence's
+    int64_t left, at, share;                 // units to do, place on the line, units a workgroup
+};
+__device__ __forceinline__ int tiles_of(const Sequence &s) { return max((s.context + 63) / 64, 1); }
+__device__ __forceinline__ int blocks_of(const Sequence &s, int G, int rows)
+{
+    return (int)(((int64_t)s.queries * G + rows - 1) / rows);
+}
+template <int WAVES> __device__ __forceinline__ int64_t workgroup_sum(int64_t x, int64_t *part)
+{
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) x += part[w];
+    __syncthreads();
+    return x;
+}
+// `at_least`: a share's least units, where rows of units are that long; short
+// rows stay whole.  part: [WAVES] in LDS.
+template <int WAVES>
+__device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of_block, int at_least, int64_t *part)
+{
+    const int lane = threadIdx.x & 63;
+    int64_t units = 0, rows = 0;
+    for (int b = threadIdx.x; b < a.B; b += 64 * WAVES) {
+        const Sequence s = sequence(a, b);
+        const int64_t r = (int64_t)blocks_of(s, G, rows_of_block) * a.Hk;
+        rows += r;
+        units += r * tiles_of(s);
+    }
+    units = uniform(workgroup_sum<WAVES>(units, part));
+    rows = uniform(workgroup_sum<WAVES>(rows, part));
+    Line l = {0, 0, 0, 0, 1};
+    if (units == 0) return l;
+    const int64_t least = min((int64_t)at_least, (units + rows - 1) / rows);
+    l.share = max((units + gridDim.x - 1) / gridDim.x, least);
+    l.at = l.share * blockIdx.x;
+    l.left = max((int64_t)0, min(l.share, units - l.at));
+    if (l.left == 0) return l;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        int64_t n = 0;
+        if (b0 + lane < a.B) {
+            const Sequence s = sequence(a, b0 + lane);
+            n = (int64_t)blocks_of(s, G, rows_of_block) * a.Hk * tiles_of(s);
+        }
+        int64_t upto = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t y = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += y;
+        }
+        const uint64_t past = __ballot(before + upto > l.at);
+        if (past) {
+            const int f = __builtin_ctzll(past);
+            l.b = b0 + f;
+            l.u = uniform(l.at - before - __shfl(upto - n, f, 64));
+            break;
+        }
+        before = uniform(before + __shfl(upto, 63, 64));
+    }
+    return l;
+}
+
+// Workgroups for a line of at most `units` units.
+inline int shares(int64_t units) { return units < SHARES && units > 0 ? (int)units : SHARES; }
+
+// The launcher for many query rows a sequence (kda_cache_attend_rows.hip), and
+// floats of workspace it may need.
+hipError_t launch_attend_rows(const AttendArgs &a, hipStream_t stream);
+int64_t attend_rows_workspace_floats(int tokens, int B, int Hq, int Hk, int D, int page, int per, int most);
+// The second launch of a line with blocks of ROWS query rows.
+template <int ROWS> hipError_t launch_attend_join(const AttendArgs &a, int workgroups, int rows, hipStream_t stream);
+
+}  // namespace kda

@@ -1,0 +1,380 @@
+// Attention over the 8-bit paged cache for gfx950, for few queries a sequence:
+//   s = scale (q . K) k_scale, o = sum softmax(s) V v_scale, query i of n at
+// position context - n + i seeing places up to its own.
+//
+// Bound by HBM bandwidth: every code is read once for the G = Hq / Hk heads and
+// the queries that share it, which make the columns of the products.  With
+// 16x16x32 float16 products and the score tile transposed (tokens x queries), a
+// lane holds 16 neighbouring tokens' scores of one query.  Which token a tile's
+// row is, and which channel an inner index, is free as long as both operands
+// agree; chosen so that a lane's codes are 16 neighbouring bytes: of a key's
+// row, and of a channel's row in the values' pages, which hold tokens innermost
+// for this.  So codes go from memory to registers to float16 (exact for either
+// code), and weights from scores to the second product, with neither LDS nor
+// exchanges between lanes.
+//
+// Work is counted in units: 64 tokens of one sequence, key head and block of
+// 16 NR queries.  All units of the call lie on one line which is cut into equal
+// shares, one a workgroup, whatever the lengths are; its waves take turns at a
+// share's units.  A share that ends inside a row of units leaves its running
+// maximum, sum and output in the workspace, and a second launch joins them.
+//
+// Float16: queries are scaled by a power of two that puts their row's largest
+// channel at 2^14 .. 2^15 (bfloat16 fits exactly, what is lost of a channel is
+// under 2^-39 of the largest); weights are at most 1, times the ratio of
+// the page's value scale to the largest met so far (also in the exponent, so
+// that no page's scale loses range), and are rounded to 11 bits.  Float32
+// queries and weights are taken in two float16 parts.
+#include "kda_attn.h"
+#include "kda_block.h"
+#include "kda_attend_device.h"
+
+namespace kda {
+namespace {
+
+template <int D, int NR, bool BF, bool INT8>
+__global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_attend_kernel(AttendArgs a, int shift)
+{
+    constexpr int SPLIT = BF ? 1 : 2, KS = D / 32, DT = D / 16, ROWS = 16 * NR;
+    typedef typename Store<BF>::type T;
+    __shared__ int64_t part[4];
+    __shared__ __align__(16) float merge[4][16][D + 4];
+    __shared__ float stat[4][2][ROWS];
+    __shared__ float ref[4];
+    const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x & 63, m = lane & 15, quarter = lane >> 4;
+    const int G = a.Hq / a.Hk;
+    Line line = cut_line<4>(a, G, ROWS, 4, part);    // a unit for each wave
+    Record mine = {0, 0, 0, -1};
+    float *const pieces = a.ws + (sizeof(Record) / 4) * gridDim.x;
+    while (line.left > 0) {
+        const Sequence s = sequence(a, line.b);
+        const int tiles = tiles_of(s), blocks = blocks_of(s, G, ROWS);
+        const int64_t u = line.u;
+        if (u >= (int64_t)tiles * blocks * a.Hk) {
+            line.u = 0;
+            ++line.b;
+            continue;
+        }
+        const int b = line.b;
+        const int row = (int)(u / tiles), t_begin = (int)(u - (int64_t)row * tiles);
+        const int t_end = (int)min((int64_t)tiles, t_begin + line.left);
+        const int h = row / blocks, block = row - h * blocks;
+        const int r0 = block * ROWS, active = min(ROWS, s.queries * G - r0);
+        // queries: lane m is row r0 + 16 n + m
+        f16x8 q[SPLIT][NR][KS];
+        float factor[NR];
+        int limit[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const int r = 16 * n + m, x = r0 + min(r, active - 1), i = x / G, g = x - i * G;
+            const T *p = (const T *)a.q + ((int64_t)(s.first + i) * a.Hq + h * G + g) * D;
+            limit[n] = r < active ? s.context - s.queries + i + 1 : 0x7fffffff;
+            factor[n] = load_query<T, D, SPLIT, KS>(p, r < active, quarter, [&](int x, int k) -> f16x8 & { return q[x][n][k]; }) *
+                        a.scale * LOG2E;
+        }
+        // tiles with every place seen by every row need no mask
+        const int whole = min(s.context - s.queries + r0 / G + 1, s.context);
+        const int furthest = min(s.context, s.context - s.queries + (r0 + active - 1) / G + 1);
+
+        f32x4 o[NR][DT];
+        float top[NR], sum[NR], reference = 0.f;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            top[n] = -__builtin_inff();
+            sum[n] = 0.f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        const int *table = a.table + (int64_t)b * a.per;
+        for (int t = t_begin + wave; t < t_end; t += 4) {
+            const int t0 = t * 64;
+            if (t0 >= furthest) break;
+            // pages of this lane's key rows (group m / 4) and of its scores' tokens (group = quarter)
+            const int gk = m >> 2;
+            const int pk = page_of(a, table, t0 + 16 * gk, s.context, shift);
+            const int pv = page_of(a, table, t0 + 16 * quarter, s.context, shift);
+            const int64_t ak = (int64_t)max(pk, 0) * a.Hk + h, av = (int64_t)max(pv, 0) * a.Hk + h;
+            const uint8_t *kp = a.k_codes + (ak * a.page + ((t0 + 16 * gk) & (a.page - 1)) + (m & 3)) * D + 16 * quarter;
+            const uint8_t *vp = a.v_codes + (av * D + m) * a.page + ((t0 + 16 * quarter) & (a.page - 1));
+            uint4 kr[4][D / 64], vr[DT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    kr[i][c] = *reinterpret_cast<const uint4 *>(kp + 4 * i * D + 64 * c);
+            const float ks = a.k_scale[av], vs = a.v_scale[av];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) vr[d] = *reinterpret_cast<const uint4 *>(vp + (int64_t)16 * d * a.page);
+
+            f16x8 ka[4][KS];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    ka[i][2 * c] = codes_f16<INT8>(kr[i][c].x, kr[i][c].y);
+                    ka[i][2 * c + 1] = codes_f16<INT8>(kr[i][c].z, kr[i][c].w);
+                }
+            const int tb = t0 + 16 * quarter;                  // this lane's first token
+            const bool masked = t0 + 64 > whole || __any(pv < 0);
+            const bool broken = pv >= 0 && !is_finite(vs);
+            const float ratio = value_ratio<NR, DT>(pv < 0 || broken ? 0.f : vs, reference, o);
+            const float shift_v = fast_log2(ratio);
+            f16x8 w[SPLIT][NR][2];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                if (NR > 1) __builtin_amdgcn_sched_barrier(0);     // one row tile's scores at a time, for the registers
+                const float c = factor[n] * (pv < 0 ? 0.f : ks);
+                const int seen = pv < 0 ? 0 : min(limit[n], s.context) - tb;     // of this lane's 16 tokens
+                float v[16], best = -__builtin_inff();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int p = 0; p < SPLIT; ++p)
+                            x = __builtin_amdgcn_mfma_f32_16x16x32_f16(ka[i][k], q[p][n][k], x, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j] * c;
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = i < seen ? v[i] : -__builtin_inff();
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) best = fmaxf(best, v[i]);
+                best = quarters_max(best);
+                const float now = fmaxf(top[n], best), base = now == -__builtin_inff() ? 0.f : now;
+                const float fade = fast_exp2(top[n] - base);
+                top[n] = now;
+                if (__any(fade != 1.f)) {
+                    sum[n] *= fade;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[n][d][i] *= fade;
+                }
+                float total = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[i] = fast_exp2(v[i] - (base - shift_v));
+                    total += v[i];
+                }
+                sum[n] += total * fast_rcp(ratio);
+                if (__any(broken)) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = broken && i < seen ? __builtin_nanf("") : v[i];
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) split_f16<SPLIT>(v + 8 * k, [&](int p) -> f16x8 & { return w[p][n][k]; });
+            }
+            if (NR > 1) __builtin_amdgcn_sched_barrier(0);
+            if (masked && !INT8) {
+                // weights of places that hold no token are zero; their codes must not be NaN
+                const int there = pv < 0 ? 0 : s.context - tb;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) vr[d] = keep_bytes(vr[d], there);
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const f16x8 lo = codes_f16<INT8>(vr[d].x, vr[d].y), hi = codes_f16<INT8>(vr[d].z, vr[d].w);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int p = 0; p < SPLIT; ++p) {
+                        o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, w[p][n][0], o[n][d], 0, 0, 0);
+                        o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, w[p][n][1], o[n][d], 0, 0, 0);
+                    }
+            }
+        }
+
+        // The four waves' parts meet: scaled to the common maximum and reference.
+        if (lane == 0) ref[wave] = reference;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            sum[n] = quarters_sum(sum[n]);
+            if (quarter == 0) {
+                stat[wave][0][16 * n + m] = top[n];
+                stat[wave][1][16 * n + m] = sum[n];
+            }
+        }
+        const bool whole_row = t_begin == 0 && t_end == tiles;
+        float *piece = pieces + (int64_t)(2 * blockIdx.x + (t_begin == 0)) * PIECE<D, ROWS>;
+        if (t_begin == 0 && !whole_row) mine = {b, h, block, (int)((line.at + tiles - 1) / line.share)};
+        line.u += t_end - t_begin;
+        line.left -= t_end - t_begin;
+        line.at += t_end - t_begin;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            __syncthreads();
+            float best = -__builtin_inff();
+#pragma unroll
+            for (int v = 0; v < 4; ++v) best = fmaxf(best, stat[v][0][16 * n + m]);
+            // in units of the values: times the reference, which is 0 where every value was
+            const float f = (best == -__builtin_inff() ? 1.f : fast_exp2(top[n] - best)) * (ref[wave] * VALUE_REST);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) merge[wave][m][16 * d + 4 * quarter + i] = o[n][d][i] * f;
+            __syncthreads();
+            for (int e = threadIdx.x; e < 16 * (D / 4); e += 256) {
+                const int r = e / (D / 4), d = 4 * (e % (D / 4)), rr = 16 * n + r;
+                if (rr >= active) continue;
+                float hi = -__builtin_inff(), l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int v = 0; v < 4; ++v) hi = fmaxf(hi, stat[v][0][rr]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    l += stat[v][1][rr] * (hi == -__builtin_inff() ? 1.f : fast_exp2(stat[v][0][rr] - hi));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] += merge[v][r][d + i];
+                }
+                if (whole_row) {
+                    write_row<T>(a, s, h, G, r0 + rr, d, D, y, hi, l);
+                } else {
+                    *reinterpret_cast<float4 *>(piece + rr * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+                    if (d == 0) {
+                        piece[ROWS * D + rr] = hi;
+                        piece[ROWS * D + ROWS + rr] = l;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) reinterpret_cast<Record *>(a.ws)[blockIdx.x] = mine;
+}
+
+// Joins the pieces of cut rows: blocks (first piece's workgroup, query row).
+template <int D, int ROWS, bool BF>
+__global__ void __launch_bounds__(256) kda_cache_attend_join_kernel(AttendArgs a)
+{
+    constexpr int L = D / 4, GROUPS = 256 / L;
+    typedef typename Store<BF>::type T;
+    __shared__ float part[4];
+    __shared__ float weight[SHARES];
+    __shared__ __align__(16) float acc[256][4];
+    const int first = blockIdx.x, rr = blockIdx.y, tid = threadIdx.x;
+    const Record rec = reinterpret_cast<const Record *>(a.ws)[first];
+    if (rec.last < 0) return;
+    const Sequence s = sequence(a, rec.b);
+    const int G = a.Hq / a.Hk, r0 = rec.block * ROWS;
+    if (r0 + rr >= s.queries * G) return;
+    const float *pieces = a.ws + (sizeof(Record) / 4) * gridDim.x;
+    const int n = rec.last - first + 1;
+    const auto piece = [&](int i) { return pieces + (int64_t)(2 * (first + i) + (i == 0)) * PIECE<D, ROWS>; };
+    float best = -__builtin_inff();
+    for (int i = tid; i < n; i += 256) best = fmaxf(best, piece(i)[ROWS * D + rr]);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) best = fmaxf(best, __shfl_xor(best, m, 64));
+    if ((tid & 63) == 0) part[tid / 64] = best;
+    __syncthreads();
+    best = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    __syncthreads();
+    const bool none = best == -__builtin_inff();
+    float l = 0.f;
+    for (int i = tid; i < n; i += 256) {
+        const float w = none ? 1.f : fast_exp2(piece(i)[ROWS * D + rr] - best);
+        weight[i] = w;
+        l += w * piece(i)[ROWS * D + ROWS + rr];
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) l += __shfl_xor(l, m, 64);
+    if ((tid & 63) == 0) part[tid / 64] = l;
+    __syncthreads();
+    l = part[0] + part[1] + part[2] + part[3];
+    const int d = 4 * (tid % L), g = tid / L;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = g; i < n; i += GROUPS) {
+        const float4 x = *reinterpret_cast<const float4 *>(piece(i) + rr * D + d);
+        const float w = weight[i];
+        y[0] += w * x.x; y[1] += w * x.y; y[2] += w * x.z; y[3] += w * x.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[tid][i] = y[i];
+    __syncthreads();
+    if (g == 0) {
+        for (int k = 1; k < GROUPS; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] += acc[k * L + tid][i];
+        write_row<T>(a, s, rec.h, G, r0 + rr, d, D, y, best, l);
+    }
+}
+
+// Query blocks of 16 NR rows: 16 or, up to 128 channels, 32; with more, the
+// queries, the outputs and a tile's keys and values do not fit the registers,
+// and the kernel whose waves share them through LDS takes over.  Not for
+// float32 rows of 256 channels, which do not fit there either.
+int block_rows(int64_t rows) { return rows <= 16 ? 1 : 2; }
+bool is_few(int D, bool bf16, int64_t rows) { return D < 256 ? rows <= 32 : rows <= 16 || !bf16; }
+
+template <int D, int NR, bool BF, bool INT8> hipError_t launch(const AttendArgs &a, int n, hipStream_t stream)
+{
+    hipLaunchKernelGGL((kda_cache_attend_kernel<D, NR, BF, INT8>), dim3(n), dim3(256), 0, stream, a, __builtin_ctz(a.page));
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_attend_join<16 * NR>(a, n, a.most * (a.Hq / a.Hk), stream);
+}
+int64_t units_of(int B, int Hk, int64_t tiles, int D, int64_t rows)
+{
+    const int64_t block = 16 * (D == 256 ? 1 : block_rows(rows));
+    return (int64_t)B * Hk * (tiles > 0 ? tiles : 1) * ((rows + block - 1) / block);
+}
+template <int D, bool BF, bool INT8> hipError_t launch_rows(const AttendArgs &a, hipStream_t s)
+{
+    const int64_t rows = (int64_t)a.most * (a.Hq / a.Hk), tiles = ((int64_t)a.per * a.page + 63) / 64;
+    const int n = shares(units_of(a.B, a.Hk, tiles, D, rows));
+    if constexpr (D <= 128)
+        if (block_rows(rows) == 2) return launch<D, 2, BF, INT8>(a, n, s);
+    return launch<D, 1, BF, INT8>(a, n, s);
+}
+template <bool BF, bool INT8> hipError_t launch_d(const AttendArgs &a, hipStream_t s)
+{
+    return a.D == 64 ? launch_rows<64, BF, INT8>(a, s) : a.D == 128 ? launch_rows<128, BF, INT8>(a, s)
+                                                                    : launch_rows<256, BF, INT8>(a, s);
+}
+template <int D, int ROWS> hipError_t join(const AttendArgs &a, int n, int rows, hipStream_t stream)
+{
+    const dim3 grid((unsigned)n, (unsigned)(rows < ROWS ? rows : ROWS));
+    if (a.bf16) hipLaunchKernelGGL((kda_cache_attend_join_kernel<D, ROWS, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((kda_cache_attend_join_kernel<D, ROWS, false>), grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+template <int ROWS> hipError_t launch_attend_join(const AttendArgs &a, int n, int rows, hipStream_t stream)
+{
+    // `rows` is what the caller says that a sequence has: where the device knows of more, every row of a block may be in use
+    if (a.q_start) rows = ROWS;
+    return a.D == 64 ? join<64, ROWS>(a, n, rows, stream) : a.D == 128 ? join<128, ROWS>(a, n, rows, stream)
+                                                                       : join<256, ROWS>(a, n, rows, stream);
+}
+template hipError_t launch_attend_join<64>(const AttendArgs &, int, int, hipStream_t);
+template hipError_t launch_attend_join<128>(const AttendArgs &, int, int, hipStream_t);
+
+int64_t cache_attend_workspace_floats(int tokens, int B, int Hq, int Hk, int D, int page, int per, int most)
+{
+    const int64_t rows = (int64_t)most * (Hq / Hk), tiles = ((int64_t)per * page + 63) / 64;
+    int64_t need = 0;
+    for (const bool bf16 : {false, true}) {          // the size does not depend on the type
+        int64_t x;
+        if (is_few(D, bf16, rows))
+            x = shares(units_of(B, Hk, tiles, D, rows)) *
+                (int64_t)(sizeof(Record) / 4 + 2 * 16 * (D == 256 ? 1 : block_rows(rows)) * (D + 2));
+        else
+            x = attend_rows_workspace_floats(tokens, B, Hq, Hk, D, page, per, most);
+        need = x > need ? x : need;
+    }
+    return need;
+}
+
+hipError_t launch_cache_attend(const AttendArgs &a, hipStream_t s)
+{
+    if (!is_few(a.D, a.bf16, (int64_t)a.most * (a.Hq / a.Hk))) return launch_attend_rows(a, s);
+    if (a.bf16) return a.int8 ? launch_d<true, true>(a, s) : launch_d<true, false>(a, s);
+    return a.int8 ? launch_d<false, true>(a, s) : launch_d<false, false>(a, s);
+}
+
+}  // namespace kda

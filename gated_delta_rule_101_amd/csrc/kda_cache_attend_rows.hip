@@ -1,0 +1,379 @@
+// Attention over the 8-bit paged cache for gfx950, for many query rows a
+// sequence: prompts, and drafts of grouped heads.  The formulas and float16
+// forms are those of kda_cache_attend.hip.
+//
+// A workgroup has 32 rows (query, head of the group) a wave, of one sequence and
+// key head, and walks the tokens 64 at a time.  Bound by the matrix cores and,
+// as much, by the softmax between its two products, so codes are turned into
+// float16 once a workgroup: the next tile's bytes are requested before this
+// tile's products and go to the other half of LDS, as float16, behind them.
+//
+// 32x32x16 products of the transposed score tile: a lane holds scores of one row
+// (its column) and, by the order in which LDS holds the keys, 8 neighbouring
+// tokens of each 16, which are the second product's inner index as they stand.
+// Values are innermost in tokens in their pages, so that product's other operand
+// is 16 bytes of a channel's row.  LDS rows are padded by 16 bytes: lanes read
+// down the rows.
+//
+// Where blocks of rows are many, each is a workgroup, the last ones (the
+// longest) first, heads innermost so that workgroups of one head share an L2.
+// Where they are few, the line of units is cut into shares as for single
+// queries.
+#include "kda_attn.h"
+#include "kda_block.h"
+#include "kda_attend_device.h"
+
+namespace kda {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int D> struct Tile {
+    static constexpr int KSTRIDE = 2 * D + 16, VSTRIDE = 2 * 64 + 16;      // bytes
+    uint8_t k[64 * KSTRIDE], v[D * VSTRIDE];
+    float ks[4], vs[4];                      // scales of the four 16-token groups
+    int there[4];                            // the group has a page
+};
+
+__device__ __forceinline__ float halves_max(float x)
+{
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+__device__ __forceinline__ float halves_sum(float x)
+{
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+// The LDS row of a tile's token: the score product's row whose result a lane
+// half h holds as the (4 b + c)th value is 8 b + 4 h + c, and is to be token
+// 16 (b / 2) + 8 h + 4 (b & 1) + c.
+__device__ __forceinline__ int key_row(int t) { return (t & 0x33) | (t & 8) >> 1 | (t & 4) << 1; }
+
+// A tile's bytes on their way from memory to LDS: each thread 16-byte parts.
+template <int D, int WAVES, bool INT8> struct Loader {
+    static constexpr int THREADS = 64 * WAVES, PARTS = 4 * D / THREADS;    // of keys, and of values
+    uint4 k[PARTS], v[PARTS];
+    float ks, vs;
+    int there;
+    // thread's part i of the keys: token, 16 channels from c; of the values: channel, group of 16 tokens
+    static __device__ __forceinline__ int key_token(int i) { return (threadIdx.x + i * THREADS) / (D / 16); }
+    static __device__ __forceinline__ int key_part(int i) { return (threadIdx.x + i * THREADS) % (D / 16); }
+    static __device__ __forceinline__ int channel(int i) { return (threadIdx.x + i * THREADS) / 4; }
+    __device__ __forceinline__ void load(const AttendArgs &a, const int *table, int h, int t0, int context, int shift)
+    {
+        const int in = a.page - 1;
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+            const int t = t0 + key_token(i);
+            const int id = max(page_of(a, table, t & ~15, context, shift), 0);
+            k[i] = *reinterpret_cast<const uint4 *>(a.k_codes + (((int64_t)id * a.Hk + h) * a.page + (t & in)) * D + 16 * key_part(i));
+        }
+        const int t = t0 + 16 * (threadIdx.x & 3), id = page_of(a, table, t, context, shift);
+        const int64_t at = (int64_t)max(id, 0) * a.Hk + h;
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i)
+            v[i] = *reinterpret_cast<const uint4 *>(a.v_codes + (at * D + channel(i)) * a.page + (t & in));
+        if (!INT8 && t0 + 64 > context) {
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) v[i] = keep_bytes(v[i], context - t);   // no NaN where the weight is zero
+        }
+        if (!INT8 && id < 0) {
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        }
+        there = id >= 0;
+        ks = there ? a.k_scale[at] : 0.f;
+        vs = there ? a.v_scale[at] : 0.f;
+    }
+    __device__ __forceinline__ void put(Tile<D> &tile) const
+    {
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+            uint8_t *to = tile.k + key_row(key_token(i)) * Tile<D>::KSTRIDE + 32 * key_part(i);
+            *reinterpret_cast<f16x8 *>(to) = codes_f16<INT8>(k[i].x, k[i].y);
+            *reinterpret_cast<f16x8 *>(to + 16) = codes_f16<INT8>(k[i].z, k[i].w);
+        }
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+            uint8_t *to = tile.v + channel(i) * Tile<D>::VSTRIDE + 32 * (threadIdx.x & 3);
+            *reinterpret_cast<f16x8 *>(to) = codes_f16<INT8>(v[i].x, v[i].y);
+            *reinterpret_cast<f16x8 *>(to + 16) = codes_f16<INT8>(v[i].z, v[i].w);
+        }
+        if (threadIdx.x < 4) {
+            tile.ks[threadIdx.x] = ks;
+            tile.vs[threadIdx.x] = vs;
+            tile.there[threadIdx.x] = there;
+        }
+    }
+};
+
+// LINE: shares of the line of units; otherwise a workgroup a block of rows.
+template <int D, int WAVES, bool BF, bool INT8, bool LINE>
+__global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 ? 1 : 2) kda_cache_attend_rows_kernel(AttendArgs a, int shift)
+{
+    constexpr int SPLIT = BF ? 1 : 2, KS = D / 16, DT = D / 32, ROWS = 32 * WAVES;
+    typedef typename Store<BF>::type T;
+    extern __shared__ __align__(16) uint8_t lds[];
+    Tile<D> *const tiles_lds = reinterpret_cast<Tile<D> *>(lds);
+    __shared__ int64_t part[WAVES];
+    const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x & 63, m = lane & 31, half = lane >> 5;
+    const int G = a.Hq / a.Hk;
+    Line line;
+    int b, h, block, t_begin = 0, t_end;
+    if constexpr (LINE) {
+        line = cut_line<WAVES>(a, G, ROWS, 1, part);
+    } else {
+        // the block's place among all sequences' blocks, sequence b's being counted from q_start[b] G / ROWS + b
+        const int64_t blocks = gridDim.x / a.Hk, at = blocks - 1 - blockIdx.x / a.Hk;
+        h = blockIdx.x % a.Hk;
+        int n = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 64) {
+            const bool upto = b0 + lane < a.B && (int64_t)sequence(a, min(b0 + lane, a.B - 1)).first * G / ROWS + b0 + lane <= at;
+            const uint64_t past = ~__ballot(upto);
+            n = b0 + (past ? __builtin_ctzll(past) : 64);
+            if (past) break;
+        }
+        if (n == 0) return;                              // rows in front of the first sequence
+        b = uniform(min(n, a.B) - 1);
+        const Sequence s = sequence(a, b);
+        block = (int)(at - ((int64_t)s.first * G / ROWS + b));
+        if (block >= blocks_of(s, G, ROWS)) return;
+    }
+    Record mine = {0, 0, 0, -1};
+    while (!LINE || line.left > 0) {
+        Sequence s;
+        int tiles;
+        if constexpr (LINE) {
+            s = sequence(a, line.b);
+            tiles = tiles_of(s);
+            const int blocks = blocks_of(s, G, ROWS);
+            if (line.u >= (int64_t)tiles * blocks * a.Hk) {
+                line.u = 0;
+                ++line.b;
+                continue;
+            }
+            b = line.b;
+            const int row = (int)(line.u / tiles);
+            t_begin = (int)(line.u - (int64_t)row * tiles);
+            t_end = (int)min((int64_t)tiles, t_begin + line.left);
+            h = row / blocks;
+            block = row - h * blocks;
+        } else {
+            s = sequence(a, b);
+            tiles = t_end = tiles_of(s);
+        }
+        const int r0 = block * ROWS, active = min(ROWS, s.queries * G - r0);
+        const int furthest = min(s.context, s.context - s.queries + (r0 + active - 1) / G + 1);
+        const int t_stop = min(t_end, (furthest + 63) / 64);       // tiles behind it are seen by no row
+
+        // this wave's rows
+        const int w0 = 32 * wave, r = w0 + m, qi = (r0 + min(r, active - 1)) / G, qg = (r0 + min(r, active - 1)) - qi * G;
+        const int limit = r < active ? min(s.context - s.queries + qi + 1, s.context) : 0x7fffffff;
+        const int whole = min(s.context - s.queries + (r0 + min(w0, active - 1)) / G + 1, s.context);
+        f16x8 q[SPLIT][KS];
+        const float factor = load_row<T, D, SPLIT>((const T *)a.q + ((int64_t)(s.first + qi) * a.Hq + h * G + qg) * D,
+                                                   r < active, half, a.scale < 0.f, q) * fabsf(a.scale) * LOG2E;
+        f32x16 o[DT];
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+        float top = -__builtin_inff(), sum = 0.f, reference = 0.f;
+
+        const int *table = a.table + (int64_t)b * a.per;
+        Loader<D, WAVES, INT8> next;
+        if (t_begin < t_stop) {
+            next.load(a, table, h, t_begin * 64, s.context, shift);
+            next.put(tiles_lds[0]);
+        }
+        __syncthreads();
+        for (int t = t_begin; t < t_stop; ++t) {
+            const Tile<D> &tile = tiles_lds[(t - t_begin) & 1];
+            const int t0 = t * 64;
+            if (t + 1 < t_stop) next.load(a, table, h, t0 + 64, s.context, shift);
+
+            f32x16 x[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[j][i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const f16x8 c = *reinterpret_cast<const f16x8 *>(tile.k + (32 * j + m) * Tile<D>::KSTRIDE + 32 * k + 16 * half);
+#pragma unroll
+                    for (int p = 0; p < SPLIT; ++p) x[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, q[p][k], x[j], 0, 0, 0);
+                }
+            }
+            // value scales: a new reference is rare after the first tiles
+            float vs[4], ks[4], most = 0.f;
+            int there = 0, broken = 0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                broken |= (is_finite(tile.vs[g]) ? 0 : 1) << g;
+                vs[g] = is_finite(tile.vs[g]) ? tile.vs[g] : 0.f;
+                ks[g] = tile.ks[g];
+                there |= tile.there[g] << g;
+                most = fmaxf(most, vs[g]);
+            }
+            if (__any(most > reference)) {
+                const float now = 2.f * most, f = reference / now;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[d][i] *= f;
+                reference = now;
+            }
+            const float inv = reference > 0.f ? fast_rcp(reference) : 0.f;
+            const bool masked = t0 + 64 > whole || there != 15;
+            float best = -__builtin_inff();
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float c = factor * ks[g];
+                const int seen = there >> g & 1 ? limit - (t0 + 16 * g + 8 * half) : 0;    // of the lane's 8 tokens
+                float y = -__builtin_inff();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float v = x[g >> 1][8 * (g & 1) + i] * c;
+                    if (masked) v = i < seen ? v : -__builtin_inff();
+                    x[g >> 1][8 * (g & 1) + i] = v;
+                    y = fmaxf(y, v);
+                }
+                best = fmaxf(best, y);
+            }
+            best = halves_max(best);
+            const float now = fmaxf(top, best), base = now == -__builtin_inff() ? 0.f : now;
+            const float fade = fast_exp2(top - base);
+            top = now;
+            if (__any(fade != 1.f)) {
+                sum *= fade;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[d][i] *= fade;
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float ratio = reference > 0.f ? vs[g] * inv : 1.f;
+                ratio = VALUE_GAIN * fmaxf(ratio, 0x1p-40f);
+                const float offset = fast_log2(ratio) - base;
+                float v[8], total = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = fast_exp2(x[g >> 1][8 * (g & 1) + i] + offset);
+                    total += v[i];
+                }
+                sum += total * fast_rcp(ratio);
+                if (broken >> g & 1) {
+                    const int seen = limit - (t0 + 16 * g + 8 * half);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = i < seen ? __builtin_nanf("") : v[i];
+                }
+                f16x8 w[SPLIT];
+                split_f16<SPLIT>(v, [&](int p) -> f16x8 & { return w[p]; });
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const f16x8 c = *reinterpret_cast<const f16x8 *>(tile.v + (32 * d + m) * Tile<D>::VSTRIDE + 32 * g + 16 * half);
+#pragma unroll
+                    for (int p = 0; p < SPLIT; ++p) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, w[p], o[d], 0, 0, 0);
+                }
+            }
+            if (t + 1 < t_stop) next.put(tiles_lds[(t + 1 - t_begin) & 1]);
+            __syncthreads();
+        }
+
+        sum = halves_sum(sum);
+        const bool whole_row = t_begin == 0 && t_end == tiles;
+        const float f = reference * VALUE_REST;
+        float *piece = nullptr;
+        if constexpr (LINE) {
+            piece = a.ws + (sizeof(Record) / 4) * gridDim.x + (int64_t)(2 * blockIdx.x + (t_begin == 0)) * PIECE<D, ROWS>;
+            if (t_begin == 0 && !whole_row) mine = {b, h, block, (int)((line.at + tiles - 1) / line.share)};
+            line.u += t_end - t_begin;
+            line.left -= t_end - t_begin;
+            line.at += t_end - t_begin;
+        }
+        if (r < active) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 32 * d + 8 * i + 4 * half;
+                    const float y[4] = {o[d][4 * i] * f, o[d][4 * i + 1] * f, o[d][4 * i + 2] * f, o[d][4 * i + 3] * f};
+                    if (!LINE || whole_row) write_row<T>(a, s, h, G, r0 + r, at, D, y, top, sum);
+                    else *reinterpret_cast<float4 *>(piece + (int64_t)r * D + at) = make_float4(y[0], y[1], y[2], y[3]);
+                }
+            if (LINE && !whole_row && half == 0) {
+                piece[ROWS * D + r] = top;
+                piece[ROWS * D + ROWS + r] = sum;
+            }
+        }
+        if constexpr (!LINE) return;
+        __syncthreads();
+    }
+    if (LINE && threadIdx.x == 0) reinterpret_cast<Record *>(a.ws)[blockIdx.x] = mine;
+}
+
+// How a call is run: waves a workgroup, and whether its line is cut.
+struct Shape {
+    int waves, workgroups;
+    bool line;
+};
+Shape shape_of(int tokens, int B, int Hq, int Hk, int D, int page, int per, int most)
+{
+    Shape s;
+    const int64_t rows = (int64_t)most * (Hq / Hk), tiles = ((int64_t)per * page + 63) / 64;
+    s.waves = rows <= 64 && D <= 128 ? 2 : 4;
+    // blocks of all sequences, at most (as the kernel counts them)
+    const int64_t blocks = ((int64_t)tokens * (Hq / Hk) / (32 * s.waves) + B) * Hk;
+    s.line = blocks < 1024;
+    s.workgroups = s.line ? shares(blocks * (tiles > 0 ? tiles : 1)) : blocks < ((int64_t)1 << 24) ? (int)blocks : 0;
+    return s;
+}
+
+template <int D, int WAVES, bool BF, bool INT8> hipError_t launch(const AttendArgs &a, const Shape &s, hipStream_t stream)
+{
+    const int shift = __builtin_ctz(a.page);
+    const size_t bytes = 2 * sizeof(Tile<D>);
+    const dim3 grid((unsigned)s.workgroups), threads(64 * WAVES);
+    const auto set = [&](const void *k) { return hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); };
+    if (!s.line) {
+        const auto k = kda_cache_attend_rows_kernel<D, WAVES, BF, INT8, false>;
+        const hipError_t e = set(reinterpret_cast<const void *>(k));
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(k, grid, threads, bytes, stream, a, shift);
+        return hipGetLastError();
+    }
+    const auto k = kda_cache_attend_rows_kernel<D, WAVES, BF, INT8, true>;
+    hipError_t e = set(reinterpret_cast<const void *>(k));
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k, grid, threads, bytes, stream, a, shift);
+    e = hipGetLastError();
+    return e != hipSuccess ? e : launch_attend_join<32 * WAVES>(a, s.workgroups, 32 * WAVES, stream);
+}
+template <bool BF, bool INT8> hipError_t launch_d(const AttendArgs &a, const Shape &s, hipStream_t stream)
+{
+    if (a.D == 64) return s.waves == 2 ? launch<64, 2, BF, INT8>(a, s, stream) : launch<64, 4, BF, INT8>(a, s, stream);
+    if (a.D == 128) return s.waves == 2 ? launch<128, 2, BF, INT8>(a, s, stream) : launch<128, 4, BF, INT8>(a, s, stream);
+    if constexpr (BF) return launch<256, 4, BF, INT8>(a, s, stream);
+    return hipErrorNotSupported;             // those rows are the other kernel's
+}
+
+}  // namespace
+
+int64_t attend_rows_workspace_floats(int tokens, int B, int Hq, int Hk, int D, int page, int per, int most)
+{
+    const Shape s = shape_of(tokens, B, Hq, Hk, D, page, per, most);
+    return s.line ? (int64_t)s.workgroups * (int64_t)(sizeof(Record) / 4 + 2 * 32 * s.waves * (D + 2)) : 0;
+}
+
+hipError_t launch_attend_rows(const AttendArgs &a, hipStream_t stream)
+{
+    const Shape s = shape_of(a.tokens, a.B, a.Hq, a.Hk, a.D, a.page, a.per, a.most);
+    if (s.workgroups == 0) return hipErrorNotSupported;
+    if (a.bf16) return a.int8 ? launch_d<true, true>(a, s, stream) : launch_d<true, false>(a, s, stream);
+    return a.int8 ? launch_d<false, true>(a, s, stream) : launch_d<false, false>(a, s, stream);
+}
+
+}  // namespace kda

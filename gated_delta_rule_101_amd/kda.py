@@ -27,6 +27,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.environ.get("KDA_LIBRARY") or os.path.join(HERE, "libkda.so")
 
 KDA_F32, KDA_BF16 = 0, 1
+KDA_CODE_E4M3, KDA_CODE_INT8 = 0, 1
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_LAUNCH, KDA_ERR_SCRATCH = 0, 1, 2, 3, 4
 
 # Every symbol include/kda.h declares.
@@ -39,7 +40,9 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_gate", "kda_chunk_fwd_ws", "kda_chunk
            "kda_short_conv_fwd", "kda_short_conv_step", "kda_short_conv_bwd", "kda_short_conv_bwd_workspace_bytes",
            "kda_selective_scan_fwd", "kda_selective_scan_fwd_workspace_bytes", "kda_selective_scan_step",
            "kda_selective_scan_bwd", "kda_selective_scan_bwd_workspace_bytes",
-           "kda_layer_norm_fwd", "kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_bytes")
+           "kda_layer_norm_fwd", "kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_bytes",
+           "kda_cache_plan", "kda_qk_norm_rope_fwd", "kda_qk_norm_rope_bwd", "kda_qk_norm_rope_bwd_workspace_bytes",
+           "kda_cache_append", "kda_cache_attention", "kda_cache_attention_workspace_bytes")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -109,13 +112,20 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
             "kda_selective_scan_step": [vp] * 10 + [i] * 6 + [vp],
             "kda_selective_scan_bwd": [vp] * 22 + [sz] + [i] * 7 + [vp],
             "kda_layer_norm_fwd": [vp] * 3 + [f, vp, i64, i, i, vp],
-            "kda_layer_norm_bwd": [vp] * 3 + [f] + [vp] * 4 + [sz, i64, i, i, vp]}.items():
+            "kda_layer_norm_bwd": [vp] * 3 + [f] + [vp] * 4 + [sz, i64, i, i, vp],
+            "kda_cache_plan": [vp] * 10 + [i] * 5 + [vp],
+            "kda_qk_norm_rope_fwd": [vp] * 4 + [f] + [vp] * 4 + [i64] + [i] * 6 + [i64] * 4 + [i, vp],
+            "kda_qk_norm_rope_bwd": [vp] * 6 + [f] + [vp] * 7 + [sz, i64] + [i] * 6 + [i64] * 6 + [i, vp],
+            "kda_cache_append": [vp] * 7 + [i] * 5 + [i64] * 2 + [i, i, vp],
+            "kda_cache_attention": [vp] * 11 + [sz] + [i] * 9 + [f, i, i, vp]}.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = i
     for name, args in {"kda_short_conv_bwd_workspace_bytes": [i] * 4,
                        "kda_selective_scan_fwd_workspace_bytes": [i] * 5,
                        "kda_selective_scan_bwd_workspace_bytes": [i] * 5,
-                       "kda_layer_norm_bwd_workspace_bytes": [i64, i]}.items():
+                       "kda_layer_norm_bwd_workspace_bytes": [i64, i],
+                       "kda_qk_norm_rope_bwd_workspace_bytes": [i64, i, i, i],
+                       "kda_cache_attention_workspace_bytes": [i] * 8}.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = sz
     lib.kda_status_string.argtypes = [i]

@@ -85,6 +85,14 @@ typedef enum {
     KDA_DTYPE_RANGE_MAX_ = 2147483647
 } kda_dtype_t;
 
+/* The cache's 8-bit codes: a value is its code times the scale of its page and head. */
+typedef enum {
+    KDA_CODE_E4M3 = 0, /* 8-bit float: 4 exponent and 3 mantissa bits, largest 448, no infinities */
+    KDA_CODE_INT8 = 1, /* integer, -127 .. 127 */
+    KDA_CODE_RANGE_MIN_ = -2147483647 - 1,
+    KDA_CODE_RANGE_MAX_ = 2147483647
+} kda_code_t;
+
 typedef enum {
     KDA_OK = 0,
     KDA_ERR_INVALID_ARG = 1,  /* NULL / misaligned / overlapping pointer, negative size, bad dtype */
@@ -620,6 +628,162 @@ size_t kda_layer_norm_bwd_workspace_bytes(int64_t rows, int D);
 kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const float *weight, float eps, void *dx,
                                 float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
                                 int64_t rows, int D, kda_dtype_t dtype, void *stream);
+
+/*
+ * The softmax attention layers between recurrent ones: a serving step's plan,
+ * norm and rotation of queries and keys, a paged cache in 8 bits and the
+ * attention that reads it.  Common to these calls:
+ *
+ *  - The cache of one layer is
+ *      k_codes [pages, Hk, page, D]   one byte each
+ *      v_codes [pages, Hk, D, page]   one byte each, tokens innermost
+ *      k_scale, v_scale [pages, Hk]   float32
+ *    A value is its code (kda_code_t) times the scale of its page and head.
+ *    page (tokens a page) is 16, 32, 64 or 128, D is 64, 128 or 256
+ *    (KDA_ERR_UNSUPPORTED otherwise); pages * page below 2^31, the codes below
+ *    2^40 bytes.  A fresh cache needs no initialisation.
+ *  - Slot s of the cache is place s % page of page s / page.
+ *  - block_table [B, max_pages] int32 holds each sequence's pages in order;
+ *    entries behind its last page are not read.
+ *  - Numbers on the device (lengths, tables, slots, row starts) are not seen by
+ *    the host.  Whatever they hold, no call reads or writes outside its
+ *    buffers: what names no place of them is skipped, as stated.
+ *  - Token rows q, k, v hold heads of D channels, heads next to each other;
+ *    where strides are given (elements from one token to the next, at least a
+ *    row) they may be parts of a wider matrix, such as a fused projection, and
+ *    need only be aligned to their element.  int32 and scale buffers are
+ *    aligned to 4 bytes.
+ *  - dtype (KDA_F32 or KDA_BF16) is the type of the token rows.  Arithmetic and
+ *    sums are float32; each output is rounded once, when stored.
+ *  - Workspaces and overlaps as for the calls above.
+ */
+
+/*
+ * kda_cache_plan -- what a serving step needs to know of its requests, built on
+ * the device: request b has cached[b] tokens in the cache and brings added[b].
+ *
+ *   cached, added [B] int32
+ *   block_table   [B, max_pages] int32: entries of the cached tokens' pages are
+ *                 read, those of pages that the new tokens begin are written
+ *   free_pages    [free_capacity] int32, free_count [1] int32 (clamped to the
+ *                 capacity): a list of free pages, taken from its end, for request
+ *                 0 first
+ *   q_start       [B + 1] int32: each request's first row among the step's tokens
+ *   context       [B] int32: its tokens after the step
+ *   positions     [tokens] int32: each row's place in its sequence
+ *   slots         [tokens] int32: and in the cache
+ *   free_left     [1] int32: entries of free_pages that are still free (not free_count itself)
+ *
+ * Requests are served in order, while the free pages and the `tokens` rows last
+ * for them and all before them.  One that is not served (nor one with a negative
+ * length, or more pages than the table holds, which takes none) keeps its rows,
+ * but its context is 0, its rows' positions and slots are -1, and its table is
+ * left as it is.  Rows behind the last request have positions and slots -1;
+ * q_start does not pass `tokens`.  A cached token whose entry is negative has
+ * slot -1.  Pages' numbers times page have to stay below 2^31.
+ */
+kda_status_t kda_cache_plan(const int *cached, const int *added, int *block_table, const int *free_pages,
+                            const int *free_count, int *q_start, int *context, int *positions, int *slots,
+                            int *free_left, int B, int max_pages, int free_capacity, int tokens, int page, void *stream);
+
+/*
+ * kda_qk_norm_rope_fwd -- norm of each query and key head and rotation by the
+ * token's position, in one pass:
+ *
+ *   n = x / sqrt(mean_d x^2 + eps) * weight
+ *   y = n with the pairs of its first rotary_dim channels turned by the angles
+ *       of the token's row of `rotary`: (a, b) -> (a cos - b sin, a sin + b cos)
+ *
+ *   q, q_out [tokens, Hq, D] dtype, k, k_out [tokens, Hk, D] dtype, with strides;
+ *            an output may be its own input
+ *   q_weight, k_weight [D] float32, each or both NULL (ones)
+ *   eps      >= 0, finite.  With eps = 0 a row of zeros is NaN
+ *   rotary   [rotary_rows, rotary_dim] float32, rotary_dim / 2 cosines and then as
+ *            many sines a row; NULL with rotary_dim = 0: no rotation
+ *   positions [tokens] int32, the rows of `rotary` to use (NULL without rotary).  A
+ *            negative one marks a row of no token: its input is not read, its
+ *            output is zero.  One of rotary_rows or more makes its outputs NaN
+ *   neighbours  0: the pairs are (i, i + rotary_dim / 2); otherwise (2 i, 2 i + 1)
+ *
+ * D even, up to 512, rotary_dim even, up to D.  A head's sum of squares has to
+ * stay below float32's 3.4e38.
+ */
+kda_status_t kda_qk_norm_rope_fwd(const void *q, const void *k, const float *q_weight, const float *k_weight, float eps,
+                                  const int *positions, const float *rotary, void *q_out, void *k_out,
+                                  int64_t tokens, int Hq, int Hk, int D, int rotary_dim, int rotary_rows, int neighbours,
+                                  int64_t q_stride, int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                                  kda_dtype_t dtype, void *stream);
+
+/*
+ * kda_qk_norm_rope_bwd -- its gradients: dq [tokens, Hq, D] and dk [tokens, Hk, D]
+ * (dtype; each may be its upstream gradient dq_out or dk_out), dq_weight and
+ * dk_weight [D] float32, summed over tokens and heads, each or both NULL where
+ * not wanted (a workspace is needed for them only).  q and k are the forward's
+ * inputs.  Rows of a negative position have zero gradients and add nothing;
+ * rows of one beyond the table make theirs, and the weights', NaN.
+ */
+size_t kda_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int Hq, int Hk, int D);
+
+kda_status_t kda_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                                  const float *q_weight, const float *k_weight, float eps,
+                                  const int *positions, const float *rotary, void *dq, void *dk,
+                                  float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes,
+                                  int64_t tokens, int Hq, int Hk, int D, int rotary_dim, int rotary_rows, int neighbours,
+                                  int64_t dq_out_stride, int64_t dk_out_stride, int64_t q_stride, int64_t k_stride,
+                                  int64_t dq_stride, int64_t dk_stride, kda_dtype_t dtype, void *stream);
+
+/*
+ * kda_cache_append -- new keys and values into the cache, IN PLACE.
+ *
+ *   k, v   [tokens, Hk, D] dtype, with strides
+ *   slots  [tokens] int32; tokens whose slot is outside the cache are skipped
+ *
+ * For each page and head that tokens go to, with Q the largest code (448 or 127):
+ *   scale' = max(scale, largest |new| * (1 / Q)), or the second alone where the
+ *            first place written is the page's first (it starts anew, whatever
+ *            it and its scale held)
+ *   code   = new / scale' to the nearest code, ties to even
+ *   codes in front of the first place written: code * (scale / scale') to the
+ *            nearest code, where the scale grew; all other places are left as they are
+ * in float32.  Infinities and NaN leave the scale not finite: such a page and
+ * head reads as NaN until it starts anew.
+ *
+ * The tokens of a call that go to one page follow each other in it, as those of
+ * one sequence do; of two with the same slot the later one counts.  A page that
+ * two sequences share is not written by either.
+ */
+kda_status_t kda_cache_append(const void *k, const void *v, const int *slots, void *k_codes, void *v_codes,
+                              float *k_scale, float *v_scale, int tokens, int Hk, int D, int pages, int page,
+                              int64_t k_stride, int64_t v_stride, kda_code_t code, kda_dtype_t dtype, void *stream);
+
+/*
+ * kda_cache_attention -- causal attention over the cache: each query head reads
+ * key and value head (its number) / (Hq / Hk).
+ *
+ *   o = sum_t softmax_t(scale q . K[t]) V[t],  lse = log sum_t exp(scale q . K[t])
+ *
+ *   q, out  [tokens, Hq, D] dtype, contiguous, all sequences' rows together
+ *   q_start [B + 1] int32: sequence b has rows q_start[b] to q_start[b + 1] - 1, not
+ *           descending, clamped to [0, tokens]; NULL: one row each (tokens = B)
+ *   context [B] int32: its tokens in the cache, those of the rows among them
+ *           (clamped to the table).  Row i of n stands at place context - n + i
+ *           and sees the places up to its own
+ *   lse     [tokens, Hq] float32, or NULL
+ *   max_queries  rows of the longest sequence, as far as the host knows: chooses
+ *           the kernel, and the results are right for any value
+ *
+ * Pages whose table entry names none of the cache (such as -1, for a page that
+ * was given up) are not seen.  A row that sees no place has out 0 and lse -inf.
+ * Rows of no sequence are left as they were.  tokens * Hq below 2^31.
+ */
+size_t kda_cache_attention_workspace_bytes(int tokens, int B, int Hq, int Hk, int D, int page, int max_pages,
+                                           int max_queries);
+
+kda_status_t kda_cache_attention(const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
+                                 const float *v_scale, const int *block_table, const int *context, const int *q_start,
+                                 void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                 int tokens, int B, int Hq, int Hk, int D, int pages, int page, int max_pages,
+                                 int max_queries, float scale, kda_code_t code, kda_dtype_t dtype, void *stream);
 
 /* Static, human-readable name of a status code (never NULL). */
 const char *kda_status_string(kda_status_t status);   /* codes outside the set: "KDA_ERR_UNKNOWN" */
