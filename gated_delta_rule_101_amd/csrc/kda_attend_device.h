@@ -144,31 +144,21 @@ __device__ __forceinline__ float load_row(const T *p, bool real, int half, bool 
     return __builtin_ldexpf(1.f, -e);
 }
 
-// The page's value scale as a fraction of the wave's reference, which is twice
-// the largest scale met and moves (with the outputs, which are in its units)
-// when a larger one comes.  Not below 2^-40: what such a page adds is lost in
-// rounding anyway, and its weights still count in the sum.  Times 2^14, which
-// leaves float16 normal weights down to 2^-28.  Scales that are not finite pass
-// as 0 here: the weights of their tokens are made NaN behind the sum.
-constexpr float VALUE_GAIN = 0x1p14f, VALUE_REST = 0x1p-14f;
-__device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
-template <int NR, int DT>
-__device__ __forceinline__ float value_ratio(float scale, float &reference, f32x4 (&o)[NR][DT])
+// Value scales go into the weights' exponents: log2 of the page's scale over the
+// wave's reference, the power of two above twice the largest scale met, which
+// moves (with the outputs, which are in its units) when a larger one comes.  Not
+// below 2^-40: what such a page adds is lost in rounding anyway, and its weights
+// still count in the sum.  Times 2^14, which leaves float16 normal weights down to
+// 2^-28.  Scales that are not finite pass as 0 here: the weights of their tokens
+// are made NaN behind the sum.
+// SLACK: how far scores may be above the base of their exponents.  Weights then
+// reach 2^14 / 2 * 2^SLACK, below float16's 65504.
+constexpr float VALUE_REST = 0x1p-14f, SLACK = 2.f;
+__device__ __forceinline__ float ratio_level(float lv, float level)
 {
-    const float most = quarters_max(scale);
-    if (__any(most > reference)) {
-        const float next = 2.f * most, f = reference / next;
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][d][i] *= f;
-        reference = next;
-    }
-    const float r = reference > 0.f ? scale / reference : 1.f;
-    return VALUE_GAIN * fmaxf(r, 0x1p-40f);
+    return fmaxf(level == -__builtin_inff() ? 0.f : lv - level, -40.f) + 14.f;
 }
+__device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // 16 bytes with those from place n on cleared.
 __device__ __forceinline__ uint4 keep_bytes(uint4 x, int n)

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
         const int furthest = min(s.context, s.context - s.queries + (r0 + active - 1) / G + 1);
 
         f32x4 o[NR][DT];
-        float top[NR], sum[NR], reference = 0.f;
+        float top[NR], sum[NR], level = -__builtin_inff();
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             top[n] = -__builtin_inff();
@@ -118,8 +118,18 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
             const int tb = t0 + 16 * quarter;                  // this lane's first token
             const bool masked = t0 + 64 > whole || __any(pv < 0);
             const bool broken = pv >= 0 && !is_finite(vs);
-            const float ratio = value_ratio<NR, DT>(pv < 0 || broken ? 0.f : vs, reference, o);
-            const float shift_v = fast_log2(ratio);
+            const float lv = pv < 0 || broken ? -__builtin_inff() : fast_log2(vs);
+            if (__any(lv > level)) {         // rare after the first tiles
+                const float now = __builtin_ceilf(quarters_max(lv)) + 1.f, f = fast_exp2(level - now);
+                level = now;
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[n][d][i] *= f;
+            }
+            const float up = ratio_level(lv, level), down = fast_exp2(-up);
             f16x8 w[SPLIT][NR][2];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
@@ -145,23 +155,23 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
 #pragma unroll
                 for (int i = 0; i < 16; ++i) best = fmaxf(best, v[i]);
                 best = quarters_max(best);
-                const float now = fmaxf(top[n], best), base = now == -__builtin_inff() ? 0.f : now;
-                const float fade = fast_exp2(top[n] - base);
-                top[n] = now;
-                if (__any(fade != 1.f)) {
+                if (__any(best > top[n] + SLACK)) {
+                    const float now = fmaxf(top[n], best), fade = now == -__builtin_inff() ? 1.f : fast_exp2(top[n] - now);
+                    top[n] = now;
                     sum[n] *= fade;
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) o[n][d][i] *= fade;
                 }
+                const float offset = up - (top[n] == -__builtin_inff() ? 0.f : top[n]);
                 float total = 0.f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    v[i] = fast_exp2(v[i] - (base - shift_v));
+                    v[i] = fast_exp2(v[i] + offset);
                     total += v[i];
                 }
-                sum[n] += total * fast_rcp(ratio);
+                sum[n] = __builtin_fmaf(total, down, sum[n]);
                 if (__any(broken)) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = broken && i < seen ? __builtin_nanf("") : v[i];
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
         }
 
         // The four waves' parts meet: scaled to the common maximum and reference.
-        if (lane == 0) ref[wave] = reference;
+        if (lane == 0) ref[wave] = level == -__builtin_inff() ? 0.f : fast_exp2(level) * VALUE_REST;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             sum[n] = quarters_sum(sum[n]);
@@ -212,7 +222,7 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
 #pragma unroll
             for (int v = 0; v < 4; ++v) best = fmaxf(best, stat[v][0][16 * n + m]);
             // in units of the values: times the reference, which is 0 where every value was
-            const float f = (best == -__builtin_inff() ? 1.f : fast_exp2(top[n] - best)) * (ref[wave] * VALUE_REST);
+            const float f = (best == -__builtin_inff() ? 1.f : fast_exp2(top[n] - best)) * ref[wave];
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll

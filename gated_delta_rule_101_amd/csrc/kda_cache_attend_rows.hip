@@ -31,8 +31,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 template <int D> struct Tile {
     static constexpr int KSTRIDE = 2 * D + 16, VSTRIDE = 2 * 64 + 16;      // bytes
     uint8_t k[64 * KSTRIDE], v[D * VSTRIDE];
-    float ks[4], vs[4];                      // scales of the four 16-token groups
-    int there[4];                            // the group has a page
 };
 
 __device__ __forceinline__ float halves_max(float x)
@@ -51,41 +49,68 @@ __device__ __forceinline__ float halves_sum(float x)
 // 16 (b / 2) + 8 h + 4 (b & 1) + c.
 __device__ __forceinline__ int key_row(int t) { return (t & 0x33) | (t & 8) >> 1 | (t & 4) << 1; }
 
-// A tile's bytes on their way from memory to LDS: each thread 16-byte parts.
+// A tile's bytes on their way from memory to LDS: each thread 16-byte parts.  A
+// wave's keys of one part are of one 16-token group, so their page is a scalar;
+// values' groups, the scales and the pages' numbers go by lane & 3.  Pages are
+// looked up a tile ahead of the codes.
 template <int D, int WAVES, bool INT8> struct Loader {
     static constexpr int THREADS = 64 * WAVES, PARTS = 4 * D / THREADS;    // of keys, and of values
     uint4 k[PARTS], v[PARTS];
-    float ks, vs;
-    int there;
+    float ks, lv;                            // key scale, log2 of the value scale
+    int there, broken;                       // by group: has a page, its value scale is not finite
+    int page, ahead;                         // of the tile whose codes are next to be requested, of the one behind
     // thread's part i of the keys: token, 16 channels from c; of the values: channel, group of 16 tokens
     static __device__ __forceinline__ int key_token(int i) { return (threadIdx.x + i * THREADS) / (D / 16); }
     static __device__ __forceinline__ int key_part(int i) { return (threadIdx.x + i * THREADS) % (D / 16); }
+    static __device__ __forceinline__ int key_group(int i) { return uniform(key_token(i) / 16); }
     static __device__ __forceinline__ int channel(int i) { return (threadIdx.x + i * THREADS) / 4; }
-    __device__ __forceinline__ void load(const AttendArgs &a, const int *table, int h, int t0, int context, int shift)
+    __device__ __forceinline__ void look_up(const AttendArgs &a, const int *table, int t0, int context, int shift)
     {
-        const int in = a.page - 1;
+        page = ahead;
+        ahead = page_of(a, table, t0 + 16 * (threadIdx.x & 3), context, shift);
+    }
+    __device__ __forceinline__ void load(const AttendArgs &a, int h, int t0, int context)
+    {
+        const int in = a.page - 1, id = max(page, 0);
+        const int64_t at = (int64_t)id * a.Hk + h, bytes = (int64_t)a.page * D;
+        ks = a.k_scale[at];
+        lv = a.v_scale[at];
+        if (a.page >= 64) {                  // the tile is of one page: scalar bases
+            const int64_t from = ((int64_t)uniform(id) * a.Hk + h) * bytes;
+            const uint8_t *kb = a.k_codes + from + (t0 & in) * D, *vb = a.v_codes + from + (t0 & in);
 #pragma unroll
-        for (int i = 0; i < PARTS; ++i) {
-            const int t = t0 + key_token(i);
-            const int id = max(page_of(a, table, t & ~15, context, shift), 0);
-            k[i] = *reinterpret_cast<const uint4 *>(a.k_codes + (((int64_t)id * a.Hk + h) * a.page + (t & in)) * D + 16 * key_part(i));
+            for (int i = 0; i < PARTS; ++i)
+                k[i] = *reinterpret_cast<const uint4 *>(kb + (uint32_t)(key_token(i) * D + 16 * key_part(i)));
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i)
+                v[i] = *reinterpret_cast<const uint4 *>(vb + (uint32_t)(channel(i) * a.page + 16 * (threadIdx.x & 3)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                const int g = key_group(i);
+                const uint8_t *kb = a.k_codes + ((int64_t)__builtin_amdgcn_readlane(id, g) * a.Hk + h) * bytes + ((t0 + 16 * g) & in) * D;
+                k[i] = *reinterpret_cast<const uint4 *>(kb + (uint32_t)((key_token(i) & 15) * D + 16 * key_part(i)));
+            }
+            const uint8_t *vb = a.v_codes + at * bytes + ((t0 + 16 * (threadIdx.x & 3)) & in);
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) v[i] = *reinterpret_cast<const uint4 *>(vb + (uint32_t)(channel(i) * a.page));
         }
-        const int t = t0 + 16 * (threadIdx.x & 3), id = page_of(a, table, t, context, shift);
-        const int64_t at = (int64_t)max(id, 0) * a.Hk + h;
+        there = (int)__ballot(page >= 0) & 15;
+        if (!INT8 && (t0 + 64 > context || there != 15)) {
+            // no NaN where the weight is zero
+            const int n = page < 0 ? 0 : context - (t0 + 16 * (threadIdx.x & 3));
 #pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-            v[i] = *reinterpret_cast<const uint4 *>(a.v_codes + (at * D + channel(i)) * a.page + (t & in));
-        if (!INT8 && t0 + 64 > context) {
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) v[i] = keep_bytes(v[i], context - t);   // no NaN where the weight is zero
+            for (int i = 0; i < PARTS; ++i) v[i] = keep_bytes(v[i], n);
         }
-        if (!INT8 && id < 0) {
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) v[i] = make_uint4(0, 0, 0, 0);
-        }
-        there = id >= 0;
-        ks = there ? a.k_scale[at] : 0.f;
-        vs = there ? a.v_scale[at] : 0.f;
+    }
+    // behind the loads' arrival
+    __device__ __forceinline__ void scales()
+    {
+        const bool fine = is_finite(lv);
+        const bool has = there >> (threadIdx.x & 3) & 1;
+        broken = (int)__ballot(has && !fine) & 15;
+        lv = fine && has ? fast_log2(lv) : -__builtin_inff();
+        ks = has ? ks : 0.f;
     }
     __device__ __forceinline__ void put(Tile<D> &tile) const
     {
@@ -101,17 +126,16 @@ template <int D, int WAVES, bool INT8> struct Loader {
             *reinterpret_cast<f16x8 *>(to) = codes_f16<INT8>(v[i].x, v[i].y);
             *reinterpret_cast<f16x8 *>(to + 16) = codes_f16<INT8>(v[i].z, v[i].w);
         }
-        if (threadIdx.x < 4) {
-            tile.ks[threadIdx.x] = ks;
-            tile.vs[threadIdx.x] = vs;
-            tile.there[threadIdx.x] = there;
-        }
     }
 };
+__device__ __forceinline__ float lane_value(float x, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
 
 // LINE: shares of the line of units; otherwise a workgroup a block of rows.
 template <int D, int WAVES, bool BF, bool INT8, bool LINE>
-__global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 ? 1 : 2) kda_cache_attend_rows_kernel(AttendArgs a, int shift)
+__global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 || (D == 128 && !BF) ? 1 : 2) kda_cache_attend_rows_kernel(AttendArgs a, int shift)
 {
     constexpr int SPLIT = BF ? 1 : 2, KS = D / 16, DT = D / 32, ROWS = 32 * WAVES;
     typedef typename Store<BF>::type T;
@@ -180,19 +204,35 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 ? 1 : 2) kd
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-        float top = -__builtin_inff(), sum = 0.f, reference = 0.f;
+        // The value scales' reference is a power of two, 2^level, above the largest met.
+        float top = -__builtin_inff(), sum = 0.f, level = -__builtin_inff();
 
         const int *table = a.table + (int64_t)b * a.per;
         Loader<D, WAVES, INT8> next;
         if (t_begin < t_stop) {
-            next.load(a, table, h, t_begin * 64, s.context, shift);
+            next.look_up(a, table, t_begin * 64, s.context, shift);
+            next.look_up(a, table, t_begin * 64 + 64, s.context, shift);
+            next.load(a, h, t_begin * 64, s.context);
             next.put(tiles_lds[0]);
         }
         __syncthreads();
         for (int t = t_begin; t < t_stop; ++t) {
             const Tile<D> &tile = tiles_lds[(t - t_begin) & 1];
             const int t0 = t * 64;
-            if (t + 1 < t_stop) next.load(a, table, h, t0 + 64, s.context, shift);
+            // this tile's scales, by group
+            next.scales();
+            float ks[4], lv[4], most = -__builtin_inff();
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                ks[g] = lane_value(next.ks, g);
+                lv[g] = lane_value(next.lv, g);
+                most = fmaxf(most, lv[g]);
+            }
+            const int there = next.there, broken = next.broken;
+            if (t + 1 < t_stop) {
+                next.look_up(a, table, t0 + 128, s.context, shift);
+                next.load(a, h, t0 + 64, s.context);
+            }
 
             f32x16 x[2];
 #pragma unroll
@@ -206,70 +246,74 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 ? 1 : 2) kd
                     for (int p = 0; p < SPLIT; ++p) x[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, q[p][k], x[j], 0, 0, 0);
                 }
             }
-            // value scales: a new reference is rare after the first tiles
-            float vs[4], ks[4], most = 0.f;
-            int there = 0, broken = 0;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                broken |= (is_finite(tile.vs[g]) ? 0 : 1) << g;
-                vs[g] = is_finite(tile.vs[g]) ? tile.vs[g] : 0.f;
-                ks[g] = tile.ks[g];
-                there |= tile.there[g] << g;
-                most = fmaxf(most, vs[g]);
-            }
-            if (__any(most > reference)) {
-                const float now = 2.f * most, f = reference / now;
+            if (most > level) {              // rare after the first tiles
+                const float now = __builtin_ceilf(most) + 1.f, f = fast_exp2(level - now);
+                level = now;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[d][i] *= f;
-                reference = now;
             }
-            const float inv = reference > 0.f ? fast_rcp(reference) : 0.f;
-            const bool masked = t0 + 64 > whole || there != 15;
+            // scores to weights, in place
+            float c[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) c[g] = factor * ks[g];
+            if (t0 + 64 > whole || there != 15) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int seen = there >> g & 1 ? limit - (t0 + 16 * g + 8 * half) : 0;       // of 8 tokens
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[g >> 1][8 * (g & 1) + i] = i < seen ? x[g >> 1][8 * (g & 1) + i] * c[g] : -__builtin_inff();
+                    c[g] = 1.f;
+                }
+            }
             float best = -__builtin_inff();
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const float c = factor * ks[g];
-                const int seen = there >> g & 1 ? limit - (t0 + 16 * g + 8 * half) : 0;    // of the lane's 8 tokens
-                float y = -__builtin_inff();
+                float y = x[g >> 1][8 * (g & 1)];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float v = x[g >> 1][8 * (g & 1) + i] * c;
-                    if (masked) v = i < seen ? v : -__builtin_inff();
-                    x[g >> 1][8 * (g & 1) + i] = v;
-                    y = fmaxf(y, v);
-                }
-                best = fmaxf(best, y);
+                for (int i = 1; i < 8; ++i) y = fmaxf(y, x[g >> 1][8 * (g & 1) + i]);
+                best = fmaxf(best, y * c[g]);
             }
             best = halves_max(best);
-            const float now = fmaxf(top, best), base = now == -__builtin_inff() ? 0.f : now;
-            const float fade = fast_exp2(top - base);
-            top = now;
-            if (__any(fade != 1.f)) {
+            // A base that is up to SLACK below the maximum serves as well: outputs then move rarely.
+            if (__any(best > top + SLACK)) {
+                const float now = fmaxf(top, best), fade = now == -__builtin_inff() ? 1.f : fast_exp2(top - now);
+                top = now;
                 sum *= fade;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[d][i] *= fade;
             }
+            const float base = top == -__builtin_inff() ? 0.f : top;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                float ratio = reference > 0.f ? vs[g] * inv : 1.f;
-                ratio = VALUE_GAIN * fmaxf(ratio, 0x1p-40f);
-                const float offset = fast_log2(ratio) - base;
-                float v[8], total = 0.f;
+                const float up = ratio_level(lv[g], level), offset = up - base;
+                float total = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    v[i] = fast_exp2(x[g >> 1][8 * (g & 1) + i] + offset);
-                    total += v[i];
+                    const float v = fast_exp2(__builtin_fmaf(x[g >> 1][8 * (g & 1) + i], c[g], offset));
+                    x[g >> 1][8 * (g & 1) + i] = v;
+                    total += v;
                 }
-                sum += total * fast_rcp(ratio);
-                if (broken >> g & 1) {
-                    const int seen = limit - (t0 + 16 * g + 8 * half);
+                sum = __builtin_fmaf(total, fast_exp2(-up), sum);
+            }
+            if (broken) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = i < seen ? __builtin_nanf("") : v[i];
+                for (int g = 0; g < 4; ++g) {
+                    const int seen = broken >> g & 1 ? limit - (t0 + 16 * g + 8 * half) : 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[g >> 1][8 * (g & 1) + i] = i < seen ? __builtin_nanf("") : x[g >> 1][8 * (g & 1) + i];
                 }
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = x[g >> 1][8 * (g & 1) + i];
                 f16x8 w[SPLIT];
                 split_f16<SPLIT>(v, [&](int p) -> f16x8 & { return w[p]; });
 #pragma unroll
@@ -285,7 +329,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 ? 1 : 2) kd
 
         sum = halves_sum(sum);
         const bool whole_row = t_begin == 0 && t_end == tiles;
-        const float f = reference * VALUE_REST;
+        const float f = level == -__builtin_inff() ? 0.f : fast_exp2(level) * VALUE_REST;
         float *piece = nullptr;
         if constexpr (LINE) {
             piece = a.ws + (sizeof(Record) / 4) * gridDim.x + (int64_t)(2 * blockIdx.x + (t_begin == 0)) * PIECE<D, ROWS>;
