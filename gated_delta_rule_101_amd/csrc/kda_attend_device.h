@@ -176,7 +176,7 @@ __device__ __forceinline__ uint4 keep_bytes(uint4 x, int n)
 struct Record {      // a row of units that is cut: its first piece is this workgroup's
     int b, h, block, last;                   // last: the workgroup of its last piece, -1: none
 };
-constexpr int SHARES = 512;                  // workgroups that share the line of units, at most
+constexpr int SHARES = 1024;                 // workgroups that share the line of units, at most
 // Floats of one piece: output rows, then maxima and sums.
 template <int D, int ROWS> constexpr int PIECE = ROWS * (D + 2);
 
@@ -273,8 +273,8 @@ __device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of
     return l;
 }
 
-// Workgroups for a line of at most `units` units.
-inline int shares(int64_t units) { return units < SHARES && units > 0 ? (int)units : SHARES; }
+// Workgroups for a line of at most `units` units, of which the device holds `most` at once.
+inline int shares(int64_t units, int most) { return units < most && units > 0 ? (int)units : most; }
 
 // The launcher for many query rows a sequence (kda_cache_attend_rows.hip), and
 // floats of workspace it may need.

@@ -256,60 +256,73 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
     if (threadIdx.x == 0) reinterpret_cast<Record *>(a.ws)[blockIdx.x] = mine;
 }
 
-// Joins the pieces of cut rows: blocks (first piece's workgroup, query row).
+// Joins the pieces of cut rows: blocks (first piece's workgroup, query rows).  A
+// group of D / 4 lanes has a row where pieces are few; where they are many (one
+// long sequence), the groups share each row's pieces and meet in LDS.
+template <int D> constexpr int JOIN_ROWS = 1024 / D;         // groups of a workgroup
 template <int D, int ROWS, bool BF>
 __global__ void __launch_bounds__(256) kda_cache_attend_join_kernel(AttendArgs a)
 {
-    constexpr int L = D / 4, GROUPS = 256 / L;
+    constexpr int L = D / 4, GROUPS = JOIN_ROWS<D>, ALONE = 16;
     typedef typename Store<BF>::type T;
-    __shared__ float part[4];
-    __shared__ float weight[SHARES];
-    __shared__ __align__(16) float acc[256][4];
-    const int first = blockIdx.x, rr = blockIdx.y, tid = threadIdx.x;
+    __shared__ __align__(16) float acc[GROUPS][L][4];
+    __shared__ float best_of[GROUPS], sum_of[GROUPS];
+    const int first = blockIdx.x, tid = threadIdx.x, l = tid % L, g = tid / L, d = 4 * l;
     const Record rec = reinterpret_cast<const Record *>(a.ws)[first];
     if (rec.last < 0) return;
     const Sequence s = sequence(a, rec.b);
-    const int G = a.Hq / a.Hk, r0 = rec.block * ROWS;
-    if (r0 + rr >= s.queries * G) return;
+    const int G = a.Hq / a.Hk, r0 = rec.block * ROWS, active = min(ROWS, s.queries * G - r0);
     const float *pieces = a.ws + (sizeof(Record) / 4) * gridDim.x;
-    const int n = rec.last - first + 1;
+    const int n = rec.last - first + 1, row0 = blockIdx.y * GROUPS;
     const auto piece = [&](int i) { return pieces + (int64_t)(2 * (first + i) + (i == 0)) * PIECE<D, ROWS>; };
-    float best = -__builtin_inff();
-    for (int i = tid; i < n; i += 256) best = fmaxf(best, piece(i)[ROWS * D + rr]);
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) best = fmaxf(best, __shfl_xor(best, m, 64));
-    if ((tid & 63) == 0) part[tid / 64] = best;
-    __syncthreads();
-    best = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    __syncthreads();
-    const bool none = best == -__builtin_inff();
-    float l = 0.f;
-    for (int i = tid; i < n; i += 256) {
-        const float w = none ? 1.f : fast_exp2(piece(i)[ROWS * D + rr] - best);
-        weight[i] = w;
-        l += w * piece(i)[ROWS * D + ROWS + rr];
-    }
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) l += __shfl_xor(l, m, 64);
-    if ((tid & 63) == 0) part[tid / 64] = l;
-    __syncthreads();
-    l = part[0] + part[1] + part[2] + part[3];
-    const int d = 4 * (tid % L), g = tid / L;
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    // pieces i, i + step, ... of a row: the running maximum, sum and output
+    const auto gather = [&](int rr, int i, int step, float &best, float &sum, float (&y)[4]) {
+        best = -__builtin_inff();
+        sum = y[0] = y[1] = y[2] = y[3] = 0.f;
 #pragma unroll 4
-    for (int i = g; i < n; i += GROUPS) {
-        const float4 x = *reinterpret_cast<const float4 *>(piece(i) + rr * D + d);
-        const float w = weight[i];
-        y[0] += w * x.x; y[1] += w * x.y; y[2] += w * x.z; y[3] += w * x.w;
+        for (; i < n; i += step) {
+            const float *p = piece(i);
+            const float top = p[ROWS * D + rr], part = p[ROWS * D + ROWS + rr];
+            const float4 x = *reinterpret_cast<const float4 *>(p + rr * D + d);
+            const float now = fmaxf(best, top);
+            const float f = best == now ? 1.f : fast_exp2(best - now), w = top == now ? 1.f : fast_exp2(top - now);
+            best = now;
+            sum = sum * f + part * w;
+            y[0] = y[0] * f + x.x * w;
+            y[1] = y[1] * f + x.y * w;
+            y[2] = y[2] * f + x.z * w;
+            y[3] = y[3] * f + x.w * w;
+        }
+    };
+    float best, sum, y[4];
+    if (n <= ALONE) {
+        const int rr = row0 + g;
+        if (rr >= active) return;
+        gather(rr, 0, 1, best, sum, y);
+        write_row<T>(a, s, rec.h, G, r0 + rr, d, D, y, best, sum);
+        return;
     }
+    for (int rr = row0; rr < min(row0 + GROUPS, active); ++rr) {
+        gather(rr, g, GROUPS, best, sum, y);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[tid][i] = y[i];
-    __syncthreads();
-    if (g == 0) {
-        for (int k = 1; k < GROUPS; ++k)
+        for (int i = 0; i < 4; ++i) acc[g][l][i] = y[i];
+        if (l == 0) {
+            best_of[g] = best;
+            sum_of[g] = sum;
+        }
+        __syncthreads();
+        if (g == 0) {
+            for (int k = 0; k < GROUPS; ++k) best = fmaxf(best, best_of[k]);
+            sum = y[0] = y[1] = y[2] = y[3] = 0.f;
+            for (int k = 0; k < GROUPS; ++k) {
+                const float w = best_of[k] == best ? 1.f : fast_exp2(best_of[k] - best);
+                sum += sum_of[k] * w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] += acc[k * L + tid][i];
-        write_row<T>(a, s, rec.h, G, r0 + rr, d, D, y, best, l);
+                for (int i = 0; i < 4; ++i) y[i] += acc[k][l][i] * w;
+            }
+            write_row<T>(a, s, rec.h, G, r0 + rr, d, D, y, best, sum);
+        }
+        __syncthreads();
     }
 }
 
@@ -334,7 +347,7 @@ int64_t units_of(int B, int Hk, int64_t tiles, int D, int64_t rows)
 template <int D, bool BF, bool INT8> hipError_t launch_rows(const AttendArgs &a, hipStream_t s)
 {
     const int64_t rows = (int64_t)a.most * (a.Hq / a.Hk), tiles = ((int64_t)a.per * a.page + 63) / 64;
-    const int n = shares(units_of(a.B, a.Hk, tiles, D, rows));
+    const int n = shares(units_of(a.B, a.Hk, tiles, D, rows), 512);
     if constexpr (D <= 128)
         if (block_rows(rows) == 2) return launch<D, 2, BF, INT8>(a, n, s);
     return launch<D, 1, BF, INT8>(a, n, s);
@@ -346,7 +359,8 @@ template <bool BF, bool INT8> hipError_t launch_d(const AttendArgs &a, hipStream
 }
 template <int D, int ROWS> hipError_t join(const AttendArgs &a, int n, int rows, hipStream_t stream)
 {
-    const dim3 grid((unsigned)n, (unsigned)(rows < ROWS ? rows : ROWS));
+    const int used = rows < ROWS ? rows : ROWS;
+    const dim3 grid((unsigned)n, (unsigned)((used + JOIN_ROWS<D> - 1) / JOIN_ROWS<D>));
     if (a.bf16) hipLaunchKernelGGL((kda_cache_attend_join_kernel<D, ROWS, true>), grid, dim3(256), 0, stream, a);
     else hipLaunchKernelGGL((kda_cache_attend_join_kernel<D, ROWS, false>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
@@ -371,7 +385,7 @@ int64_t cache_attend_workspace_floats(int tokens, int B, int Hq, int Hk, int D, 
     for (const bool bf16 : {false, true}) {          // the size does not depend on the type
         int64_t x;
         if (is_few(D, bf16, rows))
-            x = shares(units_of(B, Hk, tiles, D, rows)) *
+            x = shares(units_of(B, Hk, tiles, D, rows), 512) *
                 (int64_t)(sizeof(Record) / 4 + 2 * 16 * (D == 256 ? 1 : block_rows(rows)) * (D + 2));
         else
             x = attend_rows_workspace_floats(tokens, B, Hq, Hk, D, page, per, most);

@@ -133,11 +133,15 @@ __device__ __forceinline__ float lane_value(float x, int lane)
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
 
+// Tiles of a workgroup's LDS: two, and one barrier a tile; one where workgroups
+// are of two waves, so that four of them fit a CU.
+template <int WAVES> constexpr int TILES = WAVES == 2 ? 1 : 2;
+
 // LINE: shares of the line of units; otherwise a workgroup a block of rows.
 template <int D, int WAVES, bool BF, bool INT8, bool LINE>
-__global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 || (D == 128 && !BF) ? 1 : 2) kda_cache_attend_rows_kernel(AttendArgs a, int shift)
+__global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 : 2) kda_cache_attend_rows_kernel(AttendArgs a, int shift)
 {
-    constexpr int SPLIT = BF ? 1 : 2, KS = D / 16, DT = D / 32, ROWS = 32 * WAVES;
+    constexpr int SPLIT = BF ? 1 : 2, KS = D / 16, DT = D / 32, ROWS = 32 * WAVES, BUFFERS = TILES<WAVES>;
     typedef typename Store<BF>::type T;
     extern __shared__ __align__(16) uint8_t lds[];
     Tile<D> *const tiles_lds = reinterpret_cast<Tile<D> *>(lds);
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 || (D == 12
         }
         __syncthreads();
         for (int t = t_begin; t < t_stop; ++t) {
-            const Tile<D> &tile = tiles_lds[(t - t_begin) & 1];
+            const Tile<D> &tile = tiles_lds[BUFFERS == 2 ? (t - t_begin) & 1 : 0];
             const int t0 = t * 64;
             // this tile's scales, by group
             next.scales();
@@ -300,7 +304,8 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 || (D == 12
                 }
                 sum = __builtin_fmaf(total, fast_exp2(-up), sum);
             }
-            if (broken) {
+            if (broken) {                        // NaN for the places seen
+                asm volatile("");                // a branch, not selects for every tile
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int seen = broken >> g & 1 ? limit - (t0 + 16 * g + 8 * half) : 0;
@@ -323,7 +328,8 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 2 || D == 256 || (D == 12
                     for (int p = 0; p < SPLIT; ++p) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, w[p], o[d], 0, 0, 0);
                 }
             }
-            if (t + 1 < t_stop) next.put(tiles_lds[(t + 1 - t_begin) & 1]);
+            if (BUFFERS == 1) __syncthreads();
+            if (t + 1 < t_stop) next.put(tiles_lds[BUFFERS == 2 ? (t + 1 - t_begin) & 1 : 0]);
             __syncthreads();
         }
 
@@ -372,14 +378,14 @@ Shape shape_of(int tokens, int B, int Hq, int Hk, int D, int page, int per, int 
     // blocks of all sequences, at most (as the kernel counts them)
     const int64_t blocks = ((int64_t)tokens * (Hq / Hk) / (32 * s.waves) + B) * Hk;
     s.line = blocks < 1024;
-    s.workgroups = s.line ? shares(blocks * (tiles > 0 ? tiles : 1)) : blocks < ((int64_t)1 << 24) ? (int)blocks : 0;
+    s.workgroups = s.line ? shares(blocks * (tiles > 0 ? tiles : 1), s.waves == 2 ? 1024 : D == 256 ? 256 : 512) : blocks < ((int64_t)1 << 24) ? (int)blocks : 0;
     return s;
 }
 
 template <int D, int WAVES, bool BF, bool INT8> hipError_t launch(const AttendArgs &a, const Shape &s, hipStream_t stream)
 {
     const int shift = __builtin_ctz(a.page);
-    const size_t bytes = 2 * sizeof(Tile<D>);
+    const size_t bytes = TILES<WAVES> * sizeof(Tile<D>);
     const dim3 grid((unsigned)s.workgroups), threads(64 * WAVES);
     const auto set = [&](const void *k) { return hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); };
     if (!s.line) {
