@@ -32,19 +32,22 @@ _CODES = {torch.float8_e4m3fn: KDA_CODE_E4M3, torch.int8: KDA_CODE_INT8}
 
 def _heads(t: torch.Tensor, what: str) -> Tuple[int, int, int, int]:
     """(tokens, heads, channels, token stride) of rows [..., heads, channels]."""
-    if t.dim() < 3:
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 3:
         raise ValueError(f"{what} must be [..., heads, channels]")
-    H, D = t.shape[-2:]
-    lead = t.shape[:-2]
-    T = lead.numel()
+    H, D = shape[-2:]
     width = H * D
+    if len(shape) == 3 and strides[1:] == (D, 1) and shape[0] > 1 and width:     # the common case
+        return shape[0], H, D, strides[0]
+    lead = shape[:-2]
+    T = lead.numel()
     if T == 0 or width == 0:
         return T, H, D, width
-    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+    if (D > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != D):
         raise ValueError(f"{what}: heads and channels must be contiguous")
     # the leading axes as one: each that has more than one entry steps over the next
     stride = step = None
-    for n, s in zip(reversed(lead), reversed(t.stride()[:-2])):
+    for n, s in zip(reversed(lead), reversed(strides[:-2])):
         if n == 1:
             continue
         if stride is None:
@@ -118,12 +121,12 @@ def _qk_shapes(q, k, q_weight, k_weight, positions, rotary):
     return T, Hq, Hk, D, rows, R, sq, sk
 
 
-def _like(t: Optional[torch.Tensor], x: torch.Tensor, what: str, dev) -> torch.Tensor:
-    """An output of x's shape and type: `t`, or a new one."""
+def _like(t: Optional[torch.Tensor], x: torch.Tensor, width: int, what: str, dev) -> Tuple[torch.Tensor, int]:
+    """An output of x's shape and type, `t` or a new one, and its token stride."""
     if t is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=dev)
+        return torch.empty(x.shape, dtype=x.dtype, device=dev), width
     _shape(t, x.shape, what, x.dtype)
-    return t
+    return t, _heads(t, what)[3]
 
 
 def kda_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
@@ -147,8 +150,8 @@ def kda_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[to
         raise ValueError("all tensors must be on the GPU")
     _one_device(dev, q, k, q_out, k_out)
     with _on(dev, stream) as handle:
-        q_out, k_out = _like(q_out, q, "q_out", dev), _like(k_out, k, "k_out", dev)
-        so, sko = _heads(q_out, "q_out")[3], _heads(k_out, "k_out")[3]
+        q_out, so = _like(q_out, q, Hq * D, "q_out", dev)
+        k_out, sko = _like(k_out, k, Hk * D, "k_out", dev)
         st = lib.kda_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions),
                                       _ptr(rotary) if R else None, _ptr(q_out), _ptr(k_out), T, Hq, Hk, D, R, rows,
                                       int(neighbours), sq, sk, so, sko, code, handle)
@@ -184,12 +187,12 @@ def kda_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Te
         raise ValueError("all tensors must be on the GPU")
     _one_device(dev, dq_out, dk_out, q, k, dq, dk)
     with _on(dev, stream) as handle:
-        out = {"dq": _like(dq, q, "dq", dev), "dk": _like(dk, k, "dk", dev)}
-        sdq, sdk = _heads(out["dq"], "dq")[3], _heads(out["dk"], "dk")[3]
+        dq, sdq = _like(dq, q, Hq * D, "dq", dev)
+        dk, sdk = _like(dk, k, Hk * D, "dk", dev)
+        out = {"dq": dq, "dk": dk}
         need = 0
         if want_dweights:
-            out["dq_weight"] = torch.empty((D,), dtype=torch.float32, device=dev)
-            out["dk_weight"] = torch.empty((D,), dtype=torch.float32, device=dev)
+            out["dq_weight"], out["dk_weight"] = torch.empty((2, D), dtype=torch.float32, device=dev).unbind()
             need = int(lib.kda_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, D))
         ws = _workspace(workspace, need, dev)
         st = lib.kda_qk_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),

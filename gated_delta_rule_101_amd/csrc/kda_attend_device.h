@@ -197,24 +197,27 @@ __device__ __forceinline__ void write_row(const AttendArgs &a, const Sequence &s
 
 // A value that all lanes hold, as the scalar it is.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ int64_t uniform(int64_t x)
-{
-    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x));
-}
 
 // The line of units: 64 tokens of one sequence, key head and block of query rows,
 // sequences, heads, blocks and tokens in that order.  A workgroup's share of it.
+// The line is shorter than 2^31 units (the launchers refuse longer ones).
 struct Line {
     int b;                                   // sequence of the next unit
-    int64_t u;                               // the unit's place among its sequence's
-    int64_t left, at, share;                 // units to do, place on the line, units a workgroup
+    int u;                                   // the unit's place among its sequence's
+    int left, at, share;                     // units to do, place on the line, units a workgroup
+    bool single;                             // shares begin with the rows of units
+    // the workgroup that ends a row of units of which this one has the first, but not all
+    __device__ __forceinline__ int last(int tiles) const
+    {
+        return single ? blockIdx.x + (unsigned)(tiles - 1) / (unsigned)share : (unsigned)(at + tiles - 1) / (unsigned)share;
+    }
 };
 __device__ __forceinline__ int tiles_of(const Sequence &s) { return max((s.context + 63) / 64, 1); }
 __device__ __forceinline__ int blocks_of(const Sequence &s, int G, int rows)
 {
-    return (int)(((int64_t)s.queries * G + rows - 1) / rows);
+    return (int)(((unsigned)s.queries * G + rows - 1) / rows);   // below 2^31 rows, and rows a power of two
 }
-template <int WAVES> __device__ __forceinline__ int64_t workgroup_sum(int64_t x, int64_t *part)
+template <int WAVES> __device__ __forceinline__ int workgroup_sum(int x, int *part)
 {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
@@ -229,43 +232,68 @@ template <int WAVES> __device__ __forceinline__ int64_t workgroup_sum(int64_t x,
 // `at_least`: a share's least units, where rows of units are that long; short
 // rows stay whole.  part: [WAVES] in LDS.
 template <int WAVES>
-__device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of_block, int at_least, int64_t *part)
+__device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of_block, int at_least, int *part)
 {
     const int lane = threadIdx.x & 63;
-    int64_t units = 0, rows = 0;
-    for (int b = threadIdx.x; b < a.B; b += 64 * WAVES) {
-        const Sequence s = sequence(a, b);
-        const int64_t r = (int64_t)blocks_of(s, G, rows_of_block) * a.Hk;
-        rows += r;
-        units += r * tiles_of(s);
-    }
-    units = uniform(workgroup_sum<WAVES>(units, part));
-    rows = uniform(workgroup_sum<WAVES>(rows, part));
-    Line l = {0, 0, 0, 0, 1};
-    if (units == 0) return l;
-    const int64_t least = min((int64_t)at_least, (units + rows - 1) / rows);
-    l.share = max((units + gridDim.x - 1) / gridDim.x, least);
-    l.at = l.share * blockIdx.x;
-    l.left = max((int64_t)0, min(l.share, units - l.at));
-    if (l.left == 0) return l;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-        int64_t n = 0;
-        if (b0 + lane < a.B) {
-            const Sequence s = sequence(a, b0 + lane);
-            n = (int64_t)blocks_of(s, G, rows_of_block) * a.Hk * tiles_of(s);
+    if (a.B == 1) {
+        // all rows of units are alike: equal parts of each, of `at_least` units where that leaves enough workgroups
+        const Sequence s = sequence(a, 0);
+        const unsigned tiles = tiles_of(s), rows = blocks_of(s, G, rows_of_block) * a.Hk;
+        if (rows > 0 && rows <= gridDim.x) {
+            const unsigned parts = min((tiles + at_least - 1) / at_least, gridDim.x / rows);
+            const unsigned share = (tiles + parts - 1) / parts, row = blockIdx.x / parts, part_of = blockIdx.x - row * parts;
+            const int left = row < rows ? (int)(tiles - part_of * share) : 0;
+            return Line{0, (int)(row * tiles + part_of * share), max(min(left, (int)share), 0), 0, (int)share, true};
         }
-        int64_t upto = n;
+    }
+    int units = 0, rows = 0, upto = 0, mine = 0;
+    const auto of_lane = [&](int b) {            // units of sequence b, and of those up to it among 64
+        mine = 0;
+        if (b < a.B) {
+            const Sequence s = sequence(a, b);
+            mine = blocks_of(s, G, rows_of_block) * a.Hk;
+            rows += mine;
+            mine *= tiles_of(s);
+        }
+        upto = mine;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int64_t y = __shfl_up(upto, d, 64);
+            const int y = __shfl_up(upto, d, 64);
             if (lane >= d) upto += y;
         }
+    };
+    if (a.B <= 64) {                             // a wave sees them all
+        of_lane(lane);
+        units = uniform(__shfl(upto, 63, 64));
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) rows += __shfl_xor(rows, m, 64);
+        rows = uniform(rows);
+    } else {
+        for (int b = threadIdx.x; b < a.B; b += 64 * WAVES) {
+            const Sequence s = sequence(a, b);
+            const int r = blocks_of(s, G, rows_of_block) * a.Hk;
+            rows += r;
+            units += r * tiles_of(s);
+        }
+        units = uniform(workgroup_sum<WAVES>(units, part));
+        rows = uniform(workgroup_sum<WAVES>(rows, part));
+    }
+    Line l = {0, 0, 0, 0, 1, false};
+    if (units == 0) return l;
+    const unsigned least = min((unsigned)at_least, ((unsigned)units + rows - 1) / (unsigned)rows);
+    l.share = (int)max(((unsigned)units + gridDim.x - 1) / gridDim.x, least);
+    const int64_t at = (int64_t)l.share * blockIdx.x;
+    if (at >= units) return l;
+    l.at = (int)at;
+    l.left = min(l.share, units - l.at);
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        if (a.B > 64) of_lane(b0 + lane);
         const uint64_t past = __ballot(before + upto > l.at);
         if (past) {
             const int f = __builtin_ctzll(past);
             l.b = b0 + f;
-            l.u = uniform(l.at - before - __shfl(upto - n, f, 64));
+            l.u = uniform(l.at - before - __shfl(upto - mine, f, 64));
             break;
         }
         before = uniform(before + __shfl(upto, 63, 64));
@@ -273,7 +301,12 @@ __device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of
     return l;
 }
 
+// Whether a line of blocks of a call's query rows is short enough to be counted.
 // Workgroups for a line of at most `units` units, of which the device holds `most` at once.
+inline bool line_fits(int64_t tiles, int64_t rows, int block, int B, int Hk)
+{
+    return (tiles > 0 ? tiles : 1) * Hk * (rows / block + B) < ((int64_t)1 << 31) - 65536;
+}
 inline int shares(int64_t units, int most) { return units < most && units > 0 ? (int)units : most; }
 
 // The launcher for many query rows a sequence (kda_cache_attend_rows.hip), and

@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
 {
     constexpr int SPLIT = BF ? 1 : 2, KS = D / 32, DT = D / 16, ROWS = 16 * NR;
     typedef typename Store<BF>::type T;
-    __shared__ int64_t part[4];
+    __shared__ int part[4];
     __shared__ __align__(16) float merge[4][16][D + 4];
     __shared__ float stat[4][2][ROWS];
     __shared__ float ref[4];
@@ -49,17 +49,28 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
     while (line.left > 0) {
         const Sequence s = sequence(a, line.b);
         const int tiles = tiles_of(s), blocks = blocks_of(s, G, ROWS);
-        const int64_t u = line.u;
-        if (u >= (int64_t)tiles * blocks * a.Hk) {
+        const unsigned u = line.u;
+        if (u >= (unsigned)tiles * blocks * a.Hk) {
             line.u = 0;
             ++line.b;
             continue;
         }
         const int b = line.b;
-        const int row = (int)(u / tiles), t_begin = (int)(u - (int64_t)row * tiles);
-        const int t_end = (int)min((int64_t)tiles, t_begin + line.left);
+        const int row = u / (unsigned)tiles, t_begin = u - row * tiles;
+        const int t_end = min(tiles, t_begin + line.left);
         const int h = row / blocks, block = row - h * blocks;
         const int r0 = block * ROWS, active = min(ROWS, s.queries * G - r0);
+        // Pages of a tile: of this lane's key rows (group m / 4), of its scores' tokens (group = quarter); looked up
+        // a tile ahead.
+        const int *table = a.table + (int64_t)b * a.per;
+        const int gk = m >> 2;
+        const auto look_up = [&](int t, int &pk, int &pv) {
+            pk = page_of(a, table, t * 64 + 16 * gk, s.context, shift);
+            pv = page_of(a, table, t * 64 + 16 * quarter, s.context, shift);
+        };
+        int pk, pv;
+        look_up(t_begin + wave, pk, pv);
+
         // queries: lane m is row r0 + 16 n + m
         f16x8 q[SPLIT][NR][KS];
         float factor[NR];
@@ -86,14 +97,9 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
             for (int d = 0; d < DT; ++d) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        const int *table = a.table + (int64_t)b * a.per;
         for (int t = t_begin + wave; t < t_end; t += 4) {
             const int t0 = t * 64;
             if (t0 >= furthest) break;
-            // pages of this lane's key rows (group m / 4) and of its scores' tokens (group = quarter)
-            const int gk = m >> 2;
-            const int pk = page_of(a, table, t0 + 16 * gk, s.context, shift);
-            const int pv = page_of(a, table, t0 + 16 * quarter, s.context, shift);
             const int64_t ak = (int64_t)max(pk, 0) * a.Hk + h, av = (int64_t)max(pv, 0) * a.Hk + h;
             const uint8_t *kp = a.k_codes + (ak * a.page + ((t0 + 16 * gk) & (a.page - 1)) + (m & 3)) * D + 16 * quarter;
             const uint8_t *vp = a.v_codes + (av * D + m) * a.page + ((t0 + 16 * quarter) & (a.page - 1));
@@ -107,6 +113,8 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
 #pragma unroll
             for (int d = 0; d < DT; ++d) vr[d] = *reinterpret_cast<const uint4 *>(vp + (int64_t)16 * d * a.page);
 
+            const bool gone = pv < 0, masked = t0 + 64 > whole || __any(gone);
+            look_up(t + 4, pk, pv);
             f16x8 ka[4][KS];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -116,9 +124,8 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
                     ka[i][2 * c + 1] = codes_f16<INT8>(kr[i][c].z, kr[i][c].w);
                 }
             const int tb = t0 + 16 * quarter;                  // this lane's first token
-            const bool masked = t0 + 64 > whole || __any(pv < 0);
-            const bool broken = pv >= 0 && !is_finite(vs);
-            const float lv = pv < 0 || broken ? -__builtin_inff() : fast_log2(vs);
+            const bool broken = !gone && !is_finite(vs);
+            const float lv = gone || broken ? -__builtin_inff() : fast_log2(vs);
             if (__any(lv > level)) {         // rare after the first tiles
                 const float now = __builtin_ceilf(quarters_max(lv)) + 1.f, f = fast_exp2(level - now);
                 level = now;
@@ -134,8 +141,8 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 if (NR > 1) __builtin_amdgcn_sched_barrier(0);     // one row tile's scores at a time, for the registers
-                const float c = factor[n] * (pv < 0 ? 0.f : ks);
-                const int seen = pv < 0 ? 0 : min(limit[n], s.context) - tb;     // of this lane's 16 tokens
+                const float c = factor[n] * (gone ? 0.f : ks);
+                const int seen = gone ? 0 : min(limit[n], s.context) - tb;     // of this lane's 16 tokens
                 float v[16], best = -__builtin_inff();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
             if (NR > 1) __builtin_amdgcn_sched_barrier(0);
             if (masked && !INT8) {
                 // weights of places that hold no token are zero; their codes must not be NaN
-                const int there = pv < 0 ? 0 : s.context - tb;
+                const int there = gone ? 0 : s.context - tb;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) vr[d] = keep_bytes(vr[d], there);
             }
@@ -211,7 +218,7 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
         }
         const bool whole_row = t_begin == 0 && t_end == tiles;
         float *piece = pieces + (int64_t)(2 * blockIdx.x + (t_begin == 0)) * PIECE<D, ROWS>;
-        if (t_begin == 0 && !whole_row) mine = {b, h, block, (int)((line.at + tiles - 1) / line.share)};
+        if (t_begin == 0 && !whole_row) mine = {b, h, block, line.last(tiles)};
         line.u += t_end - t_begin;
         line.left -= t_end - t_begin;
         line.at += t_end - t_begin;
@@ -347,6 +354,7 @@ int64_t units_of(int B, int Hk, int64_t tiles, int D, int64_t rows)
 template <int D, bool BF, bool INT8> hipError_t launch_rows(const AttendArgs &a, hipStream_t s)
 {
     const int64_t rows = (int64_t)a.most * (a.Hq / a.Hk), tiles = ((int64_t)a.per * a.page + 63) / 64;
+    if (!line_fits(tiles, (int64_t)a.tokens * (a.Hq / a.Hk), D <= 128 ? 16 * block_rows(rows) : 16, a.B, a.Hk)) return hipErrorNotSupported;
     const int n = shares(units_of(a.B, a.Hk, tiles, D, rows), 512);
     if constexpr (D <= 128)
         if (block_rows(rows) == 2) return launch<D, 2, BF, INT8>(a, n, s);

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
     typedef typename Store<BF>::type T;
     extern __shared__ __align__(16) uint8_t lds[];
     Tile<D> *const tiles_lds = reinterpret_cast<Tile<D> *>(lds);
-    __shared__ int64_t part[WAVES];
+    __shared__ int part[WAVES];
     const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x & 63, m = lane & 31, half = lane >> 5;
     const int G = a.Hq / a.Hk;
     Line line;
@@ -177,15 +177,15 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
             s = sequence(a, line.b);
             tiles = tiles_of(s);
             const int blocks = blocks_of(s, G, ROWS);
-            if (line.u >= (int64_t)tiles * blocks * a.Hk) {
+            if ((unsigned)line.u >= (unsigned)tiles * blocks * a.Hk) {
                 line.u = 0;
                 ++line.b;
                 continue;
             }
             b = line.b;
-            const int row = (int)(line.u / tiles);
-            t_begin = (int)(line.u - (int64_t)row * tiles);
-            t_end = (int)min((int64_t)tiles, t_begin + line.left);
+            const int row = (unsigned)line.u / (unsigned)tiles;
+            t_begin = line.u - row * tiles;
+            t_end = min(tiles, t_begin + line.left);
             h = row / blocks;
             block = row - h * blocks;
         } else {
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
         float *piece = nullptr;
         if constexpr (LINE) {
             piece = a.ws + (sizeof(Record) / 4) * gridDim.x + (int64_t)(2 * blockIdx.x + (t_begin == 0)) * PIECE<D, ROWS>;
-            if (t_begin == 0 && !whole_row) mine = {b, h, block, (int)((line.at + tiles - 1) / line.share)};
+            if (t_begin == 0 && !whole_row) mine = {b, h, block, line.last(tiles)};
             line.u += t_end - t_begin;
             line.left -= t_end - t_begin;
             line.at += t_end - t_begin;
@@ -377,7 +377,7 @@ Shape shape_of(int tokens, int B, int Hq, int Hk, int D, int page, int per, int 
     s.waves = rows <= 64 && D <= 128 ? 2 : 4;
     // blocks of all sequences, at most (as the kernel counts them)
     const int64_t blocks = ((int64_t)tokens * (Hq / Hk) / (32 * s.waves) + B) * Hk;
-    s.line = blocks < 1024;
+    s.line = blocks < 1024 && line_fits(tiles, (int64_t)tokens * (Hq / Hk), 32 * s.waves, B, Hk);
     s.workgroups = s.line ? shares(blocks * (tiles > 0 ? tiles : 1), s.waves == 2 ? 1024 : D == 256 ? 256 : 512) : blocks < ((int64_t)1 << 24) ? (int)blocks : 0;
     return s;
 }
