@@ -20,6 +20,7 @@ allocates belong to the stream it runs on.
 
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Dict, Optional, Tuple, Union
 
 import torch
@@ -246,7 +247,13 @@ def kda_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_co
 def kda_cache_attention_workspace_bytes(tokens: int, B: int, Hq: int, Hk: int, D: int, page: int, max_pages: int,
                                         max_queries: int = 1) -> int:
     """Device bytes kda_cache_attention needs."""
-    return int(load_library().kda_cache_attention_workspace_bytes(tokens, B, Hq, Hk, D, page, max_pages, max_queries))
+    return _attention_bytes(tokens, B, Hq, Hk, D, page, max_pages, max_queries)
+
+
+@lru_cache(maxsize=1024)
+def _attention_bytes(*sizes: int) -> int:
+    """A function of the sizes alone: 0.2 us where a call of the library takes 2, of 18 for the smallest attention."""
+    return int(load_library().kda_cache_attention_workspace_bytes(*sizes))
 
 
 def kda_cache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
@@ -287,7 +294,7 @@ def kda_cache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.T
             out = torch.empty_like(q)
         if lse is None and want_lse:
             lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
-        ws = _workspace(workspace, int(lib.kda_cache_attention_workspace_bytes(N, B, Hq, Hk, D, page, per, most)), dev)
+        ws = _workspace(workspace, _attention_bytes(N, B, Hq, Hk, D, page, per, most), dev)
         st = lib.kda_cache_attention(_ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
                                      _ptr(block_table), _ptr(context), _ptr(q_start), _ptr(out), _ptr(lse), _ptr(ws),
                                      _nbytes(ws), N, B, Hq, Hk, D, pages, page, per, most,

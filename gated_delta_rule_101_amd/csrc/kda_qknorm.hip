@@ -10,7 +10,8 @@
 // hold whole pairs between them: blocks R / 2 apart in the rotated part, half
 // of the rest apart behind it.  So the rotation stays inside a lane, and the
 // token's cosines and sines are read once for all its heads.  Head groups are
-// read BATCH at a time, so that their loads are in flight together.  Where few
+// read BATCH at a time, so that their loads are in flight together; a group is all
+// queries or all keys, so that weights and their gradients are named by it.  Where few
 // tokens would leave the device empty, a token's head groups are dealt to
 // several waves.  Backward: a lane's channels are the same for every head, so
 // the weights' gradients add up in registers, meet in LDS and go to the
@@ -124,14 +125,14 @@ template <int V, int NV> struct Weights {
     float a[2][NV][V], b[2][NV][V];                  // queries', keys'
 };
 
-constexpr int BATCH = 4;
 
 template <typename T, int V, int NV, bool NEIGH, bool BWD>
 __global__ void __launch_bounds__(256) kda_qk_norm_kernel(QkNormArgs a, int lanes, int parts)
 {
     typedef Head<T, V, NV, NEIGH> H;
-    const int wave = threadIdx.x / 64, lane = threadIdx.x & 63, l = lane & (lanes - 1), sub = lane / lanes;
-    const int per_wave = 64 / lanes, heads = a.Hq + a.Hk, groups = (heads + per_wave - 1) / per_wave;
+    constexpr int BATCH = BWD ? 3 : 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63, l = lane & (lanes - 1), sub = lane / lanes;
+    const int per_wave = 64 / lanes, q_groups = (a.Hq + per_wave - 1) / per_wave, groups = q_groups + (a.Hk + per_wave - 1) / per_wave;
     const Channels<V, NV, NEIGH> ch(l, lanes, a.D, a.R);
     Weights<V, NV> w, dw;
 #pragma unroll
@@ -158,29 +159,26 @@ __global__ void __launch_bounds__(256) kda_qk_norm_kernel(QkNormArgs a, int lane
         const float poison = beyond ? __builtin_nanf("") : 0.f;
         for (int g0 = part; g0 < groups; g0 += parts * BATCH) {
             H x[BATCH], gy[BWD ? BATCH : 1];
-            const auto head_of = [&](int i) { return (g0 + i * parts) * per_wave + sub; };
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
-                const int h = head_of(i);
-                const bool on = h < heads && real, is_q = h < a.Hq;
-                const T *p = is_q ? (const T *)a.q + t * a.q_stride + (int64_t)h * a.D
-                                  : (const T *)a.k + t * a.k_stride + (int64_t)(h - a.Hq) * a.D;
-                x[i].load(on ? p : nullptr, ch);
-                if constexpr (BWD) {
-                    const T *g = is_q ? (const T *)a.gq + t * a.gq_stride + (int64_t)h * a.D
-                                      : (const T *)a.gk + t * a.gk_stride + (int64_t)(h - a.Hq) * a.D;
-                    gy[i].load(on ? g : nullptr, ch);
-                }
+                const int g = g0 + i * parts;
+                const bool is_q = g < q_groups;
+                const int h = (is_q ? g : g - q_groups) * per_wave + sub;
+                const bool on = g < groups && h < (is_q ? a.Hq : a.Hk) && real;
+                const int64_t head = (int64_t)h * a.D;
+                x[i].load(on ? (is_q ? (const T *)a.q + t * a.q_stride : (const T *)a.k + t * a.k_stride) + head : nullptr, ch);
+                if constexpr (BWD)
+                    gy[i].load(on ? (is_q ? (const T *)a.gq + t * a.gq_stride : (const T *)a.gk + t * a.gk_stride) + head : nullptr, ch);
             }
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                if (g0 + i * parts >= groups) break;
-                const int h = head_of(i), s = h < a.Hq ? 0 : 1;
+            // a group of heads, all queries or all keys
+            const auto work = [&](auto keys, const H &xi, const H &gi, int h) {
+                constexpr int S = decltype(keys)::value;
+                const bool mine = h < (S ? a.Hk : a.Hq);
                 float p[NV][V], q[NV][V], ss = 0.f, sd = 0.f;
-                x[i].to_f32(p, q);
+                xi.to_f32(p, q);
                 float gp[NV][V], gq[NV][V];
                 if constexpr (BWD) {
-                    gy[i].to_f32(gp, gq);
+                    gi.to_f32(gp, gq);
                     angles.template turn<-1>(gp, gq);
                 }
 #pragma unroll
@@ -190,8 +188,8 @@ __global__ void __launch_bounds__(256) kda_qk_norm_kernel(QkNormArgs a, int lane
                         ss += p[j][e] * p[j][e];
                         ss += q[j][e] * q[j][e];
                         if constexpr (BWD) {
-                            sd += gp[j][e] * w.a[s][j][e] * p[j][e];
-                            sd += gq[j][e] * w.b[s][j][e] * q[j][e];
+                            sd += gp[j][e] * w.a[S][j][e] * p[j][e];
+                            sd += gq[j][e] * w.b[S][j][e] * q[j][e];
                         }
                     }
                 for (int m = 1; m < lanes; m <<= 1) {
@@ -199,22 +197,20 @@ __global__ void __launch_bounds__(256) kda_qk_norm_kernel(QkNormArgs a, int lane
                     if constexpr (BWD) sd += __shfl_xor(sd, m, 64);
                 }
                 // lanes of no head and rows of no token add nothing, also where eps is 0
-                const float r = h < heads && real ? __builtin_amdgcn_rsqf(ss * inv_d + a.eps) + poison : 0.f;
+                const float r = mine && real ? __builtin_amdgcn_rsqf(ss * inv_d + a.eps) + poison : 0.f;
                 const float back = BWD ? sd * inv_d * r * r : 0.f;
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         if constexpr (BWD) {
-                            dw.a[0][j][e] += s ? 0.f : gp[j][e] * (p[j][e] * r);
-                            dw.b[0][j][e] += s ? 0.f : gq[j][e] * (q[j][e] * r);
-                            dw.a[1][j][e] += s ? gp[j][e] * (p[j][e] * r) : 0.f;
-                            dw.b[1][j][e] += s ? gq[j][e] * (q[j][e] * r) : 0.f;
-                            p[j][e] = r * (gp[j][e] * w.a[s][j][e] - p[j][e] * back);
-                            q[j][e] = r * (gq[j][e] * w.b[s][j][e] - q[j][e] * back);
+                            dw.a[S][j][e] += gp[j][e] * (p[j][e] * r);
+                            dw.b[S][j][e] += gq[j][e] * (q[j][e] * r);
+                            p[j][e] = r * (gp[j][e] * w.a[S][j][e] - p[j][e] * back);
+                            q[j][e] = r * (gq[j][e] * w.b[S][j][e] - q[j][e] * back);
                         } else {
-                            p[j][e] = p[j][e] * r * w.a[s][j][e];
-                            q[j][e] = q[j][e] * r * w.b[s][j][e];
+                            p[j][e] = p[j][e] * r * w.a[S][j][e];
+                            q[j][e] = q[j][e] * r * w.b[S][j][e];
                         }
                     }
                 if constexpr (!BWD) angles.template turn<1>(p, q);
@@ -224,9 +220,15 @@ __global__ void __launch_bounds__(256) kda_qk_norm_kernel(QkNormArgs a, int lane
 #pragma unroll
                         for (int e = 0; e < V; ++e) p[j][e] = q[j][e] = 0.f;
                 }
-                if (h < heads)
-                    H::store(s ? (T *)a.k_out + t * a.ko_stride + (int64_t)(h - a.Hq) * a.D
-                               : (T *)a.q_out + t * a.qo_stride + (int64_t)h * a.D, p, q, ch);
+                if (mine)
+                    H::store((S ? (T *)a.k_out + t * a.ko_stride : (T *)a.q_out + t * a.qo_stride) + (int64_t)h * a.D, p, q, ch);
+            };
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int g = g0 + i * parts;
+                if (g >= groups) break;
+                if (g < q_groups) work(Const<0>{}, x[i], gy[BWD ? i : 0], g * per_wave + sub);
+                else work(Const<1>{}, x[i], gy[BWD ? i : 0], (g - q_groups) * per_wave + sub);
             }
         }
     }
@@ -278,7 +280,7 @@ int head_lanes(int D, int V)
 }
 
 constexpr int64_t FILL = 4096;           // waves that fill the device
-constexpr int64_t BWD_BLOCKS = 1024;     // rows of the workspace
+constexpr int64_t FWD_BLOCKS = 1024, BWD_BLOCKS = 1024;     // rows of the workspace
 
 Shape shape_of(const QkNormArgs &a, bool bwd)
 {
@@ -289,12 +291,12 @@ Shape shape_of(const QkNormArgs &a, bool bwd)
              whole(a.qo_stride, a.q_out) && whole(a.ko_stride, a.k_out) &&
              (!bwd || (whole(a.gq_stride, a.gq) && whole(a.gk_stride, a.gk)));
     s.lanes = head_lanes(a.D, s.wide ? V : 1);
-    const int per_wave = 64 / s.lanes, groups = (a.Hq + a.Hk + per_wave - 1) / per_wave;
+    const int per_wave = 64 / s.lanes, groups = (a.Hq + per_wave - 1) / per_wave + (a.Hk + per_wave - 1) / per_wave;
     const int64_t want = a.T > 0 ? FILL / a.T : 1;
     s.parts = (int)(want < 1 ? 1 : want > groups ? groups : want);
     const int64_t units = a.T * s.parts;
     s.blocks = (units + 3) / 4;
-    const int64_t most = bwd ? BWD_BLOCKS : (int64_t)1 << 20;
+    const int64_t most = bwd ? BWD_BLOCKS : FWD_BLOCKS;
     if (s.blocks > most) s.blocks = most;
     return s;
 }
