@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
         // The value scales' reference is a power of two, 2^level, above the largest met.
-        float top = -__builtin_inff(), sum = 0.f, level = -__builtin_inff();
+        float top = -__builtin_inff(), sum = 0.f, level = -__builtin_inff(), spoiled = 0.f;
 
         const int *table = a.table + (int64_t)b * a.per;
         Loader<D, WAVES, INT8> next;
@@ -304,15 +304,10 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
                 }
                 sum = __builtin_fmaf(total, fast_exp2(-up), sum);
             }
-            if (broken) {                        // NaN for the places seen
-                asm volatile("");                // a branch, not selects for every tile
+            if (broken) {                        // a value scale that is not finite: NaN for the rows that see its tokens
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int seen = broken >> g & 1 ? limit - (t0 + 16 * g + 8 * half) : 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[g >> 1][8 * (g & 1) + i] = i < seen ? __builtin_nanf("") : x[g >> 1][8 * (g & 1) + i];
-                }
+                for (int g = 0; g < 4; ++g)
+                    spoiled = broken >> g & 1 && limit > t0 + 16 * g + 8 * half ? __builtin_nanf("") : spoiled;
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -335,7 +330,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
 
         sum = halves_sum(sum);
         const bool whole_row = t_begin == 0 && t_end == tiles;
-        const float f = level == -__builtin_inff() ? 0.f : fast_exp2(level) * VALUE_REST;
+        const float f = (level == -__builtin_inff() ? 0.f : fast_exp2(level) * VALUE_REST) + halves_sum(spoiled);
         float *piece = nullptr;
         if constexpr (LINE) {
             piece = a.ws + (sizeof(Record) / 4) * gridDim.x + (int64_t)(2 * blockIdx.x + (t_begin == 0)) * PIECE<D, ROWS>;
@@ -374,7 +369,7 @@ Shape shape_of(int tokens, int B, int Hq, int Hk, int D, int page, int per, int 
 {
     Shape s;
     const int64_t rows = (int64_t)most * (Hq / Hk), tiles = ((int64_t)per * page + 63) / 64;
-    s.waves = rows <= 64 && D <= 128 ? 2 : 4;
+    s.waves = D == 256 ? 4 : rows <= 64 ? 2 : 4;
     // blocks of all sequences, at most (as the kernel counts them)
     const int64_t blocks = ((int64_t)tokens * (Hq / Hk) / (32 * s.waves) + B) * Hk;
     s.line = blocks < 1024 && line_fits(tiles, (int64_t)tokens * (Hq / Hk), 32 * s.waves, B, Hk);
