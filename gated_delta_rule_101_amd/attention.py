@@ -59,6 +59,15 @@ def _heads(t: torch.Tensor, what: str) -> Tuple[int, int, int, int]:
     return T, H, D, width if stride is None else stride
 
 
+def _gpu(*ts: Optional[torch.Tensor]) -> torch.device:
+    """_device of tensors of which the first is given, sooner where nothing is wrong."""
+    index = ts[0].get_device()
+    for t in ts:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            return _device(*ts)
+    return ts[0].device if index >= 0 else _device(*ts)
+
+
 def _one_device(dev: torch.device, *ts: Optional[torch.Tensor]):
     for t in ts:
         if t is not None and t.device != dev:
@@ -87,7 +96,7 @@ def kda_cache_plan(cached: torch.Tensor, added: torch.Tensor, block_table: torch
     for t, shape, what in ((cached, (B,), "cached"), (added, (B,), "added"), (block_table, (B, per), "block_table"),
                            (free_pages, (free_pages.shape[0],), "free_pages"), (free_count, (1,), "free_count")):
         _shape(t, shape, what, torch.int32)
-    dev = _device(cached, added, block_table, free_pages, free_count)
+    dev = _gpu(cached, added, block_table, free_pages, free_count)
     with _on(dev, stream) as handle:
         # one allocation: the outputs are parts of it
         flat = torch.empty(2 * B + 2 + 2 * tokens, dtype=torch.int32, device=dev)
@@ -236,7 +245,7 @@ def kda_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_co
     _shape(v, k.shape, "v", k.dtype)
     _shape(slots, k.shape[:-2], "slots", torch.int32)
     code = _dtype_code(k)
-    dev = _device(slots, k_codes, v_codes, k_scale, v_scale)
+    dev = _gpu(slots, k_codes, v_codes, k_scale, v_scale)
     _one_device(dev, k, v)
     with _on(dev, stream) as handle:
         st = lib.kda_cache_append(_ptr(k), _ptr(v), _ptr(slots), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
@@ -288,7 +297,7 @@ def kda_cache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.T
     _shape(lse, (N, Hq), "lse", torch.float32)
     most = 1 if q_start is None else N if max_queries is None else int(max_queries)
     code = _dtype_code(q)
-    dev = _device(q, k_codes, v_codes, k_scale, v_scale, block_table, context, q_start, out, lse, workspace)
+    dev = _gpu(q, k_codes, v_codes, k_scale, v_scale, block_table, context, q_start, out, lse, workspace)
     with _on(dev, stream) as handle:
         if out is None:
             out = torch.empty_like(q)

@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(256) kda_cache_plan_kernel(PlanArgs a)
                 } else {
                     id = *entry;
                 }
-                slot_of = id < 0 ? -1 : id * a.page + in;
+                const int64_t place = (int64_t)id * a.page + in;
+                slot_of = place < 0 || place > 0x7fffffff ? -1 : (int)place;
             }
             a.positions[row] = pos;
             a.slots[row] = slot_of;

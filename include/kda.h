@@ -638,7 +638,8 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const float *weig
  *      k_codes [pages, Hk, page, D]   one byte each
  *      v_codes [pages, Hk, D, page]   one byte each, tokens innermost
  *      k_scale, v_scale [pages, Hk]   float32
- *    A value is its code (kda_code_t) times the scale of its page and head.
+ *    A value is its code (kda_code_t) times the scale of its page and head,
+ *    which is not negative.
  *    page (tokens a page) is 16, 32, 64 or 128, D is 64, 128 or 256
  *    (KDA_ERR_UNSUPPORTED otherwise); pages * page below 2^31, the codes below
  *    2^40 bytes.  A fresh cache needs no initialisation.
@@ -679,8 +680,8 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const float *weig
  * length, or more pages than the table holds, which takes none) keeps its rows,
  * but its context is 0, its rows' positions and slots are -1, and its table is
  * left as it is.  Rows behind the last request have positions and slots -1;
- * q_start does not pass `tokens`.  A cached token whose entry is negative has
- * slot -1.  Pages' numbers times page have to stay below 2^31.
+ * q_start does not pass `tokens`.  A row whose page has a number that is negative,
+ * or makes a slot of 2^31 or more, has slot -1.
  */
 kda_status_t kda_cache_plan(const int *cached, const int *added, int *block_table, const int *free_pages,
                             const int *free_count, int *q_start, int *context, int *positions, int *slots,
@@ -772,9 +773,14 @@ kda_status_t kda_cache_append(const void *k, const void *v, const int *slots, vo
  *   max_queries  rows of the longest sequence, as far as the host knows: chooses
  *           the kernel, and the results are right for any value
  *
- * Pages whose table entry names none of the cache (such as -1, for a page that
- * was given up) are not seen.  A row that sees no place has out 0 and lse -inf.
- * Rows of no sequence are left as they were.  tokens * Hq below 2^31.
+ * A page and head whose scale is not finite makes the rows that see its tokens
+ * NaN.  Pages whose table entry names none of the cache (such as -1, for a page
+ * that was given up) are not seen.  A row that sees no place has out 0 and lse -inf.
+ * Rows of no sequence are left as they were.
+ *
+ * tokens * Hq below 2^31.  The units of work (64 places of the table x key head x
+ * block of 16 or more query rows of a head's group) of a call whose sequences have
+ * few rows have to stay below 2^31 too (KDA_ERR_UNSUPPORTED beyond).
  */
 size_t kda_cache_attention_workspace_bytes(int tokens, int B, int Hq, int Hk, int D, int page, int max_pages,
                                            int max_queries);

@@ -625,6 +625,78 @@ def test_a_captured_step_replays(kda):
         assert torch.equal(two[0].table, two[1].table) and torch.equal(two[0].count, two[1].count)
 
 
+@pytest.mark.parametrize("new,B", [(1, 3), (40, 2), (700, 2), (2500, 4)])
+def test_captured_attention_replays(kda, new, B):
+    """Each kernel in a graph of its own: one query, lines of 64 and of 128 rows, a workgroup a block of rows."""
+    q, c, table, context, starts = layer([new + 900 - 300 * b for b in range(B)], [new] * B, 16 if new == 2500 else 4, 2, 64,
+                                         32, E4M3, BF16, 45)
+    d = [t.cuda() for t in c]
+    q, t, n, s = q.cuda(), table.cuda(), context.cuda(), starts.cuda()
+    kw = dict(q_start=s, max_queries=new, want_lse=True)
+    want = kda.kda_cache_attention(q, *d, t, n, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        kda.kda_cache_attention(q, *d, t, n, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = kda.kda_cache_attention(q, *d, t, n, **kw)
+    for i in range(4):
+        o.fill_(7)
+        lse.fill_(7)
+        graph.replay()
+        other = kda.kda_cache_attention(q, *d, t, n, **kw)
+        torch.cuda.synchronize()
+        for x, y, z in zip((o, lse), want, other):
+            assert torch.equal(x, y) and torch.equal(z, y), i
+    n.copy_(n - 50)                                           # the graph reads the lengths of the time
+    graph.replay()
+    want = kda.kda_cache_attention(q, *d, t, n, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_captured_gradients_replay(kda):
+    q, k, wq, wk, pos, table = qk_inputs(500, 4, 2, 128, 64, BF16, True, 46)
+    g = gen(47)
+    dq, dk = (torch.randn(t.shape, generator=g).to(BF16).cuda() for t in (q, k))
+    args = (dq, dk, q, k, wq, wk)
+    kw = dict(positions=pos, rotary=table)
+    kda.kda_qk_norm_rope_bwd(*args, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = kda.kda_qk_norm_rope_bwd(*args, **kw)
+    for i in range(4):
+        dq.copy_(torch.randn(q.shape, generator=g))
+        graph.replay()
+        want = kda.kda_qk_norm_rope_bwd(*args, **kw)
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(torch.nan_to_num(r[n].float()), torch.nan_to_num(want[n].float())), (i, n)
+
+
+def test_queries_that_are_not_finite(kda):
+    """A row that is not finite is NaN; the rows beside it, of the same products, are not."""
+    for new in (1, 8, 100):
+        q, c, table, context, starts = layer([300, 200], [new, new], 4, 2, 64, 32, INT8, BF16, 48)
+        clean = check_attention(kda, q, c, table, context, starts, "clean", most=new)
+        bad = q.clone()
+        bad[0, 0, 3], bad[new, 3, 60], bad[2 * new - 1, 1, 0] = math.nan, math.inf, -math.inf
+        o, lse = kda.kda_cache_attention(bad.cuda(), *[t.cuda() for t in c], table.cuda(), context.cuda(),
+                                         q_start=starts.cuda(), max_queries=new, want_lse=True)
+        hit = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+        hit[0, 0] = hit[new, 3] = hit[2 * new - 1, 1] = True
+        assert torch.isnan(o[hit]).all()
+        assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
+def test_plan_pages_of_large_numbers(kda):
+    t, p = run_plan(kda, [16, 0], [1, 1], [[2 ** 31 - 1, -1], [-1, -1]], [2 ** 27 - 1, 2 ** 30], 2, 16, 2)
+    assert p["slots"].tolist() == [-1, (2 ** 27 - 1) * 16] and t.tolist() == [[2 ** 31 - 1, 2 ** 30], [2 ** 27 - 1, -1]]
+
+
 def test_other_streams_and_repeatable(kda):
     """On a stream of the caller's, twice, bit for bit; two calls at once with workspaces of their own."""
     q, c, table, context, starts = layer([3000, 900, 64], [3, 1, 2], 8, 2, 128, 64, E4M3, BF16, 44)
