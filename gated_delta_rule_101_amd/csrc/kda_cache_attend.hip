@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
         const unsigned u = line.u;
         if (u >= (unsigned)tiles * blocks * a.Hk) {
             line.u = 0;
-            ++line.b;
+            if (++line.b >= a.B) break;         // row starts that descend may count more units than there are
             continue;
         }
         const int b = line.b;

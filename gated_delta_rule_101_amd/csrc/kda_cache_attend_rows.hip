@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
             const int blocks = blocks_of(s, G, ROWS);
             if ((unsigned)line.u >= (unsigned)tiles * blocks * a.Hk) {
                 line.u = 0;
-                ++line.b;
+                if (++line.b >= a.B) break;         // row starts that descend may count more units than there are
                 continue;
             }
             b = line.b;

@@ -29,7 +29,7 @@ namespace {
 // beyond the head's end; angle indexes for the two.
 template <int V, int NV, bool NEIGH> struct Channels {
     int a[NV], b[NV];
-    bool turned[NV];
+    int turned[NV];
     __device__ __forceinline__ Channels(int l, int lanes, int D, int R)
     {
 #pragma unroll
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(256) kda_qk_norm_kernel(QkNormArgs a, int lane
 }
 
 struct Shape {
-    bool wide;
+    int vec;                             // V
     int lanes, parts;
     int64_t blocks;
 };
@@ -287,12 +287,17 @@ constexpr int64_t FWD_BLOCKS = 1024, BWD_BLOCKS = 1024;     // rows of the works
 Shape shape_of(const QkNormArgs &a, bool bwd)
 {
     Shape s;
-    const int V = a.bf16 ? 8 : 4;
-    const auto whole = [&](int64_t stride, const void *p) { return stride % V == 0 && ((uintptr_t)p & 15) == 0; };
-    s.wide = a.D % (2 * V) == 0 && a.R % (2 * V) == 0 && whole(a.q_stride, a.q) && whole(a.k_stride, a.k) &&
-             whole(a.qo_stride, a.q_out) && whole(a.ko_stride, a.k_out) &&
-             (!bwd || (whole(a.gq_stride, a.gq) && whole(a.gk_stride, a.gk)));
-    s.lanes = head_lanes(a.D, s.wide ? V : 1);
+    // The widest V in which blocks are whole and rows aligned: 16 bytes, 8 of
+    // bfloat16 (16384 tokens of 40 heads x 120: 198 us by elements, 88 so), or elements.
+    const size_t e = a.bf16 ? 2 : 4;
+    const auto fits = [&](int V) {
+        const auto whole = [&](int64_t stride, const void *p) { return stride % V == 0 && ((uintptr_t)p & (V * e - 1)) == 0; };
+        return a.D % (2 * V) == 0 && a.R % (2 * V) == 0 && whole(a.q_stride, a.q) && whole(a.k_stride, a.k) &&
+               whole(a.qo_stride, a.q_out) && whole(a.ko_stride, a.k_out) &&
+               (!bwd || (whole(a.gq_stride, a.gq) && whole(a.gk_stride, a.gk)));
+    };
+    s.vec = a.bf16 && fits(8) ? 8 : fits(4) ? 4 : 1;
+    s.lanes = head_lanes(a.D, s.vec);
     const int per_wave = 64 / s.lanes, groups = (a.Hq + per_wave - 1) / per_wave + (a.Hk + per_wave - 1) / per_wave;
     const int64_t want = a.T > 0 ? FILL / a.T : 1;
     s.parts = (int)(want < 1 ? 1 : want > groups ? groups : want);
@@ -315,7 +320,9 @@ hipError_t launch(const QkNormArgs &a, const Shape &s, hipStream_t stream)
 }
 template <typename T, bool BWD> hipError_t launch_v(const QkNormArgs &a, const Shape &s, hipStream_t stream)
 {
-    if (s.wide) return launch<T, WIDE<T>, 1, BWD>(a, s, stream);
+    if (s.vec == WIDE<T>) return launch<T, WIDE<T>, 1, BWD>(a, s, stream);
+    if constexpr (sizeof(T) == 2)
+        if (s.vec == 4) return launch<T, 4, 1, BWD>(a, s, stream);
     if (a.D <= 128) return launch<T, 1, 1, BWD>(a, s, stream);
     return a.D <= 256 ? launch<T, 1, 2, BWD>(a, s, stream) : launch<T, 1, 4, BWD>(a, s, stream);
 }

@@ -111,7 +111,8 @@ QK = [  # T, Hq, Hk, D, R, neighbours, dtype, fused
     (9, 3, 2, 202, 100, False, BF16, True), (9, 2, 2, 510, 254, True, F32, True), (5, 2, 1, 512, 512, False, BF16, True),
     (5, 2, 1, 512, 512, True, F32, False), (40, 4, 4, 128, 0, False, BF16, True), (2000, 9, 3, 64, 16, True, BF16, True),
     (3, 6, 0, 128, 128, False, BF16, False), (3, 0, 2, 64, 64, False, F32, False), (5000, 2, 1, 128, 128, False, F32, True),
-    (1, 1, 1, 62, 30, True, BF16, True)]
+    (1, 1, 1, 62, 30, True, BF16, True), (50, 5, 2, 120, 120, False, BF16, True), (31, 3, 2, 72, 24, True, BF16, True),
+    (9, 2, 1, 504, 8, False, BF16, False), (700, 3, 2, 40, 0, False, BF16, True)]
 
 
 def qk_inputs(T, Hq, Hk, D, R, dtype, fused, seed):
@@ -690,6 +691,24 @@ def test_queries_that_are_not_finite(kda):
         hit[0, 0] = hit[new, 3] = hit[2 * new - 1, 1] = True
         assert torch.isnan(o[hit]).all()
         assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
+@pytest.mark.parametrize("most", [1, 12, 200])
+def test_row_starts_of_any_kind_stay_inside(kda, most):
+    """Row starts that descend, lengths and tables of any numbers: rows beside the call's stay as they are, and the
+    next call is right."""
+    q, c, table, context, starts = layer([300, 200, 100], [most] * 3, 4, 2, 64, 32, E4M3, BF16, 49)
+    d, N = [t.cuda() for t in c], q.shape[0]
+    room = torch.full((N + 64, 4, 64), 7.0, dtype=BF16, device="cuda")
+    g = gen(50)
+    for i in range(6):
+        bad = torch.randint(-50, N + 50, (4,), generator=g).int() if i else torch.tensor([0, N, 0, N]).int()
+        n = torch.randint(-100, 2000, (3,), generator=g).int()
+        t = torch.randint(-3, c[0].shape[0] + 3, table.shape, generator=g).int()
+        kda.kda_cache_attention(q.cuda(), *d, t.cuda(), n.cuda(), q_start=bad.cuda(), max_queries=most, out=room[32:N + 32])
+    torch.cuda.synchronize()
+    assert (room[:32] == 7).all() and (room[N + 32:] == 7).all()
+    check_attention(kda, q, c, table, context, starts, "after", most=most)
 
 
 def test_plan_pages_of_large_numbers(kda):
