@@ -14,7 +14,7 @@
 // exchanges between lanes.
 //
 // Work is counted in units: 64 tokens of one sequence, key head and block of
-// 16 NR queries.  All units of the call lie on one line which is cut into equal
+// 16 rows (query, head of the group).  All units of the call lie on one line which is cut into equal
 // shares, one a workgroup, whatever the lengths are; its waves take turns at a
 // share's units.  A share that ends inside a row of units leaves its running
 // maximum, sum and output in the workspace, and a second launch joins them.
@@ -35,10 +35,10 @@
 namespace kda {
 namespace {
 
-template <int D, int NR, bool BF, bool INT8>
-__global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_attend_kernel(AttendArgs a, int shift)
+template <int D, bool BF, bool INT8>
+__global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel(AttendArgs a, int shift)
 {
-    constexpr int SPLIT = BF ? 1 : 2, KS = D / 32, DT = D / 16, ROWS = 16 * NR;
+    constexpr int SPLIT = BF ? 1 : 2, KS = D / 32, DT = D / 16, ROWS = 16;
     typedef typename Store<BF>::type T;
     __shared__ int part[4];
     __shared__ __align__(16) float merge[4][16][D + 4];
@@ -74,31 +74,21 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
         int pk, pv;
         look_up(t_begin + wave, pk, pv);
 
-        // queries: lane m is row r0 + 16 n + m
-        f16x8 q[SPLIT][NR][KS];
-        float factor[NR];
-        int limit[NR];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            const int r = 16 * n + m, x = r0 + min(r, active - 1), i = x / G, g = x - i * G;
-            const T *p = (const T *)a.q + ((int64_t)(s.first + i) * a.Hq + h * G + g) * D;
-            limit[n] = r < active ? s.context - s.queries + i + 1 : 0x7fffffff;
-            factor[n] = load_query<T, D, SPLIT, KS>(p, r < active, quarter, [&](int x, int k) -> f16x8 & { return q[x][n][k]; }) *
-                        a.scale * LOG2E;
-        }
+        // queries: lane m is row r0 + m
+        f16x8 q[SPLIT][KS];
+        const int at_row = r0 + min(m, active - 1), qi = at_row / G, qg = at_row - qi * G;
+        const int limit = m < active ? s.context - s.queries + qi + 1 : 0x7fffffff;
+        const float factor = load_query<T, D, SPLIT, KS>((const T *)a.q + ((int64_t)(s.first + qi) * a.Hq + h * G + qg) * D,
+                                                         m < active, quarter,
+                                                         [&](int x, int k) -> f16x8 & { return q[x][k]; }) * a.scale * LOG2E;
         // tiles with every place seen by every row need no mask
         const int whole = min(s.context - s.queries + r0 / G + 1, s.context);
         const int furthest = min(s.context, s.context - s.queries + (r0 + active - 1) / G + 1);
 
-        f32x4 o[NR][DT];
-        float top[NR], sum[NR], level = -__builtin_inff();
+        f32x4 o[DT];
+        float top = -__builtin_inff(), sum = 0.f, level = -__builtin_inff();
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            top[n] = -__builtin_inff();
-            sum[n] = 0.f;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
+        for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
 
         for (int t = t_begin + wave; t < t_end; t += 4) {
             const int t0 = t * 64;
@@ -133,63 +123,56 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
                 const float now = __builtin_ceilf(quarters_max(lv)) + 1.f, f = fast_exp2(level - now);
                 level = now;
 #pragma unroll
-                for (int n = 0; n < NR; ++n)
+                for (int d = 0; d < DT; ++d)
 #pragma unroll
-                    for (int d = 0; d < DT; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[n][d][i] *= f;
+                    for (int i = 0; i < 4; ++i) o[d][i] *= f;
             }
             const float up = ratio_level(lv, level), down = fast_exp2(-up);
-            f16x8 w[SPLIT][NR][2];
+            f16x8 w[SPLIT][2];
+            const float c = factor * (gone ? 0.f : ks);
+            const int seen = gone ? 0 : min(limit, s.context) - tb;     // of this lane's 16 tokens
+            float v[16], best = -__builtin_inff();
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                if (NR > 1) __builtin_amdgcn_sched_barrier(0);     // one row tile's scores at a time, for the registers
-                const float c = factor[n] * (gone ? 0.f : ks);
-                const int seen = gone ? 0 : min(limit[n], s.context) - tb;     // of this lane's 16 tokens
-                float v[16], best = -__builtin_inff();
+            for (int i = 0; i < 4; ++i) {
+                f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < KS; ++k)
 #pragma unroll
-                    for (int k = 0; k < KS; ++k)
+                    for (int p = 0; p < SPLIT; ++p)
+                        x = __builtin_amdgcn_mfma_f32_16x16x32_f16(ka[i][k], q[p][k], x, 0, 0, 0);
 #pragma unroll
-                        for (int p = 0; p < SPLIT; ++p)
-                            x = __builtin_amdgcn_mfma_f32_16x16x32_f16(ka[i][k], q[p][n][k], x, 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j] * c;
-                }
-                if (masked) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = i < seen ? v[i] : -__builtin_inff();
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) best = fmaxf(best, v[i]);
-                best = quarters_max(best);
-                if (__any(best > top[n] + SLACK)) {
-                    const float now = fmaxf(top[n], best), fade = now == -__builtin_inff() ? 1.f : fast_exp2(top[n] - now);
-                    top[n] = now;
-                    sum[n] *= fade;
-#pragma unroll
-                    for (int d = 0; d < DT; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[n][d][i] *= fade;
-                }
-                const float offset = up - (top[n] == -__builtin_inff() ? 0.f : top[n]);
-                float total = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] = fast_exp2(v[i] + offset);
-                    total += v[i];
-                }
-                sum[n] = __builtin_fmaf(total, down, sum[n]);
-                if (__any(broken)) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = broken && i < seen ? __builtin_nanf("") : v[i];
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) split_f16<SPLIT>(v + 8 * k, [&](int p) -> f16x8 & { return w[p][n][k]; });
+                for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j] * c;
             }
-            if (NR > 1) __builtin_amdgcn_sched_barrier(0);
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = i < seen ? v[i] : -__builtin_inff();
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) best = fmaxf(best, v[i]);
+            best = quarters_max(best);
+            if (__any(best > top + SLACK)) {
+                const float now = fmaxf(top, best), fade = now == -__builtin_inff() ? 1.f : fast_exp2(top - now);
+                top = now;
+                sum *= fade;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[d][i] *= fade;
+            }
+            const float offset = up - (top == -__builtin_inff() ? 0.f : top);
+            float total = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                v[i] = fast_exp2(v[i] + offset);
+                total += v[i];
+            }
+            sum = __builtin_fmaf(total, down, sum);
+            if (__any(broken)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = broken && i < seen ? __builtin_nanf("") : v[i];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) split_f16<SPLIT>(v + 8 * k, [&](int p) -> f16x8 & { return w[p][k]; });
             if (masked && !INT8) {
                 // weights of places that hold no token are zero; their codes must not be NaN
                 const int there = gone ? 0 : s.context - tb;
@@ -200,24 +183,19 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
             for (int d = 0; d < DT; ++d) {
                 const f16x8 lo = codes_f16<INT8>(vr[d].x, vr[d].y), hi = codes_f16<INT8>(vr[d].z, vr[d].w);
 #pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int p = 0; p < SPLIT; ++p) {
-                        o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, w[p][n][0], o[n][d], 0, 0, 0);
-                        o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, w[p][n][1], o[n][d], 0, 0, 0);
-                    }
+                for (int p = 0; p < SPLIT; ++p) {
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, w[p][0], o[d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, w[p][1], o[d], 0, 0, 0);
+                }
             }
         }
 
         // The four waves' parts meet: scaled to the common maximum and reference.
         if (lane == 0) ref[wave] = level == -__builtin_inff() ? 0.f : fast_exp2(level) * VALUE_REST;
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            sum[n] = quarters_sum(sum[n]);
-            if (quarter == 0) {
-                stat[wave][0][16 * n + m] = top[n];
-                stat[wave][1][16 * n + m] = sum[n];
-            }
+        sum = quarters_sum(sum);
+        if (quarter == 0) {
+            stat[wave][0][m] = top;
+            stat[wave][1][m] = sum;
         }
         const bool whole_row = t_begin == 0 && t_end == tiles;
         float *piece = pieces + (int64_t)(2 * blockIdx.x + (t_begin == 0)) * PIECE<D, ROWS>;
@@ -225,39 +203,36 @@ __global__ void __launch_bounds__(256, NR == 1 && D <= 128 ? 2 : 1) kda_cache_at
         line.u += t_end - t_begin;
         line.left -= t_end - t_begin;
         line.at += t_end - t_begin;
+        __syncthreads();
+        float best = -__builtin_inff();
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            __syncthreads();
-            float best = -__builtin_inff();
+        for (int v = 0; v < 4; ++v) best = fmaxf(best, stat[v][0][m]);
+        // in units of the values: times the reference, which is 0 where every value was
+        const float f = (best == -__builtin_inff() ? 1.f : fast_exp2(top - best)) * ref[wave];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) best = fmaxf(best, stat[v][0][16 * n + m]);
-            // in units of the values: times the reference, which is 0 where every value was
-            const float f = (best == -__builtin_inff() ? 1.f : fast_exp2(top[n] - best)) * ref[wave];
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
+            for (int i = 0; i < 4; ++i) merge[wave][m][16 * d + 4 * quarter + i] = o[d][i] * f;
+        __syncthreads();
+        for (int e = threadIdx.x; e < 16 * (D / 4); e += 256) {
+            const int rr = e / (D / 4), d = 4 * (e % (D / 4));
+            if (rr >= active) continue;
+            float hi = -__builtin_inff(), l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) merge[wave][m][16 * d + 4 * quarter + i] = o[n][d][i] * f;
-            __syncthreads();
-            for (int e = threadIdx.x; e < 16 * (D / 4); e += 256) {
-                const int r = e / (D / 4), d = 4 * (e % (D / 4)), rr = 16 * n + r;
-                if (rr >= active) continue;
-                float hi = -__builtin_inff(), l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int v = 0; v < 4; ++v) hi = fmaxf(hi, stat[v][0][rr]);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) hi = fmaxf(hi, stat[v][0][rr]);
+            for (int v = 0; v < 4; ++v) {
+                l += stat[v][1][rr] * (hi == -__builtin_inff() ? 1.f : fast_exp2(stat[v][0][rr] - hi));
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    l += stat[v][1][rr] * (hi == -__builtin_inff() ? 1.f : fast_exp2(stat[v][0][rr] - hi));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] += merge[v][r][d + i];
-                }
-                if (whole_row) {
-                    write_row<T>(a, s, h, G, r0 + rr, d, D, y, hi, l);
-                } else {
-                    *reinterpret_cast<float4 *>(piece + rr * D + d) = make_float4(y[0], y[1], y[2], y[3]);
-                    if (d == 0) {
-                        piece[ROWS * D + rr] = hi;
-                        piece[ROWS * D + ROWS + rr] = l;
-                    }
+                for (int i = 0; i < 4; ++i) y[i] += merge[v][rr][d + i];
+            }
+            if (whole_row) {
+                write_row<T>(a, s, h, G, r0 + rr, d, D, y, hi, l);
+            } else {
+                *reinterpret_cast<float4 *>(piece + rr * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+                if (d == 0) {
+                    piece[ROWS * D + rr] = hi;
+                    piece[ROWS * D + ROWS + rr] = l;
                 }
             }
         }
@@ -336,32 +311,31 @@ __global__ void __launch_bounds__(256) kda_cache_attend_join_kernel(AttendArgs a
     }
 }
 
-// Query blocks of 16 NR rows: 16 or, up to 128 channels, 32; with more, the
-// queries, the outputs and a tile's keys and values do not fit the registers,
-// and the kernel whose waves share them through LDS takes over.  Not for
-// float32 rows of 256 channels, which do not fit there either.
-int block_rows(int64_t rows) { return rows <= 16 ? 1 : 2; }
-bool is_few(int D, bool bf16, int64_t rows) { return D < 256 ? rows <= 32 : rows <= 16 || !bf16; }
-
-template <int D, int NR, bool BF, bool INT8> hipError_t launch(const AttendArgs &a, int n, hipStream_t stream)
+// Which kernel: this one for up to 16 rows of a sequence and key head, and, as
+// blocks of 16, for up to 64 while the line is short enough that latency counts
+// (at most FEW units): its waves keep more bytes in flight.  Beyond, reading the
+// cache once for all rows wins.  32 / 8 heads x 128, 4096 to 8192 tokens, e4m3, us
+// here and there: 4 queries of 64 sequences 170 / 202, 8 of them 308 / 194; of 4
+// sequences 8 queries 32 / 44, 16 queries 39 / 57.  Not for float32 rows of 256
+// channels, which do not fit the other's registers.
+constexpr int64_t FEW = 16384;
+int64_t units_of(int B, int Hk, int64_t tiles, int64_t rows) { return (int64_t)B * Hk * (tiles > 0 ? tiles : 1) * ((rows + 15) / 16); }
+bool is_few(int D, bool bf16, int64_t rows, int64_t units)
 {
-    hipLaunchKernelGGL((kda_cache_attend_kernel<D, NR, BF, INT8>), dim3(n), dim3(256), 0, stream, a, __builtin_ctz(a.page));
-    const hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : launch_attend_join<16 * NR>(a, n, a.most * (a.Hq / a.Hk), stream);
+    return rows <= 16 || (D == 256 && !bf16) || (rows <= 64 && units <= FEW);
 }
-int64_t units_of(int B, int Hk, int64_t tiles, int D, int64_t rows)
+
+template <int D, bool BF, bool INT8> hipError_t launch(const AttendArgs &a, int n, hipStream_t stream)
 {
-    const int64_t block = 16 * (D == 256 ? 1 : block_rows(rows));
-    return (int64_t)B * Hk * (tiles > 0 ? tiles : 1) * ((rows + block - 1) / block);
+    hipLaunchKernelGGL((kda_cache_attend_kernel<D, BF, INT8>), dim3(n), dim3(256), 0, stream, a, __builtin_ctz(a.page));
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_attend_join<16>(a, n, a.most * (a.Hq / a.Hk), stream);
 }
 template <int D, bool BF, bool INT8> hipError_t launch_rows(const AttendArgs &a, hipStream_t s)
 {
     const int64_t rows = (int64_t)a.most * (a.Hq / a.Hk), tiles = ((int64_t)a.per * a.page + 63) / 64;
-    if (!line_fits(tiles, (int64_t)a.tokens * (a.Hq / a.Hk), D <= 128 ? 16 * block_rows(rows) : 16, a.B, a.Hk)) return hipErrorNotSupported;
-    const int n = shares(units_of(a.B, a.Hk, tiles, D, rows), 512);
-    if constexpr (D <= 128)
-        if (block_rows(rows) == 2) return launch<D, 2, BF, INT8>(a, n, s);
-    return launch<D, 1, BF, INT8>(a, n, s);
+    if (!line_fits(tiles, (int64_t)a.tokens * (a.Hq / a.Hk), 16, a.B, a.Hk)) return hipErrorNotSupported;
+    return launch<D, BF, INT8>(a, shares(units_of(a.B, a.Hk, tiles, rows), 512), s);
 }
 template <bool BF, bool INT8> hipError_t launch_d(const AttendArgs &a, hipStream_t s)
 {
@@ -391,15 +365,12 @@ template hipError_t launch_attend_join<128>(const AttendArgs &, int, int, hipStr
 
 int64_t cache_attend_workspace_floats(int tokens, int B, int Hq, int Hk, int D, int page, int per, int most)
 {
-    const int64_t rows = (int64_t)most * (Hq / Hk), tiles = ((int64_t)per * page + 63) / 64;
+    const int64_t rows = (int64_t)most * (Hq / Hk), tiles = ((int64_t)per * page + 63) / 64, units = units_of(B, Hk, tiles, rows);
     int64_t need = 0;
     for (const bool bf16 : {false, true}) {          // the size does not depend on the type
         int64_t x;
-        if (is_few(D, bf16, rows))
-            x = shares(units_of(B, Hk, tiles, D, rows), 512) *
-                (int64_t)(sizeof(Record) / 4 + 2 * 16 * (D == 256 ? 1 : block_rows(rows)) * (D + 2));
-        else
-            x = attend_rows_workspace_floats(tokens, B, Hq, Hk, D, page, per, most);
+        if (is_few(D, bf16, rows, units)) x = shares(units, 512) * (int64_t)(sizeof(Record) / 4 + 2 * 16 * (D + 2));
+        else x = attend_rows_workspace_floats(tokens, B, Hq, Hk, D, page, per, most);
         need = x > need ? x : need;
     }
     return need;
@@ -407,7 +378,8 @@ int64_t cache_attend_workspace_floats(int tokens, int B, int Hq, int Hk, int D, 
 
 hipError_t launch_cache_attend(const AttendArgs &a, hipStream_t s)
 {
-    if (!is_few(a.D, a.bf16, (int64_t)a.most * (a.Hq / a.Hk))) return launch_attend_rows(a, s);
+    const int64_t rows = (int64_t)a.most * (a.Hq / a.Hk), tiles = ((int64_t)a.per * a.page + 63) / 64;
+    if (!is_few(a.D, a.bf16, rows, units_of(a.B, a.Hk, tiles, rows))) return launch_attend_rows(a, s);
     if (a.bf16) return a.int8 ? launch_d<true, true>(a, s) : launch_d<true, false>(a, s);
     return a.int8 ? launch_d<false, true>(a, s) : launch_d<false, false>(a, s);
 }

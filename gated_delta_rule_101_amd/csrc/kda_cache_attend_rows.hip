@@ -376,7 +376,12 @@ Shape shape_of(int tokens, int B, int Hq, int Hk, int D, int page, int per, int 
     s.waves = D == 256 ? 4 : rows <= 64 ? 2 : 4;
     // blocks of all sequences, at most (as the kernel counts them)
     const int64_t blocks = ((int64_t)tokens * (Hq / Hk) / (32 * s.waves) + B) * Hk;
-    s.line = blocks < 1024 && line_fits(tiles, (int64_t)tokens * (Hq / Hk), 32 * s.waves, B, Hk);
+    // A line where blocks are few and the table holds several times the queries: its
+    // rows of units are taken as equally long, so a prompt's causal corner is better
+    // left to the hardware's order (32 / 8 heads x 128, us as a line and by blocks:
+    // 512 new of 512 tokens 36 / 22, 1000 of 1000 46 / 37, twice 1000 of 3000 132 /
+    // 125; 256 of 4096 65 / 118, 512 of 16384 200 / 494, 8 x 500 of 4000 249 / 254).
+    s.line = blocks < 1024 && tiles * 64 >= 4 * (int64_t)most && line_fits(tiles, (int64_t)tokens * (Hq / Hk), 32 * s.waves, B, Hk);
     s.workgroups = s.line ? shares(blocks * (tiles > 0 ? tiles : 1), s.waves == 2 ? 1024 : D == 256 ? 256 : 512) : blocks < ((int64_t)1 << 24) ? (int)blocks : 0;
     return s;
 }
