@@ -17,7 +17,7 @@
 // the weights' gradients add up in registers, meet in LDS and go to the
 // workspace once a workgroup, to be summed by column.
 // 16384 tokens of 32 + 8 heads x 128, bfloat16: forward 68 us, 5.0 TB/s; backward
-// 110 us, 4.6 TB/s, and 5 us of column sums.  256 tokens: 8.7 us.
+// 101 us, 5.1 TB/s, and 5 us of column sums.  256 tokens: 8.7 us.
 #include "kda_attn.h"
 #include "kda_block.h"
 #include "kda_block_device.h"
@@ -282,7 +282,9 @@ int head_lanes(int D, int V)
 }
 
 constexpr int64_t FILL = 4096;           // waves that fill the device
-constexpr int64_t FWD_BLOCKS = 1024, BWD_BLOCKS = 1024;     // rows of the workspace
+// Workgroups: all resident (the backward's two a CU, a row of the workspace each:
+// 101 us at 16384 tokens of 32 + 8 heads x 128, 110 with 1024, 123 with 768).
+constexpr int64_t FWD_BLOCKS = 1024, BWD_BLOCKS = 512;
 
 Shape shape_of(const QkNormArgs &a, bool bwd)
 {
