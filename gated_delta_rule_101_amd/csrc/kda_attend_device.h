@@ -301,12 +301,14 @@ __device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of
     return l;
 }
 
-// Whether a line of blocks of a call's query rows is short enough to be counted.
-// Workgroups for a line of at most `units` units, of which the device holds `most` at once.
+// Whether a line of blocks of `block` query rows is short enough to be counted in
+// 31 bits, where row starts do not descend: a sequence adds less than one block to
+// those of all rows.
 inline bool line_fits(int64_t tiles, int64_t rows, int block, int B, int Hk)
 {
     return (tiles > 0 ? tiles : 1) * Hk * (rows / block + B) < ((int64_t)1 << 31) - 65536;
 }
+// Workgroups for a line of at most `units` units, of which the device holds `most` at once.
 inline int shares(int64_t units, int most) { return units < most && units > 0 ? (int)units : most; }
 
 // The launcher for many query rows a sequence (kda_cache_attend_rows.hip), and
