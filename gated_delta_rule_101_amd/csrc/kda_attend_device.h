@@ -152,11 +152,12 @@ __device__ __forceinline__ float load_row(const T *p, bool real, int half, bool 
 // 2^-28.  Scales that are not finite pass as 0 here: the weights of their tokens
 // are made NaN behind the sum.
 // SLACK: how far scores may be above the base of their exponents.  Weights then
-// reach 2^14 / 2 * 2^SLACK, below float16's 65504.
+// reach 2^14 / 2 * 2^SLACK, below float16's 65504; also while every scale met was
+// zero: an infinite weight would make NaN of the zero codes.
 constexpr float VALUE_REST = 0x1p-14f, SLACK = 2.f;
 __device__ __forceinline__ float ratio_level(float lv, float level)
 {
-    return fmaxf(level == -__builtin_inff() ? 0.f : lv - level, -40.f) + 14.f;
+    return fmaxf(level == -__builtin_inff() ? -1.f : lv - level, -40.f) + 14.f;
 }
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
