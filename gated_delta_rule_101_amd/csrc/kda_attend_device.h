@@ -2,6 +2,7 @@
 // for few queries a sequence and the one for prompts.
 #pragma once
 
+#include "kda_attend_line.h"
 #include "kda_attn.h"
 #include "kda_code8.h"
 
@@ -9,26 +10,11 @@ namespace kda {
 
 __device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
 
-// A sequence of the call: its first query row, queries and tokens in the cache.
-// Held inside the buffers whatever the device's numbers say.
-struct Sequence {
-    int first, queries, context;
-};
 __device__ __forceinline__ Sequence sequence(const AttendArgs &a, int b)
 {
-    Sequence s;
-    if (a.q_start) {
-        const int x = min(max(a.q_start[b], 0), a.tokens), y = min(max(a.q_start[b + 1], x), a.tokens);
-        s.first = x;
-        s.queries = y - x;
-    } else {
-        s.first = b;
-        s.queries = 1;
-    }
     const int64_t room = (int64_t)a.per * a.page;
-    const int c = max(a.context[b], 0);
-    s.context = c < room ? c : (int)room;
-    return s;
+    return a.q_start ? sequence_of(a.q_start[b], a.q_start[b + 1], a.tokens, a.context[b], room)
+                     : sequence_of(b, b + 1, a.tokens, a.context[b], room);
 }
 
 // The page of a token, -1 where there is none: behind the last token, or an
@@ -199,9 +185,7 @@ __device__ __forceinline__ void write_row(const AttendArgs &a, const Sequence &s
 // A value that all lanes hold, as the scalar it is.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// The line of units: 64 tokens of one sequence, key head and block of query rows,
-// sequences, heads, blocks and tokens in that order.  A workgroup's share of it.
-// The line is shorter than 2^31 units (the launchers refuse longer ones).
+// A workgroup's share of the line of units.
 struct Line {
     int b;                                   // sequence of the next unit
     int u;                                   // the unit's place among its sequence's
@@ -210,30 +194,25 @@ struct Line {
     // the workgroup that ends a row of units of which this one has the first, but not all
     __device__ __forceinline__ int last(int tiles) const
     {
-        return single ? blockIdx.x + (unsigned)(tiles - 1) / (unsigned)share : (unsigned)(at + tiles - 1) / (unsigned)share;
+        return single ? blockIdx.x + last_share(0, tiles, share) : last_share(at, tiles, share);
     }
 };
-__device__ __forceinline__ int tiles_of(const Sequence &s) { return max((s.context + 63) / 64, 1); }
-__device__ __forceinline__ int blocks_of(const Sequence &s, int G, int rows)
-{
-    return (int)(((unsigned)s.queries * G + rows - 1) / rows);   // below 2^31 rows, and rows a power of two
-}
-template <int WAVES> __device__ __forceinline__ int workgroup_sum(int x, int *part)
+template <int WAVES> __device__ __forceinline__ unsigned workgroup_sum(unsigned x, unsigned *part)
 {
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
+    for (int m = 1; m < 64; m <<= 1) x = units_add(x, __shfl_xor(x, m, 64));
     if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = x;
     __syncthreads();
     x = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) x += part[w];
+    for (int w = 0; w < WAVES; ++w) x = units_add(x, part[w]);
     __syncthreads();
     return x;
 }
 // `at_least`: a share's least units, where rows of units are that long; short
 // rows stay whole.  part: [WAVES] in LDS.
 template <int WAVES>
-__device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of_block, int at_least, int *part)
+__device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of_block, int at_least, unsigned *part)
 {
     const int lane = threadIdx.x & 63;
     if (a.B == 1) {
@@ -247,50 +226,49 @@ __device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of
             return Line{0, (int)(row * tiles + part_of * share), max(min(left, (int)share), 0), 0, (int)share, true};
         }
     }
-    int units = 0, rows = 0, upto = 0, mine = 0;
+    unsigned units = 0, rows = 0, upto = 0, mine = 0;
     const auto of_lane = [&](int b) {            // units of sequence b, and of those up to it among 64
         mine = 0;
         if (b < a.B) {
             const Sequence s = sequence(a, b);
-            mine = blocks_of(s, G, rows_of_block) * a.Hk;
-            rows += mine;
-            mine *= tiles_of(s);
+            mine = (unsigned)blocks_of(s, G, rows_of_block) * a.Hk;
+            rows = units_add(rows, mine);
+            mine *= tiles_of(s);                 // of one sequence alone: below LINE_LIMIT
         }
         upto = mine;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int y = __shfl_up(upto, d, 64);
-            if (lane >= d) upto += y;
+            const unsigned y = __shfl_up(upto, d, 64);
+            if (lane >= d) upto = units_add(upto, y);
         }
     };
     if (a.B <= 64) {                             // a wave sees them all
         of_lane(lane);
         units = uniform(__shfl(upto, 63, 64));
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) rows += __shfl_xor(rows, m, 64);
+        for (int m = 1; m < 64; m <<= 1) rows = units_add(rows, __shfl_xor(rows, m, 64));
         rows = uniform(rows);
     } else {
         for (int b = threadIdx.x; b < a.B; b += 64 * WAVES) {
             const Sequence s = sequence(a, b);
-            const int r = blocks_of(s, G, rows_of_block) * a.Hk;
-            rows += r;
-            units += r * tiles_of(s);
+            const unsigned r = (unsigned)blocks_of(s, G, rows_of_block) * a.Hk;
+            rows = units_add(rows, r);
+            units = units_add(units, r * tiles_of(s));
         }
         units = uniform(workgroup_sum<WAVES>(units, part));
         rows = uniform(workgroup_sum<WAVES>(rows, part));
     }
     Line l = {0, 0, 0, 0, 1, false};
-    if (units == 0) return l;
-    const unsigned least = min((unsigned)at_least, ((unsigned)units + rows - 1) / (unsigned)rows);
-    l.share = (int)max(((unsigned)units + gridDim.x - 1) / gridDim.x, least);
+    if (units == 0 || units >= LINE_LIMIT) return l;
+    l.share = share_of(units, rows, gridDim.x, at_least);
     const int64_t at = (int64_t)l.share * blockIdx.x;
     if (at >= units) return l;
     l.at = (int)at;
-    l.left = min(l.share, units - l.at);
-    int before = 0;
+    l.left = min(l.share, (int)units - l.at);
+    unsigned before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
         if (a.B > 64) of_lane(b0 + lane);
-        const uint64_t past = __ballot(before + upto > l.at);
+        const uint64_t past = __ballot(before + upto > (unsigned)l.at);
         if (past) {
             const int f = __builtin_ctzll(past);
             l.b = b0 + f;
@@ -301,16 +279,6 @@ __device__ __forceinline__ Line cut_line(const AttendArgs &a, int G, int rows_of
     }
     return l;
 }
-
-// Whether a line of blocks of `block` query rows is short enough to be counted in
-// 31 bits, where row starts do not descend: a sequence adds less than one block to
-// those of all rows.
-inline bool line_fits(int64_t tiles, int64_t rows, int block, int B, int Hk)
-{
-    return (tiles > 0 ? tiles : 1) * Hk * (rows / block + B) < ((int64_t)1 << 31) - 65536;
-}
-// Workgroups for a line of at most `units` units, of which the device holds `most` at once.
-inline int shares(int64_t units, int most) { return units < most && units > 0 ? (int)units : most; }
 
 // The launcher for many query rows a sequence (kda_cache_attend_rows.hip), and
 // floats of workspace it may need.

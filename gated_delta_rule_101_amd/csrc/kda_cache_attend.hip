@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
 {
     constexpr int SPLIT = BF ? 1 : 2, KS = D / 32, DT = D / 16, ROWS = 16;
     typedef typename Store<BF>::type T;
-    __shared__ int part[4];
+    __shared__ unsigned part[4];
     __shared__ __align__(16) float merge[4][16][D + 4];
     __shared__ float stat[4][2][ROWS];
     __shared__ float ref[4];
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
         const unsigned u = line.u;
         if (u >= (unsigned)tiles * blocks * a.Hk) {
             line.u = 0;
-            if (++line.b >= a.B) break;         // row starts that descend may count more units than there are
+            if (++line.b >= a.B) break;         // the line ends with the last sequence
             continue;
         }
         const int b = line.b;

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
     typedef typename Store<BF>::type T;
     extern __shared__ __align__(16) uint8_t lds[];
     Tile<D> *const tiles_lds = reinterpret_cast<Tile<D> *>(lds);
-    __shared__ int part[WAVES];
+    __shared__ unsigned part[WAVES];
     const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x & 63, m = lane & 31, half = lane >> 5;
     const int G = a.Hq / a.Hk;
     Line line;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
             const int blocks = blocks_of(s, G, ROWS);
             if ((unsigned)line.u >= (unsigned)tiles * blocks * a.Hk) {
                 line.u = 0;
-                if (++line.b >= a.B) break;         // row starts that descend may count more units than there are
+                if (++line.b >= a.B) break;         // the line ends with the last sequence
                 continue;
             }
             b = line.b;
