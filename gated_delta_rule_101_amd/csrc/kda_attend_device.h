@@ -12,9 +12,12 @@ __device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_lo
 
 __device__ __forceinline__ Sequence sequence(const AttendArgs &a, int b)
 {
-    const int64_t room = (int64_t)a.per * a.page;
-    return a.q_start ? sequence_of(a.q_start[b], a.q_start[b + 1], a.tokens, a.context[b], room)
-                     : sequence_of(b, b + 1, a.tokens, a.context[b], room);
+    int from = b, to = b + 1;                // without row starts, one row each
+    if (a.q_start) {
+        from = a.q_start[b];
+        to = a.q_start[b + 1];
+    }
+    return sequence_of(from, to, a.tokens, a.context[b], (int64_t)a.per * a.page);
 }
 
 // The page of a token, -1 where there is none: behind the last token, or an

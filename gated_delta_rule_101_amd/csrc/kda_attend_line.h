@@ -22,14 +22,14 @@ struct Sequence {
 __host__ __device__ inline Sequence sequence_of(int from, int to, int tokens, int context, int64_t room)
 {
     const auto clamp = [&](int x, int low) { return x < low ? low : x > tokens ? tokens : x; };
-    Sequence s;
-    s.first = clamp(from, 0);
-    s.queries = clamp(to, s.first) - s.first;
-    const int c = context > 0 ? context : 0;
-    s.context = c < room ? c : (int)room;
-    return s;
+    const int first = clamp(from, 0), c = context > 0 ? context : 0;
+    return Sequence{first, clamp(to, first) - first, c < room ? c : (int)room};
 }
-__host__ __device__ inline int tiles_of(const Sequence &s) { return s.context > 0 ? (s.context - 1) / 64 + 1 : 1; }
+__host__ __device__ inline int tiles_of(const Sequence &s)       // contexts are below 2^31 - 256
+{
+    const int n = (s.context + 63) / 64;
+    return n > 1 ? n : 1;
+}
 __host__ __device__ inline int blocks_of(const Sequence &s, int G, int rows)
 {
     return (int)(((unsigned)s.queries * G + rows - 1) / rows);   // below 2^31 rows, and rows a power of two
