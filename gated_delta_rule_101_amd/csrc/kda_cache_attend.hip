@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
             }
             const float up = ratio_level(lv, level), down = fast_exp2(-up);
             f16x8 w[SPLIT][2];
-            const float c = factor * (gone ? 0.f : ks);
+            const float c = factor * (gone ? 0.f : is_finite(ks) ? ks : __builtin_nanf(""));
             const int seen = gone ? 0 : min(limit, s.context) - tb;     // of this lane's 16 tokens
             float v[16], best = -__builtin_inff();
 #pragma unroll

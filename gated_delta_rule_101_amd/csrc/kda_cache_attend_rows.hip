@@ -114,7 +114,7 @@ template <int D, int WAVES, bool INT8> struct Loader {
         const bool has = there >> (threadIdx.x & 3) & 1;
         broken = (int)__ballot(has && !fine) & 15;
         lv = fine && has ? fast_log2(lv) : -__builtin_inff();
-        ks = has ? ks : 0.f;
+        ks = !has ? 0.f : is_finite(ks) ? ks : __builtin_nanf("");   // infinite: not a weight of 0 where the product is negative
     }
     __device__ __forceinline__ void put(Tile<D> &tile) const
     {
