@@ -49,11 +49,17 @@ __host__ __device__ inline int share_of(unsigned units, unsigned rows, unsigned 
 // The workgroup whose share has the last unit of a row of `tiles` that begins at place `at`.
 __host__ __device__ inline int last_share(unsigned at, unsigned tiles, unsigned share) { return (int)((at + tiles - 1) / share); }
 
+// A product of sizes, no more than the largest number.
+inline int64_t times(int64_t a, int64_t b)
+{
+    int64_t x;
+    return __builtin_mul_overflow(a, b, &x) ? INT64_MAX : x;
+}
 // Whether a line of blocks of `block` query rows is short enough, where row starts do
 // not descend: a sequence adds less than one block to those of all rows.
 inline bool line_fits(int64_t tiles, int64_t rows, int block, int B, int Hk)
 {
-    return (tiles > 0 ? tiles : 1) * Hk * (rows / block + B) < (int64_t)LINE_LIMIT - 65535;
+    return times(times(tiles > 0 ? tiles : 1, Hk), rows / block + B) < (int64_t)LINE_LIMIT - 65535;
 }
 // Workgroups for a line of at most `units` units, of which the device holds `most` at once.
 inline int shares(int64_t units, int most) { return units < most && units > 0 ? (int)units : most; }

@@ -233,12 +233,19 @@ static kda_status_t check_attention(int tokens, int B, int Hq, int Hk, int D, in
     return KDA_OK;
 }
 
+// The longest sequence's rows, as far as the host knows: one at least, and no more than there are.
+static int longest_rows(int max_queries, int tokens)
+{
+    return max_queries < 1 ? 1 : max_queries > tokens ? tokens : max_queries;
+}
+
 size_t kda_cache_attention_workspace_bytes(int tokens, int B, int Hq, int Hk, int D, int page, int max_pages,
                                            int max_queries)
 {
     if (check_attention(tokens, B, Hq, Hk, D, 0, page, max_pages, max_queries, KDA_CODE_E4M3, KDA_F32) != KDA_OK) return 0;
     if (tokens == 0 || B == 0) return 0;
-    return (size_t)kda::cache_attend_workspace_floats(tokens, B, Hq, Hk, D, page, max_pages, max_queries) * sizeof(float);
+    return (size_t)kda::cache_attend_workspace_floats(tokens, B, Hq, Hk, D, page, max_pages,
+                                                     longest_rows(max_queries, tokens)) * sizeof(float);
 }
 
 kda_status_t kda_cache_attention(const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
@@ -267,7 +274,7 @@ kda_status_t kda_cache_attention(const void *q, const void *k_codes, const void 
     a.out = out; a.lse = lse; a.ws = (float *)workspace;
     a.tokens = tokens; a.B = B; a.Hq = Hq; a.Hk = Hk; a.D = D; a.pages = pages; a.page = page;
     a.per = pages > 0 ? max_pages : 0;                    // without pages every context is empty
-    a.most = max_queries > 0 ? max_queries : 1; a.scale = scale;
+    a.most = longest_rows(max_queries, tokens); a.scale = scale;
     a.int8 = code == KDA_CODE_INT8; a.bf16 = dtype == KDA_BF16;
     return launched(kda::launch_cache_attend(a, (hipStream_t)stream));
 }

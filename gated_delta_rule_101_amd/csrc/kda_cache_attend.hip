@@ -319,7 +319,10 @@ __global__ void __launch_bounds__(256) kda_cache_attend_join_kernel(AttendArgs a
 // sequences 8 queries 32 / 44, 16 queries 39 / 57.  Not for float32 rows of 256
 // channels, which do not fit the other's registers.
 constexpr int64_t FEW = 16384;
-int64_t units_of(int B, int Hk, int64_t tiles, int64_t rows) { return (int64_t)B * Hk * (tiles > 0 ? tiles : 1) * ((rows + 15) / 16); }
+int64_t units_of(int B, int Hk, int64_t tiles, int64_t rows)
+{
+    return times((int64_t)B * Hk, times(tiles > 0 ? tiles : 1, (rows + 15) / 16));
+}
 bool is_few(int D, bool bf16, int64_t rows, int64_t units)
 {
     return rows <= 16 || (D == 256 && !bf16) || (rows <= 64 && units <= FEW);
