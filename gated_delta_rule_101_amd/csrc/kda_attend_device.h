@@ -17,7 +17,7 @@ __device__ __forceinline__ Sequence sequence(const AttendArgs &a, int b)
         from = a.q_start[b];
         to = a.q_start[b + 1];
     }
-    return sequence_of(from, to, a.tokens, a.context[b], (int64_t)a.per * a.page);
+    return sequence_of(from, to, a.tokens, a.context[b], a.room);
 }
 
 // The page of a token, -1 where there is none: behind the last token, or an

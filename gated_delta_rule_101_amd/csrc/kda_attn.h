@@ -48,6 +48,7 @@ struct AttendArgs {
     void *out;
     float *lse = nullptr, *ws;
     int tokens, B, Hq, Hk, D, pages, page, per, most;
+    int64_t room;                            // tokens that a context may have: 0 without pages
     float scale;
     bool int8, bf16;
 };

@@ -273,7 +273,8 @@ kda_status_t kda_cache_attention(const void *q, const void *k_codes, const void 
     a.k_scale = k_scale; a.v_scale = v_scale; a.table = block_table; a.context = context; a.q_start = q_start;
     a.out = out; a.lse = lse; a.ws = (float *)workspace;
     a.tokens = tokens; a.B = B; a.Hq = Hq; a.Hk = Hk; a.D = D; a.pages = pages; a.page = page;
-    a.per = pages > 0 ? max_pages : 0;                    // without pages every context is empty
+    a.per = max_pages;                                    // by which kernel and workspace are chosen
+    a.room = pages > 0 ? (int64_t)max_pages * page : 0;
     a.most = longest_rows(max_queries, tokens); a.scale = scale;
     a.int8 = code == KDA_CODE_INT8; a.bf16 = dtype == KDA_BF16;
     return launched(kda::launch_cache_attend(a, (hipStream_t)stream));
