@@ -133,21 +133,20 @@ __device__ __forceinline__ float load_row(const T *p, bool real, int half, bool 
     return __builtin_ldexpf(1.f, -e);
 }
 
-// Value scales go into the weights' exponents: log2 of the page's scale over the
-// wave's reference, the power of two above twice the largest scale met, which
-// moves (with the outputs, which are in its units) when a larger one comes.  Not
-// below 2^-40: what such a page adds is lost in rounding anyway, and its weights
-// still count in the sum.  Times 2^14, which leaves float16 normal weights down to
-// 2^-28.  Scales that are not finite pass as 0 here: the weights of their tokens
-// are made NaN behind the sum.
-// SLACK: how far scores may be above the base of their exponents.  Weights then
-// reach 2^14 / 2 * 2^SLACK, below float16's 65504; also while every scale met was
-// zero: an infinite weight would make NaN of the zero codes.
-constexpr float VALUE_REST = 0x1p-14f, SLACK = 2.f;
-__device__ __forceinline__ float ratio_level(float lv, float level)
-{
-    return fmaxf(level == -__builtin_inff() ? -1.f : lv - level, -40.f) + 14.f;
-}
+// Value scales go into the weights' exponents: a place of score z (in base 2) on a
+// page of value scale 2^lv has weight 2^(z + lv - top - lift + 13), with `top` the
+// base of the row's scores and `lift` that of its (z - top + lv), each up to SLACK
+// below its largest value so far.  So a row's largest weight x scale stands between
+// 2^13 and 2^15, below float16's 65504, whatever pages others see, and what is up to
+// 2^27 times smaller keeps all bits.  The sum of the weights alone, in units of 2^top,
+// takes the scale back, 2^-rel.
+constexpr float VALUE_REST = 0x1p-13f, SLACK = 2.f;
+// held: a base, 0 where there is none yet.  rel = lv - lift + 13: a scale 2^64 below
+// what the row holds, or zero, adds nothing (float16 ends at 2^-25), but its weights
+// still count in the sum.  Scales that are not finite pass as zero here: the weights of
+// their tokens are made NaN behind the sum.
+__device__ __forceinline__ float held(float base) { return base == -__builtin_inff() ? 0.f : base; }
+__device__ __forceinline__ float relative_level(float lv, float lift) { return fmaxf(lv - lift, -64.f) + 13.f; }
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // 16 bytes with those from place n on cleared.

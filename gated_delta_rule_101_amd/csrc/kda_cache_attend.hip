@@ -21,10 +21,14 @@
 //
 // Float16: queries are scaled by a power of two that puts their row's largest
 // channel at 2^14 .. 2^15 (bfloat16 fits exactly, what is lost of a channel is
-// under 2^-39 of the largest).  Weights carry the ratio of their page's value scale
-// to the largest met so far, in the exponent, so that no page's scale loses range,
-// and stand 2^14 times larger; they are rounded to 11 bits.  Float32 queries and
-// weights are taken in two float16 parts.
+// under 2^-39 of the largest).  Weights carry their page's value scale, in the
+// exponent, over the largest weight x scale that their row has met, so that they
+// are in float16's range whatever the pages' scales are, and stand 2^13 times larger.
+// They are rounded to 11 bits, three more than a bfloat16 output has: over many
+// places these roundings average out, and the error against float64 stays that of the
+// output's own rounding (1.67e-3 of its size, 1.66e-3 with float32 weights), where
+// a second part would double the second product.  The sum of the weights is of
+// float32 ones.  Float32 queries and weights are taken in two float16 parts.
 //
 // 256 sequences of 4096 to 8192 tokens, 32 query and 8 key heads x 128, e4m3: 0.565
 // ms, 5.7 TB/s; one sequence of 777: 7.7 us.
@@ -43,7 +47,6 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
     __shared__ unsigned part[4];
     __shared__ __align__(16) float merge[4][16][D + 4];
     __shared__ float stat[4][2][ROWS];
-    __shared__ float ref[4];
     const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x & 63, m = lane & 15, quarter = lane >> 4;
     const int G = a.Hq / a.Hk;
     Line line = cut_line<4>(a, G, ROWS, 4, part);    // a unit for each wave
@@ -86,7 +89,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
         const int furthest = min(s.context, s.context - s.queries + (r0 + active - 1) / G + 1);
 
         f32x4 o[DT];
-        float top = -__builtin_inff(), sum = 0.f, level = -__builtin_inff();
+        float top = -__builtin_inff(), sum = 0.f, lift = -__builtin_inff();
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
 
@@ -119,19 +122,10 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
             const int tb = t0 + 16 * quarter;                  // this lane's first token
             const bool broken = !gone && !is_finite(vs);
             const float lv = gone || broken ? -__builtin_inff() : fast_log2(vs);
-            if (__any(lv > level)) {         // rare after the first tiles
-                const float now = __builtin_ceilf(quarters_max(lv)) + 1.f, f = fast_exp2(level - now);
-                level = now;
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[d][i] *= f;
-            }
-            const float up = ratio_level(lv, level), down = fast_exp2(-up);
             f16x8 w[SPLIT][2];
             const float c = factor * (gone ? 0.f : is_finite(ks) ? ks : __builtin_nanf(""));
             const int seen = gone ? 0 : min(limit, s.context) - tb;     // of this lane's 16 tokens
-            float v[16], best = -__builtin_inff();
+            float v[16], own = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 f32x4 x = {0.f, 0.f, 0.f, 0.f};
@@ -148,25 +142,31 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
                 for (int i = 0; i < 16; ++i) v[i] = i < seen ? v[i] : -__builtin_inff();
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) best = fmaxf(best, v[i]);
-            best = quarters_max(best);
-            if (__any(best > top + SLACK)) {
-                const float now = fmaxf(top, best), fade = now == -__builtin_inff() ? 1.f : fast_exp2(top - now);
+            for (int i = 0; i < 16; ++i) own = fmaxf(own, v[i]);
+            const float best = quarters_max(own);
+            if (__any(best > top + SLACK)) {     // rare after the first tiles
+                const float now = fmaxf(top, best), back = now == -__builtin_inff() ? 0.f : top - now;
                 top = now;
-                sum *= fade;
+                sum *= fast_exp2(back);
+                lift += back;                    // the outputs' unit, 2^(top + lift), stays
+            }
+            const float base = held(top), most = quarters_max(own - base + lv);
+            if (__any(most > lift + SLACK)) {
+                const float now = fmaxf(lift, most), fade = now == -__builtin_inff() ? 1.f : fast_exp2(lift - now);
+                lift = now;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[d][i] *= fade;
             }
-            const float offset = up - (top == -__builtin_inff() ? 0.f : top);
+            const float rel = relative_level(lv, held(lift)), offset = rel - base;
             float total = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 v[i] = fast_exp2(v[i] + offset);
                 total += v[i];
             }
-            sum = __builtin_fmaf(total, down, sum);
+            sum = __builtin_fmaf(total, fast_exp2(-rel), sum);
             if (__any(broken)) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = broken && i < seen ? __builtin_nanf("") : v[i];
@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
             }
         }
 
-        // The four waves' parts meet: scaled to the common maximum and reference.
-        if (lane == 0) ref[wave] = level == -__builtin_inff() ? 0.f : fast_exp2(level) * VALUE_REST;
+        // The four waves' parts meet: scaled to the common maximum, in units of the values.
         sum = quarters_sum(sum);
         if (quarter == 0) {
             stat[wave][0][m] = top;
@@ -207,12 +206,11 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
         float best = -__builtin_inff();
 #pragma unroll
         for (int v = 0; v < 4; ++v) best = fmaxf(best, stat[v][0][m]);
-        // in units of the values: times the reference, which is 0 where every value was
-        const float f = (best == -__builtin_inff() ? 1.f : fast_exp2(top - best)) * ref[wave];
+        const float f = fast_exp2(lift == -__builtin_inff() ? lift : top - best + lift);      // 0 where every value was
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) merge[wave][m][16 * d + 4 * quarter + i] = o[d][i] * f;
+            for (int i = 0; i < 4; ++i) merge[wave][m][16 * d + 4 * quarter + i] = o[d][i] * VALUE_REST * f;
         __syncthreads();
         for (int e = threadIdx.x; e < 16 * (D / 4); e += 256) {
             const int rr = e / (D / 4), d = 4 * (e % (D / 4));

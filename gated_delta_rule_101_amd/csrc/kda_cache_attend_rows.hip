@@ -212,8 +212,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-        // The value scales' reference is a power of two, 2^level, above the largest met.
-        float top = -__builtin_inff(), sum = 0.f, level = -__builtin_inff(), spoiled = 0.f;
+        float top = -__builtin_inff(), sum = 0.f, lift = -__builtin_inff(), spoiled = 0.f;
 
         const int *table = a.table + (int64_t)b * a.per;
         Loader<D, WAVES, INT8> next;
@@ -229,12 +228,11 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
             const int t0 = t * 64;
             // this tile's scales, by group
             next.scales();
-            float ks[4], lv[4], most = -__builtin_inff();
+            float ks[4], lv[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 ks[g] = lane_value(next.ks, g);
                 lv[g] = lane_value(next.lv, g);
-                most = fmaxf(most, lv[g]);
             }
             const int there = next.there, broken = next.broken;
             if (t + 1 < t_stop) {
@@ -254,14 +252,6 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
                     for (int p = 0; p < SPLIT; ++p) x[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c, q[p][k], x[j], 0, 0, 0);
                 }
             }
-            if (most > level) {              // rare after the first tiles
-                const float now = __builtin_ceilf(most) + 1.f, f = fast_exp2(level - now);
-                level = now;
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[d][i] *= f;
-            }
             // scores to weights, in place
             float c[4];
 #pragma unroll
@@ -276,29 +266,39 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
                     c[g] = 1.f;
                 }
             }
-            float best = -__builtin_inff();
+            float best = -__builtin_inff(), most = -__builtin_inff();     // of the scores, and with the value scales
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 float y = x[g >> 1][8 * (g & 1)];
 #pragma unroll
                 for (int i = 1; i < 8; ++i) y = fmaxf(y, x[g >> 1][8 * (g & 1) + i]);
-                best = fmaxf(best, y * c[g]);
+                y *= c[g];
+                best = fmaxf(best, y);
+                most = fmaxf(most, y + lv[g]);
             }
             best = halves_max(best);
+            most = halves_max(most);
             // A base that is up to SLACK below the maximum serves as well: outputs then move rarely.
             if (__any(best > top + SLACK)) {
-                const float now = fmaxf(top, best), fade = now == -__builtin_inff() ? 1.f : fast_exp2(top - now);
+                const float now = fmaxf(top, best), back = now == -__builtin_inff() ? 0.f : top - now;
                 top = now;
-                sum *= fade;
+                sum *= fast_exp2(back);
+                lift += back;                    // the outputs' unit, 2^(top + lift), stays
+            }
+            const float base = held(top);
+            most -= base;
+            if (__any(most > lift + SLACK)) {
+                const float now = fmaxf(lift, most), fade = now == -__builtin_inff() ? 1.f : fast_exp2(lift - now);
+                lift = now;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[d][i] *= fade;
             }
-            const float base = top == -__builtin_inff() ? 0.f : top;
+            const float lift_of = held(lift);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const float up = ratio_level(lv[g], level), offset = up - base;
+                const float rel = relative_level(lv[g], lift_of), offset = rel - base;
                 float total = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
                     x[g >> 1][8 * (g & 1) + i] = v;
                     total += v;
                 }
-                sum = __builtin_fmaf(total, fast_exp2(-up), sum);
+                sum = __builtin_fmaf(total, fast_exp2(-rel), sum);
             }
             if (broken) {                        // a value scale that is not finite: NaN for the rows that see its tokens
 #pragma unroll
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
 
         sum = halves_sum(sum);
         const bool whole_row = t_begin == 0 && t_end == tiles;
-        const float f = (level == -__builtin_inff() ? 0.f : fast_exp2(level) * VALUE_REST) + halves_sum(spoiled);
+        const float f = fast_exp2(lift) + halves_sum(spoiled);           // 0 where every value was
         float *piece = nullptr;
         if constexpr (LINE) {
             piece = a.ws + (sizeof(Record) / 4) * gridDim.x + (int64_t)(2 * blockIdx.x + (t_begin == 0)) * PIECE<D, ROWS>;
@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int at = 32 * d + 8 * i + 4 * half;
-                    const float y[4] = {o[d][4 * i] * f, o[d][4 * i + 1] * f, o[d][4 * i + 2] * f, o[d][4 * i + 3] * f};
+                    const float y[4] = {o[d][4 * i] * VALUE_REST * f, o[d][4 * i + 1] * VALUE_REST * f,
+                                        o[d][4 * i + 2] * VALUE_REST * f, o[d][4 * i + 3] * VALUE_REST * f};
                     if (!LINE || whole_row) write_row<T>(a, s, h, G, r0 + r, at, D, y, top, sum);
                     else *reinterpret_cast<float4 *>(piece + (int64_t)r * D + at) = make_float4(y[0], y[1], y[2], y[3]);
                 }
