@@ -146,6 +146,15 @@ constexpr float VALUE_REST = 0x1p-13f, SLACK = 2.f;
 // still count in the sum.  Scales that are not finite pass as zero here: the weights of
 // their tokens are made NaN behind the sum.
 __device__ __forceinline__ float held(float base) { return base == -__builtin_inff() ? 0.f : base; }
+// Scores beyond FAR are first taken relative to their base, both as rounded (a fused
+// product would differ by its rounding): added to rel, the base would take bits from it, as
+// many as weights past float16 from 2^24 on.
+constexpr float FAR = 0x1p20f;
+__device__ __forceinline__ float from_base(float score, float base)
+{
+#pragma clang fp contract(off)
+    return score - base;
+}
 __device__ __forceinline__ float relative_level(float lv, float lift) { return fmaxf(lv - lift, -64.f) + 13.f; }
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 

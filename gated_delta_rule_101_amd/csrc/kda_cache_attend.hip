@@ -150,7 +150,15 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) kda_cache_attend_kernel
                 sum *= fast_exp2(back);
                 lift += back;                    // the outputs' unit, 2^(top + lift), stays
             }
-            const float base = held(top), most = quarters_max(own - base + lv);
+            float base = held(top);
+            if (__any(fabsf(base) > FAR)) {
+                const float far = fabsf(base) > FAR ? base : 0.f;        // other rows stay as they are
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = from_base(v[i], far);
+                own = from_base(own, far);
+                base -= far;
+            }
+            const float most = quarters_max(own - base + lv);
             if (__any(most > lift + SLACK)) {
                 const float now = fmaxf(lift, most), fade = now == -__builtin_inff() ? 1.f : fast_exp2(lift - now);
                 lift = now;

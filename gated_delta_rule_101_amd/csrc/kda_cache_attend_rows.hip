@@ -285,7 +285,24 @@ __global__ void __launch_bounds__(64 * WAVES, D == 256 || (D == 128 && !BF) ? 1 
                 sum *= fast_exp2(back);
                 lift += back;                    // the outputs' unit, 2^(top + lift), stays
             }
-            const float base = held(top);
+            float base = held(top);
+            if (__any(fabsf(base) > FAR)) {
+                const bool far = fabsf(base) > FAR;                      // other rows stay as they are
+                float from = -__builtin_inff();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float was = x[g >> 1][8 * (g & 1) + i], z = from_base(was * c[g], base);
+                        x[g >> 1][8 * (g & 1) + i] = far ? z : was;
+                        from = fmaxf(from, z + lv[g]);
+                    }
+                    c[g] = far ? 1.f : c[g];
+                }
+                from = halves_max(from);
+                most = far ? from : most;
+                base = far ? 0.f : base;
+            }
             most -= base;
             if (__any(most > lift + SLACK)) {
                 const float now = fmaxf(lift, most), fade = now == -__builtin_inff() ? 1.f : fast_exp2(lift - now);
