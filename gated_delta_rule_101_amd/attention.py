@@ -119,15 +119,15 @@ def _qk_shapes(q, k, q_weight, k_weight, positions, rotary):
         raise TypeError("q and k must have one dtype")
     _shape(q_weight, (D,), "q_weight", torch.float32)
     _shape(k_weight, (D,), "k_weight", torch.float32)
-    if (rotary is None) != (positions is None):
-        raise ValueError("rotary and positions go together")
     rows = R = 0
     if rotary is not None:
+        if positions is None:
+            raise ValueError("rotary needs positions")
         if rotary.dim() != 2:
             raise ValueError("rotary must be [rows,rotary_dim]")
         rows, R = rotary.shape
         _shape(rotary, (rows, R), "rotary", torch.float32)
-        _shape(positions, q.shape[:-2], "positions", torch.int32)
+    _shape(positions, q.shape[:-2], "positions", torch.int32)
     return T, Hq, Hk, D, rows, R, sq, sk
 
 
@@ -151,7 +151,8 @@ def kda_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[to
     [rows,R] float32: R/2 cosines, then R/2 sines.  Pairs are (i, i + R/2), or
     neighbours.  q, k and the outputs may have a token stride (parts of a fused
     projection); q_out and k_out may be q and k themselves.  Returns (q_out,
-    k_out): zeros where a position is negative, NaN where it is not in the table."""
+    k_out): zeros where a position is negative, with a table or without one, NaN
+    where it is not in the table."""
     lib = load_library()
     T, Hq, Hk, D, rows, R, sq, sk = _qk_shapes(q, k, q_weight, k_weight, positions, rotary)
     code = _dtype_code(q)

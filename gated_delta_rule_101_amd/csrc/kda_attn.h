@@ -18,7 +18,7 @@ struct PlanArgs {
 struct QkNormArgs {
     const void *q, *k;
     const float *wq = nullptr, *wk = nullptr;        // nullable: ones
-    const int *positions = nullptr;                  // with rotary
+    const int *positions = nullptr;                  // with rotary; without, their sign alone counts
     const float *rotary = nullptr;                   // [longest][R]: R / 2 cosines, then the sines
     const void *gq = nullptr, *gk = nullptr;         // backward: upstream gradients
     void *q_out, *k_out;                             // or the gradients of q and k

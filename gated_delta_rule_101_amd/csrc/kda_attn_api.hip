@@ -139,7 +139,7 @@ kda_status_t kda_qk_norm_rope_fwd(const void *q, const void *k, const float *q_w
     if (ok != KDA_OK) return ok;
     if (tokens == 0 || Hq + Hk == 0) return KDA_OK;
     kda::QkNormArgs a;
-    a.q = q; a.k = k; a.wq = q_weight; a.wk = k_weight; a.positions = rotary ? positions : nullptr; a.rotary = rotary;
+    a.q = q; a.k = k; a.wq = q_weight; a.wk = k_weight; a.positions = positions; a.rotary = rotary;
     a.q_out = q_out; a.k_out = k_out; a.T = tokens;
     a.q_stride = q_stride; a.k_stride = k_stride; a.qo_stride = q_out_stride; a.ko_stride = k_out_stride;
     a.Hq = Hq; a.Hk = Hk; a.D = D; a.R = rotary_dim; a.longest = rotary_rows; a.eps = eps;
@@ -183,7 +183,7 @@ kda_status_t kda_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const 
     if (!some && !want) return KDA_OK;
     kda::QkNormArgs a;
     a.gq = dq_out; a.gk = dk_out; a.q = q; a.k = k; a.wq = q_weight; a.wk = k_weight;
-    a.positions = rotary ? positions : nullptr; a.rotary = rotary; a.q_out = dq; a.k_out = dk;
+    a.positions = positions; a.rotary = rotary; a.q_out = dq; a.k_out = dk;
     a.dwq = dq_weight; a.dwk = dk_weight; a.ws = want && some ? (float *)workspace : nullptr;
     a.T = some ? tokens : 0;
     a.gq_stride = dq_out_stride; a.gk_stride = dk_out_stride; a.q_stride = q_stride; a.k_stride = k_stride;

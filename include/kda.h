@@ -701,9 +701,10 @@ kda_status_t kda_cache_plan(const int *cached, const int *added, int *block_tabl
  *   eps      >= 0, finite.  With eps = 0 a row of zeros is NaN
  *   rotary   [rotary_rows, rotary_dim] float32, rotary_dim / 2 cosines and then as
  *            many sines a row; NULL with rotary_dim = 0: no rotation
- *   positions [tokens] int32, the rows of `rotary` to use (NULL without rotary).  A
- *            negative one marks a row of no token: its input is not read, its
- *            output is zero.  One of rotary_rows or more makes its outputs NaN
+ *   positions [tokens] int32, the rows of `rotary` to use; NULL, if there is none:
+ *            every row is a token.  A negative one marks a row of no token: its input
+ *            is not read, its output is zero.  One of rotary_rows or more makes its
+ *            outputs NaN, with a table
  *   neighbours  0: the pairs are (i, i + rotary_dim / 2); otherwise (2 i, 2 i + 1)
  *
  * D even, up to 512, rotary_dim even, up to D.  A head's sum of squares has to
