@@ -186,7 +186,7 @@ def kda_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Te
     dq and dk (q's and k's shapes and type) and, unless want_dweights is False,
     dq_weight and dk_weight [D] float32, the sums over tokens and heads (with or
     without weights).  dq and dk may be passed, with a token stride, and may be
-    dq_out and dk_out themselves."""
+    dq_out and dk_out, or q and k, themselves."""
     lib = load_library()
     T, Hq, Hk, D, rows, R, sq, sk = _qk_shapes(q, k, q_weight, k_weight, positions, rotary)
     code = _dtype_code(q)

@@ -43,7 +43,8 @@ kda_status_t check_heads(int64_t T, int Hq, int Hk, int D)
 }
 
 // What both directions of the norm check: `in` and `out` are rows of queries
-// and keys in turn; in place where out[i] is in[same[i]].
+// and keys in turn.  An output may be any input of its kind, whole: each head is read
+// once, by the lanes that write it.
 kda_status_t check_qk(const Rows *in, int ni, const Rows *out, const float *wq, const float *wk, float eps,
                       const int *positions, const float *rotary, int64_t T, int Hq, int Hk, int D, int R, int longest,
                       kda_dtype_t dtype, const Rows *more, int nm)
@@ -171,7 +172,6 @@ kda_status_t kda_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const 
     if (workspace_bytes < need || (need && (!workspace || (uintptr_t)workspace & 15))) return KDA_ERR_INVALID_ARG;
     if (((uintptr_t)dq_weight | (uintptr_t)dk_weight) & 3) return KDA_ERR_INVALID_ARG;
     const size_t e = dsize(dtype), wq = (size_t)Hq * D * e, wk = (size_t)Hk * D * e;
-    // in place for the upstream gradients; the inputs are read again by the caller's next step
     const Rows in[] = {{dq_out, wq, (size_t)dq_out_stride * e, tokens}, {dk_out, wk, (size_t)dk_out_stride * e, tokens},
                        {q, wq, (size_t)q_stride * e, tokens}, {k, wk, (size_t)k_stride * e, tokens}};
     const Rows out[] = {{dq, wq, (size_t)dq_stride * e, tokens}, {dk, wk, (size_t)dk_stride * e, tokens}};

@@ -718,7 +718,8 @@ kda_status_t kda_qk_norm_rope_fwd(const void *q, const void *k, const float *q_w
 
 /*
  * kda_qk_norm_rope_bwd -- its gradients: dq [tokens, Hq, D] and dk [tokens, Hk, D]
- * (dtype; each may be its upstream gradient dq_out or dk_out), dq_weight and
+ * (dtype; each may be its upstream gradient dq_out or dk_out, or its input q or k,
+ * with the same stride), dq_weight and
  * dk_weight [D] float32, summed over tokens and heads, each or both NULL where
  * not wanted (a workspace is needed for them only).  q and k are the forward's
  * inputs.  Rows of a negative position have zero gradients and add nothing;
