@@ -283,8 +283,11 @@ int head_lanes(int D, int V)
 
 constexpr int64_t FILL = 4096;           // waves that fill the device
 // Workgroups: all resident (the backward's two a CU, a row of the workspace each:
-// 101 us at 16384 tokens of 32 + 8 heads x 128, 110 with 1024, 123 with 768).
-constexpr int64_t FWD_BLOCKS = 1024, BWD_BLOCKS = 512;
+// 101 us at 16384 tokens of 32 + 8 heads x 128, 110 with 1024, 123 with 768).  By
+// elements a wave has fewer bytes in flight, and four a CU serve better (the same of
+// 100 channels, bfloat16 / float32: 282 / 203 us, 483 / 292 with 512), but for long
+// float32 rows (250 channels 449 us, 489 with 1024).
+constexpr int64_t FWD_BLOCKS = 1024, BWD_BLOCKS = 512, BWD_NARROW = 1024;
 
 Shape shape_of(const QkNormArgs &a, bool bwd)
 {
@@ -305,7 +308,7 @@ Shape shape_of(const QkNormArgs &a, bool bwd)
     s.parts = (int)(want < 1 ? 1 : want > groups ? groups : want);
     const int64_t units = a.T * s.parts;
     s.blocks = (units + 3) / 4;
-    const int64_t most = bwd ? BWD_BLOCKS : FWD_BLOCKS;
+    const int64_t most = !bwd ? FWD_BLOCKS : s.vec > 1 || (!a.bf16 && a.D > 128) ? BWD_BLOCKS : BWD_NARROW;
     if (s.blocks > most) s.blocks = most;
     return s;
 }
@@ -341,7 +344,7 @@ int64_t qk_norm_bwd_workspace_floats(int64_t T, int Hq, int Hk, int D)
 {
     // as many rows as any shape of these sizes has workgroups: a wave at least a head group
     const int64_t units = T * (Hq + Hk), blocks = (units + 3) / 4;
-    return (blocks < BWD_BLOCKS ? blocks : BWD_BLOCKS) * 2 * D;
+    return (blocks < BWD_NARROW ? blocks : BWD_NARROW) * 2 * D;
 }
 
 hipError_t launch_qk_norm_bwd(const QkNormArgs &a, hipStream_t stream)

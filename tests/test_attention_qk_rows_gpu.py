@@ -42,3 +42,17 @@ def test_a_table_needs_positions(kda):  # noqa: F811
     q, k, _, _, _, table = qk_inputs(5, 2, 1, 64, 64, F32, False, 1)
     with pytest.raises(ValueError):
         kda.kda_qk_norm_rope_fwd(q, k, rotary=table)
+
+
+@pytest.mark.parametrize("T,D,R,dtype", [(2500, 90, 30, BF16), (2500, 90, 90, F32), (2500, 250, 250, F32)])
+def test_gradients_by_elements_over_many_workgroups(kda, T, D, R, dtype):  # noqa: F811
+    """Rows whose channels fit no wider access, in more workgroups than such rows had."""
+    q, k, wq, wk, pos, table = qk_inputs(T, 6, 2, D, R, dtype, False, D)
+    pos = pos % (3 * T)                                       # none beyond the table: the weights' sums stay finite
+    g = gen(T)
+    dq, dk = (torch.randn(t.shape, generator=g).to(dtype).cuda() for t in (q, k))
+    r = kda.kda_qk_norm_rope_bwd(dq, dk, q, k, wq, wk, 1e-6, positions=pos, rotary=table)
+    for n, x, w, dy in (("q", q, wq, dq), ("k", k, wk, dk)):
+        dx, tol, dw, wtol = ref.qk_bwd(*cpu(dy, x, w), 1e-6, *cpu(pos, table), False)
+        close(r["d" + n], dx, tol, "d" + n)
+        close(r[f"d{n}_weight"], dw, wtol, f"d{n}_weight")
