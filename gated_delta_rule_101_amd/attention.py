@@ -236,7 +236,8 @@ def kda_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_co
     the cache's places slots [...] int32, IN PLACE; slots outside the cache are
     skipped.  A page's scale for a head grows with its largest value, and the
     codes in front of the first place written with it; a page written from its
-    first place starts anew.  The tokens that go to one page follow each other."""
+    first place starts anew.  The tokens that go to one page stand next to each
+    other in the call, none that is skipped between them."""
     lib = load_library()
     pages, Hk, page, D, fmt = _cache_shapes(k_codes, v_codes, k_scale, v_scale)
     T, H, Dk, sk = _heads(k, "k")
@@ -277,7 +278,8 @@ def kda_cache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.T
     block_table[b] (int32 [B,max_pages]), it has context[b] tokens, and its
     queries, the last of them, are the rows from q_start[b] to q_start[b+1]
     (int32 [B+1]; None: one row each).  max_queries is the most rows of a
-    sequence (None: all of them, or one), by which the kernel is chosen; scale is
+    sequence, by which the kernel is chosen; None says one without q_start and
+    with it that one sequence may have them all, so pass it for speed.  scale is
     D**-0.5 unless given.  Returns out (q's shape and type), or (out, lse) with
     lse [tokens,Hq] float32 if want_lse or lse is given.  A row that sees no
     token has out 0 and lse -inf; rows of no sequence are not written."""

@@ -14,7 +14,8 @@
 // hold tokens innermost, pass through LDS so that both are read and written in
 // whole lines.  Each place takes the last of the call's tokens that name it.
 // Bound by latency: 256 tokens of 8 heads x 128, a page each, 9.7 us; prompts of
-// 19472 tokens 41 us, 2.9 TB/s.
+// 19472 tokens 42 us, 2.8 TB/s (float32 51 us, 3.9).  At 256 channels and pages of 128
+// the kernel of float32 rows and integers spills 84 bytes a lane.
 #include "kda_attn.h"
 #include "kda_block.h"
 #include "kda_code8.h"
@@ -377,8 +378,9 @@ template <typename T, int D, bool INT8> hipError_t launch(const AppendArgs &a, h
 {
     // Chunks of 4 to 62 tokens for 4096 workgroups or more: a decoding step's tokens
     // are a page each, and a wave takes one after the other; of a prompt's chunks
-    // those that begin no page have nothing to do (19472 tokens of 8 heads: 59 us
-    // with chunks of 16, 57 with 48).
+    // those that begin no page have nothing to do (19472 tokens of 8 heads, us with
+    // chunks of up to 8, 16, 48 and 62: pages of 64 47, 45, 38 and 42, of 16 91, 83,
+    // 75 and 74).
     const int64_t lanes = 2 * (int64_t)a.Hk, even = a.tokens * lanes / 4096;
     const int chunk = (int)(even < 4 ? 4 : even > 62 ? 62 : even);
     const int64_t blocks = ((int64_t)a.tokens + chunk - 1) / chunk;

@@ -655,7 +655,8 @@ kda_status_t kda_layer_norm_bwd(const void *dy, const void *x, const float *weig
  *    need only be aligned to their element.  int32 and scale buffers are
  *    aligned to 4 bytes.
  *  - dtype (KDA_F32 or KDA_BF16) is the type of the token rows.  Arithmetic and
- *    sums are float32; each output is rounded once, when stored.
+ *    sums are float32, but for the weights of the attention (stated there); each
+ *    output is rounded once, when stored.
  *  - Workspaces and overlaps as for the calls above.
  */
 
@@ -708,7 +709,7 @@ kda_status_t kda_cache_plan(const int *cached, const int *added, int *block_tabl
  *   neighbours  0: the pairs are (i, i + rotary_dim / 2); otherwise (2 i, 2 i + 1)
  *
  * D even, up to 512, rotary_dim even, up to D.  A head's sum of squares has to
- * stay below float32's 3.4e38.
+ * stay below float32's 3.4e38, and its mean with eps, unless 0, not below 1.2e-38.
  */
 kda_status_t kda_qk_norm_rope_fwd(const void *q, const void *k, const float *q_weight, const float *k_weight, float eps,
                                   const int *positions, const float *rotary, void *q_out, void *k_out,
@@ -751,9 +752,11 @@ kda_status_t kda_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const 
  * in float32.  Infinities and NaN leave the scale not finite: such a page and
  * head reads as NaN until it starts anew.
  *
- * The tokens of a call that go to one page follow each other in it, as those of
- * one sequence do; of two with the same slot the later one counts.  A page that
- * two sequences share is not written by either.
+ * The tokens of a call that go to one page stand next to each other in the call, in
+ * any order, as those of one sequence do: no token of another page and none that is
+ * skipped comes between them (each such part would be taken for all of them, at
+ * once).  Of two with the same slot the later one counts.  A page that two sequences
+ * share is not written by either.
  */
 kda_status_t kda_cache_append(const void *k, const void *v, const int *slots, void *k_codes, void *v_codes,
                               float *k_scale, float *v_scale, int tokens, int Hk, int D, int pages, int page,
@@ -773,7 +776,13 @@ kda_status_t kda_cache_append(const void *k, const void *v, const int *slots, vo
  *           and sees the places up to its own
  *   lse     [tokens, Hq] float32, or NULL
  *   max_queries  rows of the longest sequence, as far as the host knows: chooses
- *           the kernel, and the results are right for any value
+ *           the kernel, and the results are right for any value (taken as at least 1
+ *           and at most tokens)
+ *
+ * For their product with the values, the weights are rounded to float16 with 11 bits
+ * (float32 rows: two parts, 22 bits) relative to the row's largest weight x value
+ * scale, and lose bits only where that is 2^27 times smaller; their sum is of float32
+ * ones.  A value scale below 1.2e-38 counts as 0.
  *
  * A page and head whose scale is not finite makes the rows that see its tokens
  * NaN.  Pages whose table entry names none of the cache (such as -1, for a page
@@ -782,7 +791,9 @@ kda_status_t kda_cache_append(const void *k, const void *v, const int *slots, vo
  *
  * tokens * Hq below 2^31.  The units of work (64 places of the table x key head x
  * block of 16 or more query rows of a head's group) of a call whose sequences have
- * few rows have to stay below 2^31 too (KDA_ERR_UNSUPPORTED beyond).
+ * few rows have to stay below 2^31 too (KDA_ERR_UNSUPPORTED beyond).  Row starts that
+ * descend may count some rows many times: what such a call writes is inside its
+ * outputs, and nothing where they count 2^31 units or more.
  */
 size_t kda_cache_attention_workspace_bytes(int tokens, int B, int Hq, int Hk, int D, int page, int max_pages,
                                            int max_queries);
